@@ -2,7 +2,8 @@
 
 PyTorch is used only to own device memory and streams; every step of the layer runs
 in the library's CUDA kernels.  Each function below marshals its arguments and calls
-the C entry point of the same name (include/moe.h); a non-OK status raises MoeError.
+the C entry point of the same name (include/moe.h; the serving operators of
+include/moe_serving.h are bound in serving.py); a non-OK status raises MoeError.
 """
 from __future__ import annotations
 
@@ -15,33 +16,17 @@ import torch
 from . import _native
 from ._native import PATH_AUTO, PATH_DECODE, PATH_PREFILL, DEVERR_EXPERT_ID, DEVERR_TIMEOUT  # noqa
 from ._native import SF_ATOMS_NONE, SF_ATOMS_GATE_UP, SF_ATOMS_ROWS  # noqa
+from ._native import DEVERR_PAGE, DEVERR_POSITION, DEVERR_TOKEN, DEVERR_PROBS  # noqa
+from ._native import MoeError, check as _check, ptr as _ptr, stream as _stream
+from .serving import *  # noqa
+from . import serving as _serving
 
 __all__ = ["MoeError", "NvFp4Bank", "ExpertCSR", "workspace_bytes", "workspace_layout", "decode_tensor_core_min_pairs",
            "resolve_path", "prefill_min_pairs", "kernel_launches", "moe_route_topk", "moe_build_expert_csr",
            "moe_build_expert_csr_static",
            "moe_grouped_gate_up_silu_nvfp4", "moe_grouped_down_combine_nvfp4",
-           "get_device_error", "MoeLayer", "PATH_AUTO", "PATH_DECODE", "PATH_PREFILL"]
-
-
-class MoeError(RuntimeError):
-    def __init__(self, status: int, where: str):
-        self.status = status
-        super().__init__(f"{where}: {_native.STATUS.get(status, status)}")
-
-
-def _check(status: int, where: str) -> None:
-    if status != _native.MOE_OK:
-        raise MoeError(status, where)
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+           "get_device_error", "MoeLayer", "PATH_AUTO", "PATH_DECODE", "PATH_PREFILL",
+           *_serving.__all__]
 
 
 class NvFp4Bank:

@@ -4,18 +4,22 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_gb300.so")
 
 c_i32 = ctypes.c_int32
 c_vp = ctypes.c_void_p
 c_size = ctypes.c_size_t
+c_i64 = ctypes.c_int64
+c_f32 = ctypes.c_float
 
 MOE_OK = 0
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT"}
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
 DEVERR_EXPERT_ID, DEVERR_TIMEOUT = 1, 2
-
+DEVERR_PAGE, DEVERR_POSITION, DEVERR_TOKEN, DEVERR_PROBS = 4, 8, 16, 32
 
 SF_ATOMS_NONE, SF_ATOMS_GATE_UP, SF_ATOMS_ROWS = 0, 1, 2
 
@@ -36,7 +40,19 @@ class WsLayout(ctypes.Structure):
         "qh_codes", "qh_scales", "qh_exp", "partial", "tiles", "slice_tiles", "sync", "row_tok")]
 
 
-# (name, restype, argtypes) of every exported entry point declared in include/moe.h
+class KvCache(ctypes.Structure):
+    _fields_ = [("k_codes", c_vp), ("v_codes", c_vp), ("k_scales", c_vp), ("v_scales", c_vp),
+                ("num_pages", c_i32), ("kv_heads", c_i32), ("page_size", c_i32),
+                ("head_dim", c_i32), ("page_stride", c_i64)]
+
+
+class SeqBatch(ctypes.Structure):
+    _fields_ = [("q_offsets", c_vp), ("seq_lens", c_vp), ("page_table", c_vp), ("B", c_i32),
+                ("max_pages", c_i32), ("table_stride", c_i32)]
+
+
+# (name, restype, argtypes) of every exported entry point declared in include/moe.h and
+# include/moe_serving.h
 SIGNATURES = [
     ("moe_workspace_bytes", c_size, [c_i32] * 6),
     ("moe_workspace_layout", c_i32, [c_i32] * 6 + [ctypes.POINTER(WsLayout)]),
@@ -61,6 +77,21 @@ SIGNATURES = [
     ("moe_decode_layer_supported", c_i32, [c_i32] * 5),
     ("moe_status_string", ctypes.c_char_p, [c_i32]),
     ("moe_get_device_error", c_i32, [c_vp, c_vp, ctypes.POINTER(c_i32)]),
+    ("moe_kv_append_workspace_bytes", c_size, []),
+    ("moe_kv_append_rope_e4m3", c_i32,
+     [ctypes.POINTER(KvCache), ctypes.POINTER(SeqBatch), c_i32, c_vp, c_i64, c_vp, c_i64, c_vp,
+      c_i64, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_size, c_vp]),
+    ("moe_attention_workspace_bytes", c_size, [c_i32] * 3),
+    ("moe_attention_paged_e4m3", c_i32,
+     [c_vp, c_i64, c_i32, c_i32, c_i32, ctypes.POINTER(KvCache), ctypes.POINTER(SeqBatch), c_f32,
+      c_i32, c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
+    ("moe_linear_workspace_bytes", c_size, [c_i32] * 3),
+    ("moe_linear_nvfp4", c_i32,
+     [c_vp, c_i64, c_i32, c_i32, ctypes.POINTER(Bank), c_vp, c_i64, c_i32, c_vp, c_size, c_vp]),
+    ("moe_verify_workspace_bytes", c_size, [c_i32] * 2),
+    ("moe_verify_draft", c_i32,
+     [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp,
+      c_vp, c_size, c_vp]),
 ]
 
 _lib = None
@@ -85,3 +116,25 @@ def load():
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+class MoeError(RuntimeError):
+    def __init__(self, status: int, where: str):
+        self.status = status
+        super().__init__(f"{where}: {STATUS.get(status, status)}")
+
+
+def check(status: int, where: str) -> None:
+    if status != MOE_OK:
+        raise MoeError(status, where)
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def stream(s):
+    """The CUDA stream handle of a torch stream (None: the current one)."""
+    if s is None:
+        s = torch.cuda.current_stream()
+    return s.cuda_stream

@@ -1,0 +1,101 @@
+// Declarations shared by the serving operators' translation units (moe_serving.h).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "moe_internal.cuh"
+#include "moe_serving.h"
+
+namespace moe {
+
+struct KvAppendArgs {
+  moe_kv_cache c;
+  moe_seq_batch b;
+  int T, q_heads, max_pos, rotary, interleaved;
+  const uint16_t *k, *v, *q;
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  const float *cos, *sin;
+  const int32_t* positions;
+  uint32_t* err;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, cudaStream_t s);
+
+struct AttentionArgs {
+  moe_kv_cache c;
+  moe_seq_batch b;
+  int T, q_heads, window;
+  float scale;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_stride, out_stride;
+  float* lse;
+  char* ws;
+};
+size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_attention(const AttentionArgs& a, int dtype, cudaStream_t s);
+
+struct LinearArgs {
+  const uint16_t* x;
+  int64_t x_stride, y_stride;
+  int T, N, K;
+  const uint8_t *codes, *scales;
+  const float* alpha;
+  void* y;
+  char* ws;
+};
+size_t linear_ws_bytes(int T, int N, int K);
+cudaError_t launch_linear(const LinearArgs& a, int x_dtype, int y_dtype, cudaStream_t s);
+
+struct VerifyArgs {
+  const int32_t *draft_ids, *n_draft;
+  int B, n, V;
+  const void *target, *draft;
+  int64_t target_stride, draft_stride;
+  const float *u_accept, *u_sample;
+  int32_t *out_ids, *n_accepted;
+  char* ws;
+};
+size_t verify_ws_bytes(int B, int V);
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
+
+// 16-bit activations as f32 and back (nearest even).
+template <int DT>
+__device__ __forceinline__ float act_to_f32(uint32_t bits16) {
+  if (DT == MOE_DTYPE_BF16) return __uint_as_float(bits16 << 16);
+  return __half2float(__ushort_as_half((unsigned short)bits16));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t f32_to_act(float v) {
+  if (DT == MOE_DTYPE_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  return __half_as_ushort(__float2half_rn(v));
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = act_to_f32<DT>(w[i] & 0xffffu);
+    f[2 * i + 1] = act_to_f32<DT>(w[i] >> 16);
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f32_to_act<DT>(f[2 * i]) | (f32_to_act<DT>(f[2 * i + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two floats to two E4M3 codes (low byte = a), nearest even, finite values saturating at 448.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t v) {
+  const uint32_t h = e4m3x2_to_f16x2(v);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace moe

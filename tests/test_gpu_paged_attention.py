@@ -1,0 +1,209 @@
+"""moe_attention_paged_e4m3 against the float64 oracle, within the oracle's error bound plus the
+rounding of the output type."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_grouped_gemm_gb300 as moe
+from oracle import serving as oracle
+from serving_util import Batch, activations, cache_planes, device_cache, zeros_ws
+
+pytestmark = pytest.mark.gpu
+# half a unit in the last place of 8 and 11 significant bits, and half the least subnormal
+ROUND = {"bf16": (2.0 ** -8, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}
+
+
+def stale_nan(planes, batch):
+    """NaN codes in every slot that no sequence uses."""
+    used = np.zeros((batch.num_pages, batch.page), bool)
+    for b, n in enumerate(batch.lens):
+        for i in range(min(int(n), batch.table.shape[1] * batch.page)):
+            if 0 <= batch.table[b, i // batch.page] < batch.num_pages:
+                used[batch.table[b, i // batch.page], i % batch.page] = True
+    for c in (planes[0], planes[2]):
+        c.transpose(0, 2, 1, 3)[~used] = 0x7F
+
+
+def run(q, cache, batch, qh, D, scale, window=0, ws=None, out=None, stream=None):
+    T = q.shape[0]
+    out = torch.full((T, qh, D), float("nan"), dtype=q.dtype, device="cuda") if out is None else out
+    lse = torch.full((T, qh), float("nan"), device="cuda")
+    ws = zeros_ws(moe.attention_workspace_bytes(qh, cache.kv_heads, D)) if ws is None else ws
+    moe.moe_attention_paged_e4m3(q, cache, batch, out, ws, scale=scale, window=window, lse=lse,
+                                 stream=stream)
+    return out, lse, ws
+
+
+def check(rng, pairs, page, heads, group, D, dtype, window=0, amp=1.0, planes=None, scale=None,
+          edit=None, err=0):
+    batch = Batch(rng, pairs, page)
+    if edit:
+        edit(batch)
+    planes = planes(batch) if planes else cache_planes(rng, batch.num_pages, heads, page, D)
+    stale_nan(planes, batch)
+    q = activations(rng, (batch.T, heads * group, D), dtype, amp)
+    scale = D ** -0.5 if scale is None else scale
+    want, wl, eo, el = oracle.attention(q.double().numpy(), *planes, batch.offsets, batch.lens,
+                                        batch.table, scale, window)
+    out, lse, ws = run(q.cuda(), device_cache(planes), batch.device(), heads * group, D, scale, window)
+    assert moe.get_device_error(ws) == err
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    rel, floor = ROUND[dtype]
+    tol = eo + rel * (np.abs(want) + eo) + floor
+    assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+    seen = np.isfinite(wl)
+    assert np.array_equal(np.isfinite(gl), seen) and np.all(gl[~seen] == -np.inf)
+    assert np.all(np.abs(gl[seen] - wl[seen]) <= el[seen] + 1e-6)
+    assert np.all(got[~seen] == 0)
+    return out, lse
+
+
+@pytest.mark.parametrize("D,page,heads,group,dtype", [
+    (128, 64, 2, 4, "bf16"), (64, 16, 1, 1, "f16"), (128, 16, 1, 8, "f16"), (256, 32, 1, 5, "bf16"),
+    (64, 128, 2, 16, "bf16"), (128, 128, 1, 12, "bf16"), (256, 16, 2, 2, "f16"), (64, 64, 1, 33, "f16")])
+def test_single_tokens_over_ragged_lengths(D, page, heads, group, dtype):
+    rng = np.random.default_rng(D + page + group)
+    pairs = [(n - 1, 1) for n in (1, 2, page - 1, page, page + 1, 7 * page + 5, 300, 1025)] + [(40, 0), (0, 0)]
+    check(rng, pairs, page, heads, group, D, dtype)
+
+
+@pytest.mark.parametrize("D,page,heads,group,dtype,pairs", [
+    (128, 64, 2, 4, "bf16", [(100, 8), (0, 3), (511, 5), (64, 16)]),
+    (64, 16, 1, 5, "f16", [(0, 1), (0, 17), (33, 31), (700, 4)]),
+    (256, 32, 1, 2, "bf16", [(10, 40), (200, 9)]),
+    (128, 16, 1, 1, "bf16", [(5, 130)]),
+    (128, 64, 1, 4, "bf16", [(0, 129), (300, 64), (3, 1)]),
+    (64, 64, 2, 8, "f16", [(77, 100), (0, 200)]),
+    (128, 128, 1, 7, "f16", [(1000, 37), (0, 150)])])
+def test_several_new_tokens_are_causal(D, page, heads, group, dtype, pairs):
+    check(np.random.default_rng(group + D), pairs, page, heads, group, D, dtype)
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 100])
+def test_windows(window):
+    rng = np.random.default_rng(window)
+    check(rng, [(0, 1), (500, 1), (63, 30), (200, 70)], 64, 2, 4, 128, "bf16", window=window)
+    check(rng, [(0, 5), (130, 160)], 16, 1, 2, 64, "f16", window=window)
+
+
+def test_a_long_sequence_beside_short_ones():
+    rng = np.random.default_rng(21)
+    check(rng, [(20000, 1), (3, 1), (0, 1), (4095, 1)], 64, 1, 8, 128, "bf16")
+
+
+def test_rows_that_see_nothing():
+    """More new tokens than the sequence is long: the first rows have no place and see nothing."""
+    rng = np.random.default_rng(22)
+
+    def edit(b):
+        b.lens[0], b.lens[1] = 3, 0
+    check(rng, [(0, 9), (0, 4), (8, 2)], 16, 2, 3, 64, "bf16", edit=edit, err=moe.DEVERR_PAGE)
+
+
+def test_sharp_and_flat_scores():
+    rng = np.random.default_rng(23)
+    check(rng, [(900, 4)], 32, 1, 4, 128, "bf16", amp=40.0)
+    check(rng, [(900, 4)], 32, 1, 4, 128, "f16", amp=0.0)
+
+
+def test_large_and_small_activations():
+    rng = np.random.default_rng(24)
+    check(rng, [(90, 2)], 16, 1, 2, 64, "bf16", amp=1e20, scale=1e-21)
+    check(rng, [(90, 2)], 16, 1, 2, 64, "bf16", amp=1e-20, scale=1e18)
+
+
+def test_pages_whose_scales_lie_far_apart():
+    """Value scales from 2^-40 to 2^40 and zero pages with the smallest scale an append writes."""
+    rng = np.random.default_rng(25)
+
+    def planes(batch):
+        p = list(cache_planes(rng, batch.num_pages, 2, 16, 64))
+        p[3] = (2.0 ** rng.integers(-40, 41, p[3].shape)).astype(np.float32)
+        p[1] = (rng.uniform(0.5, 2, p[1].shape) * 0.003).astype(np.float32)
+        p[2][::3] = 0
+        p[3][::3] = np.float32(2.0 ** -64)
+        return tuple(p)
+    check(rng, [(700, 3), (80, 1)], 16, 2, 4, 64, "bf16", planes=planes)
+
+
+def test_bad_pages_are_left_out_and_reported():
+    rng = np.random.default_rng(26)
+
+    def edit(b):
+        b.table[0, 2], b.table[1, 0] = -1, b.num_pages
+    check(rng, [(100, 2), (10, 1), (40, 3)], 16, 2, 2, 128, "bf16", edit=edit, err=moe.DEVERR_PAGE)
+
+
+def test_a_sequence_longer_than_its_table():
+    rng = np.random.default_rng(27)
+
+    def edit(b):
+        b.lens[0] = b.table.shape[1] * b.page + 9
+        b.table[0] = np.arange(b.table.shape[1]) % b.num_pages
+    check(rng, [(60, 2), (4, 1)], 16, 1, 2, 64, "bf16", edit=edit, err=moe.DEVERR_PAGE)
+
+
+def test_pages_spaced_past_32_bits():
+    """Pages more than 2^31 bytes apart in one allocation."""
+    rng = np.random.default_rng(28)
+    heads, P, D = 1, 16, 64
+    batch = Batch(rng, [(40, 1)], P, spare=0)
+    planes = cache_planes(rng, batch.num_pages, heads, P, D)
+    stride = (1 << 31) + 4096
+    big = torch.zeros(2 * P * D + stride * (batch.num_pages - 1), dtype=torch.uint8, device="cuda")
+    shape, st = (batch.num_pages, heads, P, D), (stride, P * D, D, 1)
+    k, v = big.as_strided(shape, st), big.as_strided(shape, st, P * D)
+    k.copy_(torch.from_numpy(planes[0]).cuda())
+    v.copy_(torch.from_numpy(planes[2]).cuda())
+    cache = moe.PagedKvCache(k, v, torch.from_numpy(planes[1]).cuda(), torch.from_numpy(planes[3]).cuda())
+    q = activations(rng, (1, 4, D), "bf16").cuda()
+    a = run(q, cache, batch.device(), 4, D, 0.125)
+    b = run(q, device_cache(planes), batch.device(), 4, D, 0.125)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_strided_queries_outputs_and_no_lse():
+    rng = np.random.default_rng(29)
+    batch = Batch(rng, [(100, 3), (30, 2)], 64)
+    planes = cache_planes(rng, batch.num_pages, 2, 64, 128)
+    cache = device_cache(planes)
+    rows = activations(rng, (batch.T, 12 * 128), "bf16").cuda()
+    q = rows[:, :8 * 128].view(batch.T, 8, 128)
+    a, _, _ = run(q.contiguous(), cache, batch.device(), 8, 128, 0.1)
+    wide = torch.zeros(batch.T, 12, 128, dtype=torch.bfloat16, device="cuda")
+    ws = zeros_ws(moe.attention_workspace_bytes(8, 2, 128))
+    moe.moe_attention_paged_e4m3(q, cache, batch.device(), wide[:, 2:10], ws, scale=0.1)
+    assert torch.equal(wide[:, 2:10], a)
+    assert not wide[:, :2].any() and not wide[:, 10:].any()
+
+
+def test_repeated_calls_graph_replays_and_another_stream_agree():
+    """The same workspace serves call after call, in a graph whose lengths change between
+    replays, and the results are the same bits."""
+    rng = np.random.default_rng(30)
+    pairs = [(3000, 1), (64, 1), (0, 1), (777, 1)]
+    batch = Batch(rng, pairs, 32)
+    cache = device_cache(cache_planes(rng, batch.num_pages, 2, 32, 128))
+    dev = batch.device()
+    q = activations(rng, (4, 16, 128), "bf16").cuda()
+    a, la, ws = run(q, cache, dev, 16, 128, 0.09)
+    for _ in range(3):
+        b, lb, _ = run(q, cache, dev, 16, 128, 0.09, ws=ws)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c, lc, _ = run(q, cache, dev, 16, 128, 0.09, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(a, c) and torch.equal(la, lc)
+    out, lse = torch.empty_like(a), torch.empty_like(la)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_attention_paged_e4m3(q, cache, dev, out, ws, scale=0.09, lse=lse)
+    graph.replay()
+    assert torch.equal(a, out)
+    dev.seq_lens.copy_(torch.tensor([1500, 10, 1, 778], dtype=torch.int32))
+    graph.replay()
+    d, ld, _ = run(q, cache, dev, 16, 128, 0.09)
+    assert torch.equal(d, out) and torch.equal(ld, lse)
+    assert moe.get_device_error(ws) == 0
