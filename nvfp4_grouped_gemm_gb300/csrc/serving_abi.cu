@@ -124,7 +124,7 @@ moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, 
   if ((st = check_rows(out, out_stride, (int64_t)q_heads * cache->head_dim)) != MOE_OK) return st;
   if (!aligned(lse, 4)) return MOE_ERR_INVALID_ARG;
   if (T >= (1 << 24) || (int64_t)T * q_heads >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)batch->max_pages * cache->page_size >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, attention_ws_bytes(q_heads, cache->kv_heads, cache->head_dim))) !=
       MOE_OK)
     return st;
