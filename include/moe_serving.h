@@ -15,8 +15,9 @@
  * sizes are checked on the host before anything is launched; no call prints, aborts or
  * throws. Every call takes a workspace `ws` (256-byte aligned, zero-filled once after it is
  * allocated, of the bytes its size function returns) whose first word is the device error
- * word of moe_get_device_error. A workspace serves any number of calls of the sizes it was
- * made for in one stream; calls that can overlap need one each.
+ * word of moe_get_device_error. A workspace serves any number of calls in one stream, of the
+ * sizes it was made for and smaller ones (the attention's of its head_dim); calls that can
+ * overlap need one each. After MOE_DEVERR_TIMEOUT zero-fill it again.
  */
 #ifndef MOE_GB300_SERVING_H
 #define MOE_GB300_SERVING_H
@@ -127,7 +128,7 @@ moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, 
 size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t K);
 
 /* y[t][n] = alpha * sum_k x[t][k] * W[n][k] for T tokens, W a bank of one expert (E = 1) with
- * N rows of in_f = K weights (K a multiple of 32, at most 65536; N and T any). x: x_dtype (bf16
+ * N rows of in_f = K weights (K a multiple of 32, at most 65536; N any, T <= 65535). x: x_dtype (bf16
  * or f16) [T][K], rows x_stride elements apart (16-byte aligned as above); y: y_dtype (bf16, f16
  * or f32) [T][N], rows y_stride elements apart. Products are exact (x as f16 times a power of
  * two, exact for values within 2^-28 of the row's largest; E2M1 * UE4M3 in f16), sums are f32.

@@ -158,7 +158,7 @@ moe_status moe_linear_nvfp4(const void* x, int64_t x_stride, int32_t x_dtype, in
   if (!act_dtype(x_dtype) || (!act_dtype(y_dtype) && y_dtype != MOE_DTYPE_F32))
     return MOE_ERR_INVALID_ARG;
   if (w->in_f % 32 != 0 || w->in_f > 65536) return MOE_ERR_UNSUPPORTED;
-  if (T > 65536 || (int64_t)T * w->rows >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  if (T > 65535 || (int64_t)T * w->rows >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
   moe_status st = check_rows(x, x_stride, w->in_f);
   if (st != MOE_OK) return st;
   if (!y || !aligned(y, y_dtype == MOE_DTYPE_F32 ? 4 : 2) || y_stride < w->rows)

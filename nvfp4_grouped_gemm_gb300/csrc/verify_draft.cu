@@ -1,19 +1,40 @@
 // Verification of drafted tokens with given random numbers (moe_verify_draft).
 //
-// One block per sequence: it tests the drafted tokens in order, then sums the masses of the row
-// the next token is drawn from and walks the row again to the goal. Masses are whole numbers, so
-// no order of summation shows in the result.
+// Bound by one row of the target's probabilities (and one of the draft's after a refusal) per
+// sequence. The row is cut into chunks, a block each, so that few sequences still fill the GPU.
+// Every block finds the row for itself (lane i of its first warp tests drafted tokens i and
+// 32 + i; the first refusal is the lowest bit of two ballots), sums the masses of its chunk and
+// leaves the sum in the workspace. The last block of a sequence to arrive finds the chunk that
+// holds the goal and walks that chunk alone (and in the rare case that nothing is left after a
+// refusal's difference, sums the row itself first). Masses are whole numbers and their sums wrap
+// nowhere (V <= 2^22 masses of at most 2^40), so neither the order of summation nor that of
+// arrival shows in the result.
 #include "serving.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Tokens per chunk: the least power of two from 1024 that leaves at most 16 blocks per SM of a
+// 152-SM GPU (smaller chunks shorten the walk of the last block, more blocks cost launches).
+constexpr int kBlocks = 16 * 152;
+constexpr int kMaxChunk = 8192;
+int chunk_tokens(int B, int V) {
+  int chunk = 1024;
+  while (chunk < kMaxChunk && (long long)B * ((V + chunk - 1) / chunk) > kBlocks) chunk *= 2;
+  return chunk;
+}
+
+// Workspace: error word, arrival counters of up to 2^16 sequences (their place does not depend
+// on the sizes, so a workspace serves smaller calls too), chunk sums.
+constexpr size_t kSumsAt = kAlign + 65536 * 4;
 
 template <int DT>
 __device__ __forceinline__ float prob(const void* row, int64_t at) {
-  if (DT == MOE_DTYPE_F32) return static_cast<const float*>(row)[at];
-  return act_to_f32<DT>(static_cast<const uint16_t*>(row)[at]);
+  if (DT == MOE_DTYPE_F32) return __ldg(static_cast<const float*>(row) + at);
+  return act_to_f32<DT>(__ldg(static_cast<const uint16_t*>(row) + at));
 }
 
 // floor(min(w, 1) * 2^40); 0 for NaN and negative weights.
@@ -21,108 +42,233 @@ __device__ __forceinline__ unsigned long long mass_of(float w) {
   return __float2ull_rz(fminf(fmaxf(w, 0.0f), 1.0f) * 1099511627776.0f);
 }
 
-__device__ unsigned long long block_sum(unsigned long long v, unsigned long long* s_warp) {
+template <class T>
+__device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  unsigned long long sum = 0;
-  for (int i = 0; i < kThreads / 32; ++i) sum += s_warp[i];
-  return sum;
+  return v;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
-  __shared__ unsigned long long s_warp[kThreads / 32];
-  __shared__ int s_count, s_token;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+struct Row {
+  const void *target, *draft;      // the row drawn from and the draft's beside it, or null
+  int left_out;                    // a token without its unit of draft mass, or -1
+};
+template <int DT, int EACH>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, int chunks) {
+  constexpr int kChunk = EACH * kThreads;
+  constexpr int kBatch = EACH < 8 ? EACH : 8;    // loads in flight per thread (and row)
+  __shared__ unsigned long long s_warp[kWarps];
+  __shared__ int s_count, s_last, s_chunk, s_token, s_back;
+  __shared__ unsigned long long s_before, s_goal;
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* err = reinterpret_cast<uint32_t*>(a.ws);
+  uint32_t* arrived = reinterpret_cast<uint32_t*>(a.ws + kAlign);
+  unsigned long long* sums = reinterpret_cast<unsigned long long*>(a.ws + kSumsAt) + (size_t)b * chunks;
   const int n = a.n_draft ? min(max(a.n_draft[b], 0), a.n) : a.n;
   const int64_t size = DT == MOE_DTYPE_F32 ? 4 : 2;
   const char* target = static_cast<const char*>(a.target) + (int64_t)b * (a.n + 1) * a.target_stride * size;
   const char* draft = a.draft ? static_cast<const char*>(a.draft) + (int64_t)b * a.n * a.draft_stride * size : nullptr;
-  if (tid == 0) {
-    int count = 0;
-    for (; count < n; ++count) {
-      const int id = a.draft_ids[(int64_t)b * a.n + count];
-      if (id < 0 || id >= a.V) {
-        atomicOr(err, (uint32_t)MOE_DEVERR_TOKEN);
-        break;
+  const int32_t* ids = a.draft_ids + (int64_t)b * a.n;
+  if (warp == 0) {
+    uint32_t refused[2] = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (32 * h >= a.n) break;
+      const int i = 32 * h + lane;
+      bool no = false, odd = false;
+      if (i < a.n) {
+        const int id = ids[i];
+        const float u = a.u_accept[(int64_t)b * a.n + i];
+        odd = id < 0 || id >= a.V;
+        no = odd;
+        if (!odd) {
+          const float q = draft ? prob<DT>(draft, i * a.draft_stride + id) : 1.0f;
+          no = !(__fmul_rn(u, q) < prob<DT>(target, i * a.target_stride + id));
+        }
       }
-      const float p = prob<DT>(target, count * a.target_stride + id);
-      const float q = draft ? prob<DT>(draft, count * a.draft_stride + id) : 1.0f;
-      if (!(__fmul_rn(a.u_accept[(int64_t)b * a.n + count], q) < p)) break;
+      refused[h] = __ballot_sync(0xffffffffu, no && i < n);
+      const uint32_t odds = __ballot_sync(0xffffffffu, odd && i < n);
+      // an id out of range counts where it is the first refusal
+      if (lane == 0 && blockIdx.x == 0 && (h == 0 || refused[0] == 0) &&
+          (odds & refused[h] & (0u - refused[h])))
+        atomicOr(err, (uint32_t)MOE_DEVERR_TOKEN);
     }
-    s_count = count;
-    s_token = -1;
+    if (lane == 0)
+      s_count = refused[0] ? __ffs(refused[0]) - 1 : refused[1] ? 31 + __ffs(refused[1]) : n;
   }
   __syncthreads();
   const int count = s_count;
   const bool refused = count < n;
-  const int64_t row = count * a.target_stride, drow = count * a.draft_stride;
-  const int left_out = refused && !draft ? a.draft_ids[(int64_t)b * a.n + count] : -1;
-  auto mass = [&](int v, bool whole) {
-    float w = prob<DT>(target, row + v);
-    if (!whole && refused) {
-      if (draft) w = __fsub_rn(w, prob<DT>(draft, drow + v));
-      else if (v == left_out) w = __fsub_rn(w, 1.0f);
+  Row r;
+  r.target = target + count * a.target_stride * size;
+  r.draft = refused && draft ? draft + count * a.draft_stride * size : nullptr;
+  r.left_out = refused && !draft ? ids[count] : -1;
+
+  // The masses of tokens from, from + step, ... (EACH of them) below `to`.
+  auto masses = [&](int from, int step, int to, unsigned long long (&m)[EACH]) {
+#pragma unroll
+    for (int i0 = 0; i0 < EACH; i0 += kBatch) {
+      float w[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int v = from + (i0 + i) * step;
+        w[i] = v < to ? prob<DT>(r.target, v) : 0.0f;
+      }
+      if (r.draft) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int v = from + (i0 + i) * step;
+          w[i] = v < to ? __fsub_rn(w[i], prob<DT>(r.draft, v)) : 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (from + (i0 + i) * step == r.left_out) w[i] = __fsub_rn(w[i], 1.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) m[i0 + i] = mass_of(w[i]);
     }
-    return mass_of(w);
   };
-  bool whole = false;
-  unsigned long long total = 0;
-  for (int pass = 0; pass < 2 && total == 0; ++pass) {
-    whole = pass == 1;
-    unsigned long long sum = 0;
-    for (int v = tid; v < a.V; v += kThreads) sum += mass(v, whole);
-    total = block_sum(sum, s_warp);
+  auto block_total = [&](unsigned long long v) {       // of every thread; all threads call it
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) s_warp[warp] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += s_warp[w];
+    return v;
+  };
+  auto chunk_total = [&](int x) {
+    unsigned long long m[EACH], sum = 0;
+    masses(x * kChunk + tid, kThreads, a.V, m);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) sum += m[i];
+    return block_total(sum);
+  };
+
+  // ---- this block's chunk ----
+  {
+    const unsigned long long sum = chunk_total(blockIdx.x);
+    if (tid == 0) {
+      sums[blockIdx.x] = sum;
+      __threadfence();
+      s_last = atomicAdd(&arrived[b], 1u) == (uint32_t)chunks - 1;
+      if (s_last) arrived[b] = 0;                // ready for the next call
+      s_token = -1;
+      s_chunk = -1;
+    }
+    __syncthreads();
   }
-  const float u = fminf(fmaxf(a.u_sample[b], 0.0f), 1.0f);
-  unsigned long long m = __float2ull_rz(u * 16777216.0f);
-  if (m > 16777215ull) m = 16777215ull;
-  const unsigned long long goal = m * (total >> 24) + ((m * (total & 0xffffffull)) >> 24);
-  unsigned long long base = 0;
-  for (int v0 = 0; v0 < a.V && total > 0; v0 += kThreads) {
-    const int v = v0 + tid;
-    unsigned long long x = v < a.V ? mass(v, whole) : 0, sum = x;
+  if (!s_last) return;
+  __threadfence();
+
+  // ---- the last block: total, goal, chunk, token ----
+  auto find_chunk = [&]() {                      // first warp; whether there is any mass
+    unsigned long long total = 0;
+    for (int i = lane; i < chunks; i += 32) total += __ldcg(sums + i);
+    total = warp_sum(total);
+    const float u = fminf(fmaxf(a.u_sample[b], 0.0f), 1.0f);
+    unsigned long long m = __float2ull_rz(u * 16777216.0f);
+    if (m > 16777215ull) m = 16777215ull;
+    const unsigned long long goal = m * (total >> 24) + ((m * (total & 0xffffffull)) >> 24);
+    unsigned long long before = 0;
+    for (int i0 = 0; i0 < chunks && total > 0; i0 += 32) {
+      const unsigned long long x = i0 + lane < chunks ? __ldcg(sums + i0 + lane) : 0;
+      unsigned long long run = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long up = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + run > goal);
+      if (past) {
+        if (lane == __ffs(past) - 1) s_chunk = i0 + lane, s_before = before + run - x;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, run, 31);
+    }
+    if (lane == 0) s_goal = goal;
+    return total > 0;
+  };
+  if (warp == 0) {
+    const bool any = find_chunk();
+    if (lane == 0) s_back = !any;
+  }
+  __syncthreads();
+  if (s_back && refused) {                       // nothing left after the difference
+    r.draft = nullptr, r.left_out = -1;
+    for (int x = 0; x < chunks; ++x) {
+      const unsigned long long sum = chunk_total(x);
+      if (tid == 0) __stcg(sums + x, sum);
+    }
+    __threadfence();
+    __syncthreads();
+    if (warp == 0) {
+      const bool any = find_chunk();
+      if (lane == 0) s_back = !any;
+    }
+    __syncthreads();
+  }
+  if (s_chunk >= 0) {
+    // a thread takes EACH consecutive tokens
+    const int v0 = s_chunk * kChunk + tid * EACH;
+    unsigned long long m[EACH], mine = 0;
+    masses(v0, 1, a.V, m);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) mine += m[i];
+    unsigned long long run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
+      const unsigned long long up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
     }
     __syncthreads();
-    if (lane == 31) s_warp[warp] = sum;
+    if (lane == 31) s_warp[warp] = run;
     __syncthreads();
-    unsigned long long before = base, all = base;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += s_warp[i];
-      all += s_warp[i];
+    unsigned long long at = s_before + run - mine;
+    for (int w = 0; w < warp; ++w) at += s_warp[w];
+    if (at <= s_goal && at + mine > s_goal) {    // one thread
+      int token = v0;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        at += m[i];
+        if (at <= s_goal) token = v0 + i + 1;
+      }
+      s_token = token;
     }
-    sum += before;
-    if (sum > goal && sum - x <= goal) s_token = v;
-    base = all;
-    if (base > goal) break;
   }
   __syncthreads();
   if (tid == 0) {
-    if (total == 0) atomicOr(err, (uint32_t)MOE_DEVERR_PROBS);
     a.n_accepted[b] = count;
+    if (s_back) atomicOr(err, (uint32_t)MOE_DEVERR_PROBS);
   }
   for (int i = tid; i <= a.n; i += kThreads)
-    a.out_ids[(int64_t)b * (a.n + 1) + i] =
-        i < count ? a.draft_ids[(int64_t)b * a.n + i] : i == count ? s_token : -1;
+    a.out_ids[(int64_t)b * (a.n + 1) + i] = i < count ? ids[i] : i == count ? s_token : -1;
+}
+
+template <int DT>
+cudaError_t launch_chunk(const VerifyArgs& a, cudaStream_t s) {
+  const int chunk = chunk_tokens(a.B, a.V), chunks = (a.V + chunk - 1) / chunk;
+  const dim3 grid(chunks, a.B);
+  if (chunk == 1024) verify_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a, chunks);
+  else if (chunk == 2048) verify_kernel<DT, 8><<<grid, kThreads, 0, s>>>(a, chunks);
+  else if (chunk == 4096) verify_kernel<DT, 16><<<grid, kThreads, 0, s>>>(a, chunks);
+  else verify_kernel<DT, 32><<<grid, kThreads, 0, s>>>(a, chunks);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t verify_ws_bytes(int B, int V) { return kAlign; }
+size_t verify_ws_bytes(int B, int V) {
+  // enough for any smaller B and V: with chunks below the largest there are at most kBlocks
+  const size_t most = (size_t)B * ((V + kMaxChunk - 1) / kMaxChunk);
+  return align_up(kSumsAt + (most > kBlocks ? most : kBlocks) * 8);
+}
 
 cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_F32) verify_kernel<MOE_DTYPE_F32><<<a.B, kThreads, 0, s>>>(a);
-  else if (dtype == MOE_DTYPE_BF16) verify_kernel<MOE_DTYPE_BF16><<<a.B, kThreads, 0, s>>>(a);
-  else verify_kernel<MOE_DTYPE_F16><<<a.B, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (dtype == MOE_DTYPE_F32) return launch_chunk<MOE_DTYPE_F32>(a, s);
+  return dtype == MOE_DTYPE_BF16 ? launch_chunk<MOE_DTYPE_BF16>(a, s) : launch_chunk<MOE_DTYPE_F16>(a, s);
 }
 
 }  // namespace moe

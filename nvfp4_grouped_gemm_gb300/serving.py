@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _native
-from ._native import MoeError, check as _check, ptr as _ptr, stream as _stream
+from ._native import MoeError, check as _check
 
 __all__ = ["PagedKvCache", "SeqBatch", "NvFp4Linear", "kv_append_workspace_bytes",
            "attention_workspace_bytes", "linear_workspace_bytes", "verify_workspace_bytes",
@@ -21,6 +21,12 @@ __all__ = ["PagedKvCache", "SeqBatch", "NvFp4Linear", "kv_append_workspace_bytes
            "moe_verify_draft"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+# These checks stand in front of calls of a few microseconds, so each reads a tensor's
+# properties once and the device is compared by its index.
 
 
 def _dtype(t: torch.Tensor, what: str) -> int:
@@ -30,27 +36,49 @@ def _dtype(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _on(dev: torch.device, t: torch.Tensor, what: str) -> None:
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor on the call's device")
+def _device() -> int:
+    """Index of the current CUDA device, which a call's tensors must be on."""
+    return _current_device()
 
 
-def _need(dev: torch.device, t: torch.Tensor, dtype: torch.dtype, shape, what: str) -> None:
-    _on(dev, t, what)
-    if t.dtype != dtype:
+def _queue(dev: int, stream) -> int:
+    return _current_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _elsewhere(what: str):
+    return ValueError(f"{what} must be on the current CUDA device")
+
+
+def _workspace(dev: int, ws: torch.Tensor) -> int:
+    """Bytes of the workspace."""
+    if ws.get_device() != dev:
+        raise _elsewhere("ws")
+    return ws.numel() * ws.itemsize
+
+
+def _need(dev: int, t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
+    if t.get_device() != dev:
+        raise _elsewhere(what)
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {tuple(shape)}")
+    return t.data_ptr()
 
 
-def _rows(dev: torch.device, t: torch.Tensor, heads: int, dim: int, what: str) -> int:
+def _rows(dev: int, t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
     """Row stride of token rows [T, heads, dim] whose heads are contiguous."""
-    _on(dev, t, what)
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what} must be [tokens, {heads}, {dim}]")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    if t.get_device() != dev:
+        raise _elsewhere(what)
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}")
+    T, heads, dim = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != dim and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return s0 if T > 1 else heads * dim
 
 
 class PagedKvCache:
@@ -71,11 +99,11 @@ class PagedKvCache:
         n, h, p, d = k_codes.shape
         if v_codes.shape != k_codes.shape or (n > 1 and v_codes.stride(0) != k_codes.stride(0)):
             raise ValueError("k_codes and v_codes must have the same shape and page stride")
-        self.device = k_codes.device
-        _on(self.device, k_codes, "k_codes")
-        _on(self.device, v_codes, "v_codes")
-        _need(self.device, k_scales, torch.float32, (n, h), "k_scales")
-        _need(self.device, v_scales, torch.float32, (n, h), "v_scales")
+        dev = self.dev = k_codes.get_device()
+        if dev < 0 or v_codes.get_device() != dev:
+            raise ValueError("the cache's planes must be on one CUDA device")
+        _need(dev, k_scales, _F32, (n, h), "k_scales")
+        _need(dev, v_scales, _F32, (n, h), "v_scales")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = n, h, p, d
         stride = k_codes.stride(0) if n > 1 else h * p * d
@@ -107,10 +135,11 @@ class SeqBatch:
                 (page_table.shape[1] > 1 and page_table.stride(1) != 1):
             raise TypeError("page_table must be int32 [B, max_pages] with contiguous rows")
         B, cols = page_table.shape
-        self.device = page_table.device
-        _on(self.device, page_table, "page_table")
-        _need(self.device, seq_lens, torch.int32, (B,), "seq_lens")
-        _need(self.device, q_offsets, torch.int32, (B + 1,), "q_offsets")
+        dev = self.dev = page_table.get_device()
+        if dev < 0:
+            raise ValueError("the batch's arrays must be on a CUDA device")
+        _need(dev, seq_lens, _I32, (B,), "seq_lens")
+        _need(dev, q_offsets, _I32, (B + 1,), "q_offsets")
         self.q_offsets, self.seq_lens, self.page_table = q_offsets, seq_lens, page_table
         self.B, self.max_pages = B, cols
         stride = page_table.stride(0) if B > 1 else cols
@@ -144,33 +173,32 @@ def moe_kv_append_rope_e4m3(cache: PagedKvCache, batch: SeqBatch, k: torch.Tenso
     """Append k, v [T, kv_heads, head_dim] to the cache, keys rotated by cos/sin [max_pos,
     rotary_dim/2] (None: not rotated), and write the rotated q [T, q_heads, head_dim] to q_out
     (q itself when None)."""
-    T, h, d, dev = k.shape[0], cache.kv_heads, cache.head_dim, cache.device
-    ks, vs = _rows(dev, k, h, d, "k"), _rows(dev, v, h, d, "v")
-    _on(dev, ws, "ws")
-    _on(dev, batch.page_table, "batch")
-    if v.shape[0] != T or v.dtype != k.dtype:
-        raise ValueError("k and v must have the same tokens and type")
+    dev = _device()
+    if cache.dev != dev or batch.dev != dev:
+        raise _elsewhere("cache and batch")
+    T, h, d, dt = k.shape[0], cache.kv_heads, cache.head_dim, k.dtype
+    ks, vs = _rows(dev, k, dt, (T, h, d), "k"), _rows(dev, v, dt, (T, h, d), "v")
     qh = qs = qos = 0
+    qp = qop = None
     if q is not None:
         q_out = q if q_out is None else q_out
         qh = q.shape[1]
-        qs, qos = _rows(dev, q, qh, d, "q"), _rows(dev, q_out, qh, d, "q_out")
-        if q.shape[0] != T or q_out.shape[0] != T or q.dtype != k.dtype or q_out.dtype != k.dtype:
-            raise ValueError("q and q_out must have k's tokens and type")
+        qs, qos = _rows(dev, q, dt, (T, qh, d), "q"), _rows(dev, q_out, dt, (T, qh, d), "q_out")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     max_pos = rotary = 0
+    cp = sp = pp = None
     if cos is not None or sin is not None:
         if cos is None or sin is None:
             raise ValueError("pass both cos and sin, or neither")
-        max_pos, rotary = cos.shape[0], 2 * cos.shape[1]
-        _need(dev, cos, torch.float32, (max_pos, rotary // 2), "cos")
-        _need(dev, sin, torch.float32, (max_pos, rotary // 2), "sin")
+        max_pos, half = shape = cos.shape
+        rotary = 2 * half
+        cp, sp = _need(dev, cos, _F32, shape, "cos"), _need(dev, sin, _F32, shape, "sin")
     if positions is not None:
-        _need(dev, positions, torch.int32, (T,), "positions")
+        pp = _need(dev, positions, _I32, (T,), "positions")
     _check(_native.load().moe_kv_append_rope_e4m3(
-        cache._ref, batch._ref, T, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs,
-        _ptr(q_out) if q is not None else None, qos, qh, _dtype(k, "k"), _ptr(cos), _ptr(sin),
-        max_pos, rotary, 1 if interleaved else 0, _ptr(positions), ws.data_ptr(), ws.nbytes,
-        _stream(stream)), "moe_kv_append_rope_e4m3")
+        cache._ref, batch._ref, T, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qop, qos, qh,
+        _dtype(k, "k"), cp, sp, max_pos, rotary, 1 if interleaved else 0, pp, ws.data_ptr(),
+        _workspace(dev, ws), _queue(dev, stream)), "moe_kv_append_rope_e4m3")
 
 
 def moe_attention_paged_e4m3(q: torch.Tensor, cache: PagedKvCache, batch: SeqBatch,
@@ -179,36 +207,37 @@ def moe_attention_paged_e4m3(q: torch.Tensor, cache: PagedKvCache, batch: SeqBat
                              stream=None) -> None:
     """Causal attention of the new tokens q [T, q_heads, head_dim] over the cache into out (same
     shape and type); scale defaults to head_dim**-0.5; lse float32 [T, q_heads] if given."""
-    d, dev = cache.head_dim, cache.device
-    T, qh = q.shape[0], q.shape[1]
-    qs, os_ = _rows(dev, q, qh, d, "q"), _rows(dev, out, qh, d, "out")
-    _on(dev, ws, "ws")
-    _on(dev, batch.page_table, "batch")
-    if out.shape[0] != T or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and type")
-    if lse is not None:
-        _need(dev, lse, torch.float32, (T, qh), "lse")
+    dev = _device()
+    if cache.dev != dev or batch.dev != dev:
+        raise _elsewhere("cache and batch")
+    d, shape, dt = cache.head_dim, q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"q must be [tokens, heads, {d}]")
+    T, qh, _ = shape
+    qs, os_ = _rows(dev, q, dt, shape, "q"), _rows(dev, out, dt, shape, "out")
+    lp = None if lse is None else _need(dev, lse, _F32, (T, qh), "lse")
     _check(_native.load().moe_attention_paged_e4m3(
         q.data_ptr(), qs, T, qh, _dtype(q, "q"), cache._ref, batch._ref,
-        d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, _ptr(lse),
-        ws.data_ptr(), ws.nbytes, _stream(stream)), "moe_attention_paged_e4m3")
+        d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, lp, ws.data_ptr(),
+        _workspace(dev, ws), _queue(dev, stream)), "moe_attention_paged_e4m3")
 
 
 def moe_linear_nvfp4(x: torch.Tensor, bank, y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """y [T, N] = x [T, K] W^T with W an NvFp4Bank of one expert (N rows of K weights)."""
-    if x.dim() != 2 or y.dim() != 2 or x.shape[1] != bank.in_f or \
-            y.shape[0] != x.shape[0] or y.shape[1] != bank.rows:
+    dev = _device()
+    if x.get_device() != dev or y.get_device() != dev or bank.codes.get_device() != dev:
+        raise _elsewhere("x, y and the bank")
+    shape, N = x.shape, bank.rows
+    if len(shape) != 2 or shape[1] != bank.in_f or y.shape != (shape[0], N):
         raise ValueError("x must be [T, in_f] and y [T, rows] of the bank")
-    if x.stride(1) != 1 or (y.shape[1] > 1 and y.stride(1) != 1):
+    T, K = shape
+    (xs, x1), (ys, y1) = x.stride(), y.stride()
+    if x1 != 1 or (y1 != 1 and N > 1):
         raise ValueError("the rows of x and y must be contiguous")
-    T, dev = x.shape[0], bank.codes.device
-    _on(dev, x, "x")
-    _on(dev, y, "y")
-    _on(dev, ws, "ws")
     _check(_native.load().moe_linear_nvfp4(
-        x.data_ptr(), x.stride(0) if T > 1 else bank.in_f, _dtype(x, "x"), T,
-        ctypes.byref(bank._c), y.data_ptr(), y.stride(0) if T > 1 else bank.rows, _dtype(y, "y"),
-        ws.data_ptr(), ws.nbytes, _stream(stream)), "moe_linear_nvfp4")
+        x.data_ptr(), xs if T > 1 else K, _dtype(x, "x"), T, ctypes.byref(bank._c), y.data_ptr(),
+        ys if T > 1 else N, _dtype(y, "y"), ws.data_ptr(), _workspace(dev, ws),
+        _queue(dev, stream)), "moe_linear_nvfp4")
 
 
 def moe_verify_draft(draft_ids: torch.Tensor, target_probs: torch.Tensor, u_accept: torch.Tensor,
@@ -218,38 +247,36 @@ def moe_verify_draft(draft_ids: torch.Tensor, target_probs: torch.Tensor, u_acce
     """Accept or refuse draft_ids int32 [B, n] against target_probs [B, n+1, V] (and draft_probs
     [B, n, V]) with u_accept [B, n] and u_sample [B] in [0, 1); out_ids int32 [B, n+1] gets the
     accepted ids, the drawn one, then -1, and n_accepted int32 [B] their number."""
+    dev = _device()
     B, n = draft_ids.shape
-    V = target_probs.shape[2]
-    ts = _prob_rows(target_probs, B, n + 1, V, "target_probs")
-    ds = 0
+    V, dt = target_probs.shape[2], target_probs.dtype
+    ts = _prob_rows(dev, target_probs, dt, (B, n + 1, V), "target_probs")
+    ds, dp = 0, None
     if draft_probs is not None:
-        ds = _prob_rows(draft_probs, B, n, V, "draft_probs")
-        _on(target_probs.device, draft_probs, "draft_probs")
-        if draft_probs.dtype != target_probs.dtype:
-            raise TypeError("draft_probs must have target_probs' type")
-    i32, f32, dev = torch.int32, torch.float32, target_probs.device
-    _on(dev, target_probs, "target_probs")
-    _on(dev, ws, "ws")
-    _need(dev, draft_ids, i32, (B, n), "draft_ids")
-    _need(dev, u_accept, f32, (B, n), "u_accept")
-    _need(dev, u_sample, f32, (B,), "u_sample")
-    _need(dev, out_ids, i32, (B, n + 1), "out_ids")
-    _need(dev, n_accepted, i32, (B,), "n_accepted")
-    if n_draft is not None:
-        _need(dev, n_draft, i32, (B,), "n_draft")
+        ds = _prob_rows(dev, draft_probs, dt, (B, n, V), "draft_probs")
+        dp = draft_probs.data_ptr()
+    np_ = None if n_draft is None else _need(dev, n_draft, _I32, (B,), "n_draft")
     _check(_native.load().moe_verify_draft(
-        draft_ids.data_ptr(), _ptr(n_draft), B, n, V, target_probs.data_ptr(), ts,
-        _ptr(draft_probs), ds, _dtype(target_probs, "target_probs"), u_accept.data_ptr(),
-        u_sample.data_ptr(), out_ids.data_ptr(), n_accepted.data_ptr(), ws.data_ptr(), ws.nbytes,
-        _stream(stream)), "moe_verify_draft")
+        _need(dev, draft_ids, _I32, (B, n), "draft_ids"), np_, B, n, V, target_probs.data_ptr(), ts,
+        dp, ds, _dtype(target_probs, "target_probs"),
+        _need(dev, u_accept, _F32, (B, n), "u_accept"),
+        _need(dev, u_sample, _F32, (B,), "u_sample"),
+        _need(dev, out_ids, _I32, (B, n + 1), "out_ids"),
+        _need(dev, n_accepted, _I32, (B,), "n_accepted"), ws.data_ptr(), _workspace(dev, ws),
+        _queue(dev, stream)), "moe_verify_draft")
 
 
-def _prob_rows(t: torch.Tensor, B: int, rows: int, V: int, what: str) -> int:
+def _prob_rows(dev: int, t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
     """Stride between the rows of [B, rows, V], which must be the same across sequences."""
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != rows or t.shape[2] != V:
-        raise ValueError(f"{what} must be [{B}, {rows}, {V}]")
+    if t.get_device() != dev:
+        raise _elsewhere(what)
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}")
+    B, rows, V = shape
     sb, sr, sv = t.stride()
-    if V > 1 and sv != 1:
+    if sv != 1 and V > 1:
         raise ValueError(f"{what}: a row must be contiguous")
     stride = sr if rows > 1 else sb if B > 1 else V
     if B > 1 and rows > 0 and sb != rows * stride:
