@@ -8,15 +8,16 @@
 // their rows' (maximum, sum, weighted values) in the workspace and the last of them to arrive
 // joins them in the order of the pieces, so results do not depend on arrival.
 //
-// Inside a CTA four warps take the piece's steps in turn. Each streams its steps through a ring
+// Inside a CTA the warps take the piece's steps in turn. Each streams its steps through a ring
 // of its own (TMA boxes of E4M3 rows, swizzled so that the fragment reads below hit distinct
 // banks), widens the codes to f16 in registers (exact) and multiplies with mma.sync m16n8k16
-// (f32 accumulation):
-//   S = Q K^T   lane 4g+c holds, of key g of each 8-key block, 16 consecutive values at 16c of
-//               every 64; the four bytes of a word are its values of one k-step, and Q's
-//               fragments are laid out with the same permutation of k
-//   O = P V     P's accumulator layout is the A operand's; V's pairs of keys for one value
-//               come from two rows' bytes by byte permutes
+// (f32 accumulation), keys and values as the 16-row operand and the queries as its 8 columns, so
+// that a conversion serves every query and few queries waste little:
+//   S^T = K Q^T    lane 4g+c holds, of keys tau(g) and 8 + tau(g) of a half-step, 16 consecutive
+//                  values at 16c of every 64; the four bytes of a word are its values of one
+//                  k-step, and Q's fragments are laid out with the same permutation of k
+//   O^T = V^T P^T  P^T's fragments are S^T's accumulators through an 8x8 transpose; V's pairs
+//                  of keys for one value come from two rows' bytes by byte permutes
 // With f = scale * k_scale * log2 e and v = log2 v_scale of a key's page, the weight that meets
 // V's codes is w = 2^(s f + v - M) and the softmax sum adds w / v_scale, so the value scale
 // costs nothing per element. M follows the running maximum of s f + v lazily: it moves only when
@@ -31,12 +32,13 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxGrid = 512;              // partial slots of the workspace
 constexpr int kMaxRows = 32;
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
+// What a segment costs beside its steps (queries, first copies, the warps' rows meeting), in
+// steps: pieces of the line are equal with it counted.
+constexpr int kSegmentCost = 6;
 
 // Workspace: error word; arrival counters [kMaxGrid]; partial maxima and sums
 // [2 * kMaxGrid][2][kMaxRows]; partial rows f32 [2 * kMaxGrid][kMaxRows][D].
@@ -44,23 +46,26 @@ constexpr size_t kCountersAt = kAlign;
 constexpr size_t kStatsAt = kCountersAt + kMaxGrid * 4;
 constexpr size_t kRowsAt = kStatsAt + (size_t)2 * kMaxGrid * 2 * kMaxRows * 4;
 
-template <int D_, int MT_>
+template <int D_, int NT_, int WARPS_>
 struct Shape {
-  static constexpr int D = D_, MT = MT_;
+  static constexpr int D = D_, NT = NT_, kWarps = WARPS_, kThreads = 32 * WARPS_;
   static constexpr int kStep = D == 256 ? 16 : 32;       // tokens per step
   static constexpr int kHalves = kStep / 16;
   static constexpr int kSubs = D == 256 ? 2 : 1;         // swizzled sub-tiles of a row
   static constexpr int kRowB = D == 64 ? 64 : 128;       // bytes of a sub-tile row
   static constexpr int kPlaneB = kStep * D;              // a step's K (or V) bytes
   static constexpr int kStageB = 2 * kPlaneB;
-  static constexpr int kSlots = D == 64 ? 4 : MT == 2 ? 3 : 2;
-  static constexpr int kCtas = D == 256 ? 2 : MT == 2 ? 2 : 3;   // per SM
-  static constexpr int kRows = 16 * MT;
+  static constexpr int kSlots = D == 64 ? 4 : NT == 4 ? 3 : 2;
+  static constexpr int kCtas = WARPS_ > 4 ? 1 : NT == 4 || (NT == 2 && D == 256) ? 2 : 3;   // per SM
+  static constexpr int kRows = 8 * NT;
   static constexpr int kRingB = kWarps * kSlots * kStageB;
   static constexpr int kMergeB = kWarps * kRows * D * 4; // aliases the ring
-  static constexpr int kBigB = kRingB > kMergeB ? kRingB : kMergeB;
+  static constexpr int kJoinB = kMaxGrid * kRows * 4;    // aliases the ring
+  static constexpr int kBig0 = kRingB > kMergeB ? kRingB : kMergeB;
+  static constexpr int kBigB = kBig0 > kJoinB ? kBig0 : kJoinB;
   static constexpr int kQB = kRows * D * 2;
   static constexpr int kSmem = 1024 + kBigB + kQB;
+  static constexpr bool kQRegs = NT * D <= 128;          // query fragments stay in registers
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -68,16 +73,21 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+// The 8x8 transpose of f16 pairs across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int m) {
+  return m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w;
 }
 // The four E4M3 codes of a word as two f16x2.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -113,6 +123,7 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
 }
 
 // Sum of v over the block; the exclusive prefix of the calling thread in *before.
+template <int WARPS>
 __device__ long long block_scan(long long v, long long* s_sum, long long* before) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
@@ -126,7 +137,7 @@ __device__ long long block_scan(long long v, long long* s_sum, long long* before
   __syncthreads();
   long long base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) base += s_sum[w];
     all += s_sum[w];
   }
@@ -141,11 +152,175 @@ struct Keys {
   float f, v, inv;              // scale * k_scale * log2 e; log2 v_scale; 1 / v_scale
 };
 
-template <int DT, class S>
-__global__ void __launch_bounds__(kThreads, S::kCtas)
+// A lane's share of a block of rows: query fragments, accumulators, and what the running softmax
+// keeps for rows 2c and 2c+1 of each row tile.
+template <class S>
+struct Rows {
+  uint4 Q[S::kQRegs ? S::NT : 1][S::kQRegs ? S::D / 32 : 1];
+  float O[S::NT][S::D / 16][4];
+  float M[S::NT][2], L[S::NT][2], rowf[S::NT][2];
+  int place[S::NT][2];
+};
+// Where a lane reads a stage: half-step token of accumulator row g, of a fragment's columns 2c
+// and 2c+1, and byte offsets of its keys' and values' 16-byte pieces.
+struct Frag {
+  int tau, tok_a, tok_b, koff0, koff1, voffa, voffb;
+};
+// A step's page factors per half, and whether the half's page is there.
+template <int H>
+struct StepKeys {
+  float f[H], v[H], inv[H];
+  bool good[H];
+};
+
+// One step of STEP keys for all rows; `masked` where a key of it is hidden from a row or is not
+// there.
+template <class S, bool masked>
+__device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepKeys<S::kHalves>& k,
+                                          const char* st, const char* s_q, int lane, int j0, int len,
+                                          int window) {
+  constexpr int D = S::D, NT = S::NT, H = S::kHalves;
+  float sc[NT][H][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sc[nt][h][x] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    uint4 k0[H], k1[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const char* at_ = st + (j >> 1) * (S::kStep * 128) + h * 16 * S::kRowB + (j & 1 ? f.koff1 : f.koff0);
+      k0[h] = *reinterpret_cast<const uint4*>(at_);
+      k1[h] = *reinterpret_cast<const uint4*>(at_ + 8 * S::kRowB);
+    }
+#pragma unroll
+    for (int m2 = 0; m2 < 2; ++m2) {
+      uint4 qf[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        qf[nt] = S::kQRegs ? t.Q[S::kQRegs ? nt : 0][S::kQRegs ? 2 * j + m2 : 0]
+                           : *reinterpret_cast<const uint4*>(s_q + ((2 * j + m2) * NT + nt) * 512 + lane * 16);
+#pragma unroll
+      for (int m1 = 0; m1 < 2; ++m1)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint32_t a0, a1, a2, a3;
+          widen4(word_of(k0[h], 2 * m2 + m1), a0, a2);
+          widen4(word_of(k1[h], 2 * m2 + m1), a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma(sc[nt][h], a0, a1, a2, a3, m1 ? qf[nt].z : qf[nt].x, m1 ? qf[nt].w : qf[nt].y);
+        }
+    }
+  }
+
+  // weights
+  uint32_t pb[NT][H][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float top[2] = {-INFINITY, -INFINITY};
+    float raw[H][4];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        raw[h][x] = sc[nt][h][x];
+        const int y = x & 1;
+        if (masked) {
+          const int j = j0 + h * 16 + (x >> 1) * 8 + f.tau, pl = t.place[nt][y];
+          const bool see = k.good[h] && j <= pl && j < len && (window == 0 || j > pl - window);
+          raw[h][x] = see ? raw[h][x] : __int_as_float(0x7fffffff);
+          sc[nt][h][x] = see ? fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - t.M[nt][y]) : -INFINITY;
+        } else {
+          sc[nt][h][x] = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - t.M[nt][y]);
+        }
+        top[y] = fmaxf(top[y], sc[nt][h][x]);
+      }
+    if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > kLazy)) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        // the maximum itself, from the scores: M may be far below it
+        float to = t.M[nt][y];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int x = y; x < 4; x += 2) {
+            const float v = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h]);
+            if (!masked || sc[nt][h][x] > -INFINITY) to = fmaxf(to, v);
+          }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+        const float keep = exp2_approx(t.M[nt][y] - to);
+        t.M[nt][y] = to;
+        t.L[nt][y] *= keep;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) t.O[nt][n][y] *= keep, t.O[nt][n][2 + y] *= keep;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int x = y; x < 4; x += 2)
+            if (!masked || sc[nt][h][x] > -INFINITY)
+              sc[nt][h][x] = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - to);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sc[nt][h][x] = exp2_approx(sc[nt][h][x]);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) t.L[nt][y] = fmaf(k.inv[h], sc[nt][h][y] + sc[nt][h][2 + y], t.L[nt][y]);
+      pb[nt][h][0] = transpose8(pack_f16(sc[nt][h][0], sc[nt][h][1]));
+      pb[nt][h][1] = transpose8(pack_f16(sc[nt][h][2], sc[nt][h][3]));
+    }
+  }
+
+  // values
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int s = 0; s < S::kSubs; ++s) {
+      constexpr int kWords = D == 64 ? 2 : 4;
+      uint32_t x[4][kWords];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const char* at_ = st + s * (S::kStep * 128) + (h * 16 + (r >> 1) * 8) * S::kRowB + (r & 1 ? f.voffb : f.voffa);
+        if (D == 64) {
+          const uint2 w = *reinterpret_cast<const uint2*>(at_);
+          x[r][0] = w.x, x[r][1] = w.y;
+        } else {
+          const uint4 w = *reinterpret_cast<const uint4*>(at_);
+          x[r][0] = w.x, x[r][1] = w.y, x[r][kWords - 2] = w.z, x[r][kWords - 1] = w.w;
+        }
+        if (masked) {
+          const bool there = k.good[h] && j0 + h * 16 + (r >> 1) * 8 + (r & 1 ? f.tok_b : f.tok_a) < len;
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) x[r][i] = there ? x[r][i] : 0u;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < kWords; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t a0, a1, a2, a3;
+          widen4(__byte_perm(x[0][m], x[1][m], e ? 0x7362 : 0x5140), a0, a1);
+          widen4(__byte_perm(x[2][m], x[3][m], e ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma(t.O[nt][s * 8 + 2 * m + e], a0, a1, a2, a3, pb[nt][h][0], pb[nt][h][1]);
+        }
+      }
+    }
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas)
 attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
-  constexpr int D = S::D, MT = S::MT, NB = S::kStep / 8;
+  constexpr int D = S::D, NT = S::NT, H = S::kHalves, kWarps = S::kWarps, kThreads = S::kThreads;
+  constexpr int kPer = 32 / H;                 // steps per batch of keys
   extern __shared__ char smem_raw[];
   __shared__ uint64_t s_full[kWarps * S::kSlots];
   __shared__ long long s_sum[kWarps];
@@ -158,28 +333,27 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   char* s_q = big + S::kBigB;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
+  const bool bf16 = a.dtype == MOE_DTYPE_BF16;
   uint32_t* err = reinterpret_cast<uint32_t*>(a.ws);
   uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kCountersAt);
   float* stats = reinterpret_cast<float*>(a.ws + kStatsAt);
   float* part = reinterpret_cast<float*>(a.ws + kRowsAt);
   const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size;
 
-  if (tid < kWarps * S::kSlots) mbar_init(&s_full[tid], 1);
+  for (int i = tid; i < kWarps * S::kSlots; i += kThreads) mbar_init(&s_full[i], 1);
   if (tid == 0) s_abort = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
-  // This CTA's piece of the line of steps.
+  // This CTA's piece of the line.
+  auto line_of = [&](const Seq& q) { return (long long)(q.steps + kSegmentCost) * q.blocks * heads; };
   long long total = 0, mine = 0, at = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
     mine = 0;
-    if (b0 + tid < a.b.B) {
-      const Seq q = read_seq<S>(a, b0 + tid, group, blockIdx.x == 0 ? err : nullptr);
-      mine = (long long)q.steps * q.blocks * heads;
-    }
-    total += block_scan(mine, s_sum, &at);
+    if (b0 + tid < a.b.B) mine = line_of(read_seq<S>(a, b0 + tid, group, blockIdx.x == 0 ? err : nullptr));
+    total += block_scan<kWarps>(mine, s_sum, &at);
   }
   long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kWarps) per = kWarps;
+  if (per < kWarps + kSegmentCost) per = kWarps + kSegmentCost;
   const long long begin = per * blockIdx.x, end = min(begin + per, total);
   if (begin >= end) return;
   if (a.b.B <= kThreads) {
@@ -188,61 +362,66 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     long long base = 0;
     for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
       mine = 0;
-      if (b0 + tid < a.b.B) {
-        const Seq q = read_seq<S>(a, b0 + tid, group, nullptr);
-        mine = (long long)q.steps * q.blocks * heads;
-      }
-      const long long sum = block_scan(mine, s_sum, &at);
+      if (b0 + tid < a.b.B) mine = line_of(read_seq<S>(a, b0 + tid, group, nullptr));
+      const long long sum = block_scan<kWarps>(mine, s_sum, &at);
       if (mine > 0 && base + at <= begin && begin < base + at + mine) s_seq = b0 + tid, s_first = base + at;
       base += sum;
     }
   }
   __syncthreads();
   int b = s_seq;
-  long long first = s_first;                  // the line's place of sequence b's first step
+  long long first = s_first;                   // the line's place of sequence b's first step
   Seq q = read_seq<S>(a, b, group, nullptr);
 
   char* ring = big + warp * S::kSlots * S::kStageB;
   uint64_t* full = s_full + warp * S::kSlots;
-  int issued = 0, taken = 0;                  // stages of this warp's ring, over all segments
-  const int tok_n = D == 64 ? g : (g >> 1) + 4 * (g & 1);   // key of an 8-key block in column g
-  const int tok_a = D == 64 ? 2 * c : c, tok_b = D == 64 ? 2 * c + 1 : c + 4;  // columns 2c, 2c+1
-  const int swz_k = D == 64 ? (tok_n >> 1) & 3 : tok_n;
+  int islot = 0, tslot = 0;                    // next slot to fill, to take
+  uint32_t tphase = 0;
+  int in_flight = 0;
+  // half-step token of accumulator row g, and of a fragment's columns 2c and 2c+1
+  const int tau = D == 64 ? g : (g >> 1) + 4 * (g & 1);
+  const int tok_a = D == 64 ? 2 * c : c, tok_b = D == 64 ? 2 * c + 1 : c + 4;
+  const int kx = D == 64 ? (tau >> 1) & 3 : tau;
+  const int koff0 = tau * S::kRowB + ((c ^ kx) * 16);
+  const int koff1 = tau * S::kRowB + (((4 + c) ^ kx) * 16);
   const int vch = D == 64 ? g >> 1 : (g >> 1) + 4 * (g & 1);
-  const uint32_t q_addr = smem_u32(s_q) + lane * 16;
+  const int vxa = D == 64 ? (tok_a >> 1) & 3 : tok_a, vxb = D == 64 ? (tok_b >> 1) & 3 : tok_b;
+  const int voffa = S::kPlaneB + tok_a * S::kRowB + ((vch ^ vxa) * 16) + (D == 64 ? (g & 1) * 8 : 0);
+  const int voffb = S::kPlaneB + tok_b * S::kRowB + ((vch ^ vxb) * 16) + (D == 64 ? (g & 1) * 8 : 0);
+
+  const Frag frag = {tau, tok_a, tok_b, koff0, koff1, voffa, voffb};
 
   for (long long pos = begin; pos < end;) {
-    while (pos >= first + (long long)q.steps * q.blocks * heads) {
-      first += (long long)q.steps * q.blocks * heads;
+    while (pos >= first + line_of(q)) {
+      first += line_of(q);
       q = read_seq<S>(a, ++b, group, nullptr);
     }
+    const int length = q.steps + kSegmentCost;
     const long long in_seq = pos - first;
-    const int seg = (int)(in_seq / q.steps), st0 = (int)(in_seq % q.steps);
-    const long long seg_at = first + (long long)seg * q.steps;
-    const int st1 = (int)min((long long)q.steps, end - seg_at);
+    const int seg = (int)(in_seq / length);
+    const long long seg_at = first + (long long)seg * length;
+    const int st0 = max(0, (int)(pos - seg_at) - kSegmentCost);
+    const int st1 = (int)min((long long)length, end - seg_at) - kSegmentCost;
+    pos = seg_at + st1 + kSegmentCost;
+    if (st1 <= st0) continue;                  // only the segment's fixed cost fell to this CTA
     const int head = seg / q.blocks, block = seg % q.blocks;
     const int R = min(S::kRows, q.n * group - block * S::kRows);
     // rows' places: row r of the block belongs to token (block * kRows + r) / group
     const int tok_first = block * S::kRows / group, tok_last = (block * S::kRows + R - 1) / group;
-    const int place_lo = q.start + tok_first;
+    const int place_lo = q.start + tok_first, place_hi = q.start + tok_last;
     // steps this block of rows can see at all
-    int w0 = q.step0 + st0, w1 = q.step0 + st1;
-    {
-      const int hi = min(q.len, q.start + tok_last + 1);
-      const int lo = a.window > 0 ? max(0, place_lo - a.window + 1) : 0;
-      w1 = min(w1, (max(hi, 0) + S::kStep - 1) / S::kStep);
-      w0 = max(w0, lo / S::kStep);
-    }
+    const int hi = min(q.len, place_hi + 1), lo = a.window > 0 ? max(0, place_lo - a.window + 1) : 0;
+    const int w0 = max(q.step0 + st0, lo / S::kStep);
+    const int w1 = min(q.step0 + st1, (max(hi, 0) + S::kStep - 1) / S::kStep);
 
     // ---- this warp's stream ----
     const int count = w1 > w0 + warp ? (w1 - w0 - warp + kWarps - 1) / kWarps : 0;
     Keys cur = {-1, 0.f, 0.f, 0.f}, nxt = cur;
     auto load_keys = [&](int batch) {
       Keys k = {-1, 0.f, 0.f, 0.f};
-      constexpr int kPer = 32 / S::kHalves;               // steps per batch
-      const int i = batch * kPer + lane / S::kHalves;
+      const int i = batch * kPer + lane / H;
       if (i < count) {
-        const int j = (w0 + warp + i * kWarps) * S::kStep + (lane % S::kHalves) * 16;
+        const int j = (w0 + warp + i * kWarps) * S::kStep + (lane % H) * 16;
         if (j < q.len) {
           const int page = __ldg(a.b.page_table + (int64_t)b * a.b.table_stride + j / P);
           if (page >= 0 && page < a.c.num_pages) {
@@ -259,47 +438,53 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       }
       return k;
     };
-    constexpr int kPer = 32 / S::kHalves;
-    int have = 0;                                          // key batches loaded
-    auto issue = [&](int i) {                              // all lanes
-      const int batch = i / kPer;
+    int have = 0;                              // key batches loaded
+    auto issue = [&](int i) {                  // all lanes: step i of this warp into the next slot
+      const int batch = i / kPer, src = (i % kPer) * H;
       if (batch >= have) {
         cur = nxt;
         nxt = load_keys(batch);
         if (have == 0) cur = nxt;
         ++have;
       }
-      const int slot = issued % S::kSlots;
-      const int src = (i % kPer) * S::kHalves;
-      int page[S::kHalves];
+      int page[H];
 #pragma unroll
-      for (int h = 0; h < S::kHalves; ++h) page[h] = __shfl_sync(0xffffffffu, nxt.page, src + h);
+      for (int h = 0; h < H; ++h) page[h] = __shfl_sync(0xffffffffu, nxt.page, src + h);
       if (lane == 0) {
-        char* st = ring + slot * S::kStageB;
+        char* st = ring + islot * S::kStageB;
+        uint64_t* bar = &full[islot];
         const int j = (w0 + warp + i * kWarps) * S::kStep;
-        const bool whole = P >= S::kStep;                  // one box per step and sub-tile
-        uint32_t bytes = 0;
+        const int row = head * P + j % P;
+        if (P >= S::kStep) {                   // one box per plane and sub-tile
+          if (page[0] >= 0) {
+            mbar_expect_tx(bar, S::kStageB);
 #pragma unroll
-        for (int h = 0; h < S::kHalves; ++h)
-          if (page[h] >= 0 && (!whole || h == 0)) bytes += whole ? S::kStageB : S::kStageB / S::kHalves;
-        mbar_expect_tx(&full[slot], bytes);
+            for (int s = 0; s < S::kSubs; ++s) {
+              tma_load_3d(st + s * (S::kStep * 128), &kmap, s * 128, row, page[0], bar);
+              tma_load_3d(st + S::kPlaneB + s * (S::kStep * 128), &vmap, s * 128, row, page[0], bar);
+            }
+          } else {
+            mbar_arrive(bar);
+          }
+        } else {                               // two pages of 16 tokens
+          uint32_t bytes = 0;
 #pragma unroll
-        for (int h = 0; h < S::kHalves; ++h) {
-          if (page[h] < 0 || (whole && h > 0)) continue;
-          const int row = head * P + (j + h * 16) % P;
+          for (int h = 0; h < H; ++h) bytes += page[h] >= 0 ? S::kStageB / H : 0;
+          mbar_expect_tx(bar, bytes);
 #pragma unroll
-          for (int s = 0; s < S::kSubs; ++s) {
-            char* dst = st + s * (S::kStep * 128) + h * 16 * S::kRowB;
-            tma_load_3d(dst, &kmap, s * 128, row, page[h], &full[slot]);
-            tma_load_3d(dst + S::kPlaneB, &vmap, s * 128, row, page[h], &full[slot]);
+          for (int h = 0; h < H; ++h) {
+            if (page[h] < 0) continue;
+            tma_load_3d(st + h * 16 * S::kRowB, &kmap, 0, head * P, page[h], bar);
+            tma_load_3d(st + S::kPlaneB + h * 16 * S::kRowB, &vmap, 0, head * P, page[h], bar);
           }
         }
       }
-      ++issued;
+      islot = islot + 1 == S::kSlots ? 0 : islot + 1;
+      ++in_flight;
     };
     for (int i = 0; i < min(count, S::kSlots); ++i) issue(i);
 
-    // ---- queries as A fragments: k-step ks, row tile mt: lane 16 B (a0, a2, a1, a3) ----
+    // ---- queries as B fragments: k-steps 2i and 2i+1 of row tile nt: lane 16 B ----
     for (int r = warp; r < S::kRows; r += kWarps) {
       constexpr int kQuads = (D / 4 + 31) / 32;
       float v[kQuads][4];
@@ -312,15 +497,17 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         const int u = lane + 32 * i;
         uint2 w = make_uint2(0, 0);
         if (r < R && u < D / 4) w = *reinterpret_cast<const uint2*>(src + 4 * u);
-        v[i][0] = act_to_f32<DT>(w.x & 0xffffu), v[i][1] = act_to_f32<DT>(w.x >> 16);
-        v[i][2] = act_to_f32<DT>(w.y & 0xffffu), v[i][3] = act_to_f32<DT>(w.y >> 16);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) amax = fmaxf(amax, fabsf(v[i][x]));
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t bits = (x < 2 ? w.x : w.y) >> (16 * (x & 1)) & 0xffffu;
+          v[i][x] = bf16 ? act_to_f32<MOE_DTYPE_BF16>(bits) : act_to_f32<MOE_DTYPE_F16>(bits);
+          amax = fmaxf(amax, fabsf(v[i][x]));
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       // bf16 rows get the power of two that puts their largest magnitude below 2^15
-      const int e = DT == MOE_DTYPE_BF16 && amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
+      const int e = bf16 && amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
       const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
       if (lane == 0) s_rowf[r] = pow2f(e);
 #pragma unroll
@@ -328,7 +515,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         const int u = lane + 32 * i;
         if (u < D / 4) {
           const int ks = (u >> 4) * 4 + (u & 3), cc = (u >> 2) & 3;
-          char* dst = s_q + (ks * MT + (r >> 4)) * 512 + ((r & 7) * 4 + cc) * 16 + ((r >> 3) & 1) * 8;
+          char* dst = s_q + ((ks >> 1) * NT + (r >> 3)) * 512 + ((r & 7) * 4 + cc) * 16 + (ks & 1) * 8;
           *reinterpret_cast<uint2*>(dst) =
               make_uint2(pack_f16(v[i][0] * s1 * s2, v[i][1] * s1 * s2),
                          pack_f16(v[i][2] * s1 * s2, v[i][3] * s1 * s2));
@@ -337,249 +524,128 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     }
     __syncthreads();
 
-    float O[MT][D / 8][4];
-    float M[MT][2], L[MT][2], rowf[MT][2];
-    int place[MT][2];
+    Rows<S> t;
+    if (S::kQRegs) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+      for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
+        for (int nt = 0; nt < NT; ++nt)
+          t.Q[S::kQRegs ? nt : 0][S::kQRegs ? i : 0] =
+              *reinterpret_cast<const uint4*>(s_q + (i * NT + nt) * 512 + lane * 16);
+    }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) O[mt][n][x] = 0.0f;
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = 16 * mt + 8 * x + g;
-        M[mt][x] = kNoMax, L[mt][x] = 0.0f;
-        rowf[mt][x] = s_rowf[r];
-        place[mt][x] = q.start + (block * S::kRows + r) / group;
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) t.O[nt][n][x] = 0.0f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = 8 * nt + 2 * c + y;
+        t.M[nt][y] = kNoMax, t.L[nt][y] = 0.0f;
+        t.rowf[nt][y] = s_rowf[r];
+        t.place[nt][y] = q.start + (block * S::kRows + r) / group;
       }
     }
 
     bool ok = true;
-    for (int i = 0; i < count && ok; ++i) {
-      const int slot = taken % S::kSlots;
-      ok = mbar_wait_warp(&full[slot], (taken / S::kSlots) & 1, &s_abort, err);
+    for (int i = 0; i < count; ++i) {
+      // every lane looks at the barrier itself; the bounded wait is for copies not there yet
+      if (!__all_sync(0xffffffffu, mbar_try(&full[tslot], tphase)))
+        ok = mbar_wait_warp(&full[tslot], tphase, &s_abort, err);
       if (!ok) break;
-      const uint32_t kb = smem_u32(ring + slot * S::kStageB), vb = kb + S::kPlaneB;
       const int j0 = (w0 + warp + i * kWarps) * S::kStep;
-
-      float sc[MT][NB][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[mt][nb][x] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        uint4 kc[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          kc[nb] = lds128(kb + (j >> 1) * (S::kStep * 128) + (nb * 8 + tok_n) * S::kRowB +
-                          (((4 * (j & 1) + c) ^ swz_k) * 16));
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          uint4 A[MT];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) A[mt] = lds128(q_addr + ((4 * j + m) * MT + mt) * 512);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const uint32_t w = m == 0 ? kc[nb].x : m == 1 ? kc[nb].y : m == 2 ? kc[nb].z : kc[nb].w;
-            uint32_t b0, b1;
-            widen4(w, b0, b1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma_f16_16816(sc[mt][nb], A[mt].x, A[mt].z, A[mt].y, A[mt].w, b0, b1);
-          }
-        }
-      }
-
-      // weights
-      const int src = (i % kPer) * S::kHalves;
+      const int src = (i % kPer) * H;
       const bool newer = i / kPer == have - 1;             // which key batch this step is in
-      float kf[S::kHalves], kv[S::kHalves], ki[S::kHalves];
-      bool good[S::kHalves];
+      StepKeys<H> k;
       bool masked = j0 + S::kStep > place_lo + 1 || j0 + S::kStep > q.len;
-      if (a.window > 0) masked |= j0 <= q.start + tok_last - a.window;
+      if (a.window > 0) masked |= j0 <= place_hi - a.window;
 #pragma unroll
-      for (int h = 0; h < S::kHalves; ++h) {
-        kf[h] = __shfl_sync(0xffffffffu, newer ? nxt.f : cur.f, src + h);
-        kv[h] = __shfl_sync(0xffffffffu, newer ? nxt.v : cur.v, src + h);
-        ki[h] = __shfl_sync(0xffffffffu, newer ? nxt.inv : cur.inv, src + h);
-        good[h] = __shfl_sync(0xffffffffu, newer ? nxt.page : cur.page, src + h) >= 0;
-        masked |= !good[h];
+      for (int h = 0; h < H; ++h) {
+        k.f[h] = __shfl_sync(0xffffffffu, newer ? nxt.f : cur.f, src + h);
+        k.v[h] = __shfl_sync(0xffffffffu, newer ? nxt.v : cur.v, src + h);
+        k.inv[h] = __shfl_sync(0xffffffffu, newer ? nxt.inv : cur.inv, src + h);
+        k.good[h] = k.inv[h] > 0.0f;
+        masked |= !k.good[h];
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int h = nb / 2;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[mt][nb][x] = fmaf(sc[mt][nb][x], kf[h] * rowf[mt][x >> 1], kv[h]);
-          if (masked) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int j = j0 + nb * 8 + (x & 1 ? tok_b : tok_a);
-              const int pl = place[mt][x >> 1];
-              const bool see = good[h] && j <= pl && j < q.len && (a.window == 0 || j > pl - a.window);
-              if (!see) sc[mt][nb][x] = -INFINITY;
-            }
-          }
-        }
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top[x >> 1] = fmaxf(top[x >> 1], sc[mt][nb][x]);
-        const bool move = top[0] > M[mt][0] + kLazy || top[1] > M[mt][1] + kLazy;
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-            const float to = fmaxf(M[mt][x], top[x]);
-            const float keep = exp2_approx(M[mt][x] - to);
-            M[mt][x] = to;
-            L[mt][x] *= keep;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) O[mt][n][2 * x] *= keep, O[mt][n][2 * x + 1] *= keep;
-          }
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[mt][nb][x] = exp2_approx(sc[mt][nb][x] - M[mt][x >> 1]);
-#pragma unroll
-        for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            L[mt][x] = fmaf(ki[h], (sc[mt][2 * h][2 * x] + sc[mt][2 * h][2 * x + 1]) +
-                                       (sc[mt][2 * h + 1][2 * x] + sc[mt][2 * h + 1][2 * x + 1]), L[mt][x]);
-      }
-
-      // values
-#pragma unroll
-      for (int h = 0; h < S::kHalves; ++h) {
-        uint32_t pa[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          pa[mt][0] = pack_f16(sc[mt][2 * h][0], sc[mt][2 * h][1]);
-          pa[mt][1] = pack_f16(sc[mt][2 * h][2], sc[mt][2 * h][3]);
-          pa[mt][2] = pack_f16(sc[mt][2 * h + 1][0], sc[mt][2 * h + 1][1]);
-          pa[mt][3] = pack_f16(sc[mt][2 * h + 1][2], sc[mt][2 * h + 1][3]);
-        }
-        const int rows[4] = {h * 16 + tok_a, h * 16 + tok_b, h * 16 + 8 + tok_a, h * 16 + 8 + tok_b};
-#pragma unroll
-        for (int s = 0; s < S::kSubs; ++s) {
-          constexpr int kWords = D == 64 ? 2 : 4;
-          uint32_t x[4][kWords];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int swz = D == 64 ? (rows[r] >> 1) & 3 : rows[r] & 7;
-            const uint32_t at_ = vb + s * (S::kStep * 128) + rows[r] * S::kRowB + ((vch ^ swz) * 16);
-            if (D == 64) {
-              const uint2 t = lds64(at_ + (g & 1) * 8);
-              x[r][0] = t.x, x[r][1] = t.y;
-            } else {
-              const uint4 t = lds128(at_);
-              x[r][0] = t.x, x[r][1] = t.y, x[r][kWords - 2] = t.z, x[r][kWords - 1] = t.w;
-            }
-            if (masked && !(good[h] && j0 + rows[r] < q.len)) {
-#pragma unroll
-              for (int i2 = 0; i2 < kWords; ++i2) x[r][i2] = 0;
-            }
-          }
-#pragma unroll
-          for (int m = 0; m < kWords; ++m) {
-            uint32_t b0[4], b1[4];
-            widen4(__byte_perm(x[0][m], x[1][m], 0x5140), b0[0], b0[1]);
-            widen4(__byte_perm(x[0][m], x[1][m], 0x7362), b0[2], b0[3]);
-            widen4(__byte_perm(x[2][m], x[3][m], 0x5140), b1[0], b1[1]);
-            widen4(__byte_perm(x[2][m], x[3][m], 0x7362), b1[2], b1[3]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma_f16_16816(O[mt][s * 16 + 4 * m + t], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3],
-                              b0[t], b1[t]);
-          }
-        }
-      }
-      ++taken;
+      const char* st = ring + tslot * S::kStageB;
+      if (masked) take_step<S, true>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+      else take_step<S, false>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+      if (++tslot == S::kSlots) tslot = 0, tphase ^= 1;
+      --in_flight;
       __syncwarp();
       if (i + S::kSlots < count) issue(i + S::kSlots);
     }
     if (!ok) {
       // gave up: let this warp's copies in flight land (bounded) before the CTA leaves
-      for (; taken < issued; ++taken) {
+      for (; in_flight > 0; --in_flight) {
         const uint64_t t0 = global_ns();
-        while (!mbar_try(&full[taken % S::kSlots], (taken / S::kSlots) & 1) &&
-               global_ns() - t0 < 100000000ull) {
+        while (!mbar_try(&full[tslot], tphase) && global_ns() - t0 < 100000000ull) {
         }
+        if (++tslot == S::kSlots) tslot = 0, tphase ^= 1;
       }
     }
 
-    // ---- the four warps' rows meet ----
+    // ---- the warps' rows meet ----
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        L[mt][x] += __shfl_xor_sync(0xffffffffu, L[mt][x], 1);
-        L[mt][x] += __shfl_xor_sync(0xffffffffu, L[mt][x], 2);
-        if (c == 0) {
-          s_m[warp][16 * mt + 8 * x + g] = M[mt][x];
-          s_l[warp][16 * mt + 8 * x + g] = L[mt][x];
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) t.L[nt][y] += __shfl_xor_sync(0xffffffffu, t.L[nt][y], o);
+        if (g == 0) {
+          s_m[warp][8 * nt + 2 * c + y] = t.M[nt][y];
+          s_l[warp][8 * nt + 2 * c + y] = t.L[nt][y];
         }
       }
     __syncthreads();                           // also: every warp is done with the ring
     if (s_abort) return;                       // the same for the whole block
     float* merge = reinterpret_cast<float*>(big);
+    // 16-byte units of a row are permuted so that a quarter warp's stores differ in bank
+    auto unit_of = [](int r, int d) {
+      const int u = d / 4, cc = (r & 7) >> 1;
+      return D == 64 ? u ^ ((cc & 1) | (cc >> 1) << 2) : u ^ (cc | ((u >> 4) & 1) << 2);
+    };
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = 16 * mt + 8 * x + g;
+      for (int y = 0; y < 2; ++y) {
+        const int r = 8 * nt + 2 * c + y;
         float top = kNoMax;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
-        const float keep = exp2_approx(M[mt][x] - top);
-        // columns 2c and 2c+1 of the 8-value blocks: runs of 16 (D = 64: 8) values
+        const float keep = exp2_approx(t.M[nt][y] - top);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int col = 2 * c + y;
-#pragma unroll
-          for (int n = 0; n < D / 8; n += 4) {
-            const int at_ = D == 64 ? col * 8 + n : (n / 16) * 128 + ((col >> 1) + 4 * (col & 1)) * 16 + n % 16;
-            // 16-byte units of a row rotated so that a quarter warp's stores differ in bank
-            const int unit = (at_ / 4) ^ ((c >> 1) ^ ((g & 1) << 1));
-            *reinterpret_cast<float4*>(merge + ((size_t)warp * S::kRows + r) * D + unit * 4) =
-                make_float4(O[mt][n][2 * x + y] * keep, O[mt][n + 1][2 * x + y] * keep,
-                            O[mt][n + 2][2 * x + y] * keep, O[mt][n + 3][2 * x + y] * keep);
-          }
+        for (int n = 0; n < D / 16; n += 2) {  // values 2n .. 2n+3 of a run of 16 (D = 64: 8)
+          const int d = D == 64 ? g * 8 + 2 * n : (n / 8) * 128 + vch * 16 + 2 * (n % 8);
+          *reinterpret_cast<float4*>(merge + ((size_t)warp * S::kRows + r) * D + unit_of(r, d) * 4) =
+              make_float4(t.O[nt][n][y] * keep, t.O[nt][n][2 + y] * keep, t.O[nt][n + 1][y] * keep,
+                          t.O[nt][n + 1][2 + y] * keep);
         }
       }
     __syncthreads();
     const bool opens = st0 == 0, closes = st1 == q.steps;
-    const bool whole_seg = opens && closes;
     const int slot = 2 * blockIdx.x + (opens ? 1 : 0);
     auto store_row = [&](int r, int d, float4 v, float top, float sum) {
       const int rr = block * S::kRows + r;
       const int64_t row = q.row0 + rr / group;
       const int hq = head * group + rr % group;
-      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
+      const float inv = sum > 0.0f ? 1.0f / sum : sum;     // 0 stays 0, NaN stays NaN
       uint2 w;
-      w.x = f32_to_act<DT>(v.x * inv) | (f32_to_act<DT>(v.y * inv) << 16);
-      w.y = f32_to_act<DT>(v.z * inv) | (f32_to_act<DT>(v.w * inv) << 16);
+      if (bf16) {
+        w.x = f32_to_act<MOE_DTYPE_BF16>(v.x * inv) | (f32_to_act<MOE_DTYPE_BF16>(v.y * inv) << 16);
+        w.y = f32_to_act<MOE_DTYPE_BF16>(v.z * inv) | (f32_to_act<MOE_DTYPE_BF16>(v.w * inv) << 16);
+      } else {
+        w.x = f32_to_act<MOE_DTYPE_F16>(v.x * inv) | (f32_to_act<MOE_DTYPE_F16>(v.y * inv) << 16);
+        w.y = f32_to_act<MOE_DTYPE_F16>(v.z * inv) | (f32_to_act<MOE_DTYPE_F16>(v.w * inv) << 16);
+      }
       *reinterpret_cast<uint2*>(a.out + row * a.out_stride + (int64_t)hq * D + d) = w;
       if (d == 0 && a.lse)
         a.lse[row * a.q_heads + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     };
     for (int u = tid; u < R * (D / 4); u += kThreads) {
       const int r = u / (D / 4), d = (u % (D / 4)) * 4;
-      // the writer of this unit was the lane with column col of row r
-      const int col16 = D == 64 ? d / 8 : (d % 128) / 16;
-      const int col = D == 64 ? col16 : ((col16 & 3) << 1) | (col16 >> 2);
-      const int unit = (d / 4) ^ (((col >> 1) >> 1) ^ ((r & 1) << 1));
+      const int unit = unit_of(r, d);
       float top = kNoMax, sum = 0.0f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -590,7 +656,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - top), sum);
       }
-      if (whole_seg) {
+      if (opens && closes) {
         store_row(r, d, v, top, sum);
       } else {
         *reinterpret_cast<float4*>(part + ((size_t)slot * kMaxRows + r) * D + d) = v;
@@ -600,48 +666,72 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         }
       }
     }
-    if (!whole_seg) {
+    if (!(opens && closes)) {
       // the last piece of the segment to arrive joins all of them
-      const int c0 = (int)(seg_at / per), c1 = (int)((seg_at + q.steps - 1) / per);
+      const int c0 = (int)((seg_at + kSegmentCost) / per), c1 = (int)((seg_at + length - 1) / per);
+      const int np = c1 - c0 + 1;
       __threadfence();
       __syncthreads();
       if (tid == 0) {
         const uint32_t before = atomicAdd(&counters[c0], 1u);
-        s_last = before == (uint32_t)(c1 - c0);
+        s_last = before == (uint32_t)(np - 1);
         if (s_last) counters[c0] = 0;
       }
       __syncthreads();
       if (s_last) {
         __threadfence();
+        // every piece's factor per row; the ring's memory holds them
+        float* fac = reinterpret_cast<float*>(big);
+        auto stat = [&](int p, int r) { return stats + (size_t)(2 * (c0 + p) + (p == 0)) * 2 * kMaxRows + r; };
+        for (int r = warp; r < R; r += kWarps) {
+          float top = kNoMax, sum = 0.0f;
+          for (int p = lane; p < np; p += 32) top = fmaxf(top, __ldcg(stat(p, r)));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          for (int p = lane; p < np; p += 32) {
+            const float k = exp2_approx(__ldcg(stat(p, r)) - top);
+            fac[p * S::kRows + r] = k;
+            sum = fmaf(__ldcg(stat(p, r) + kMaxRows), k, sum);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) s_m[0][r] = top, s_l[0][r] = sum;
+        }
+        __syncthreads();
         for (int u = tid; u < R * (D / 4); u += kThreads) {
           const int r = u / (D / 4), d = (u % (D / 4)) * 4;
-          float top = kNoMax;
-          for (int p = c0; p <= c1; ++p)
-            top = fmaxf(top, __ldcg(stats + (size_t)(2 * p + (p == c0)) * 2 * kMaxRows + r));
-          float sum = 0.0f;
+          const float* src = part + ((size_t)(2 * c0) * kMaxRows + r) * D + d;
+          constexpr size_t kSlot = (size_t)kMaxRows * D;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int p = c0; p <= c1; ++p) {
-            const size_t sl = 2 * p + (p == c0);
-            const float k = exp2_approx(__ldcg(stats + sl * 2 * kMaxRows + r) - top);
-            sum = fmaf(__ldcg(stats + sl * 2 * kMaxRows + kMaxRows + r), k, sum);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(part + (sl * kMaxRows + r) * D + d));
-            v.x = fmaf(o.x, k, v.x), v.y = fmaf(o.y, k, v.y), v.z = fmaf(o.z, k, v.z), v.w = fmaf(o.w, k, v.w);
+          constexpr int kBatch = 8;
+          for (int p0 = 0; p0 < np; p0 += kBatch) {
+            float4 o[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int p = p0 + i;
+              o[i] = p < np ? __ldcg(reinterpret_cast<const float4*>(src + (2 * p + (p == 0)) * kSlot))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const float k = p0 + i < np ? fac[(p0 + i) * S::kRows + r] : 0.0f;
+              v.x = fmaf(o[i].x, k, v.x), v.y = fmaf(o[i].y, k, v.y);
+              v.z = fmaf(o[i].z, k, v.z), v.w = fmaf(o[i].w, k, v.w);
+            }
           }
-          store_row(r, d, v, top, sum);
+          store_row(r, d, v, s_m[0][r], s_l[0][r]);
         }
       }
     }
-    pos = seg_at + st1;
     // plain writes to the ring's memory come before the next segment's copies into it
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
   }
 }
 
-template <int DT, int D, int MT>
+template <int D, int NT, int WARPS>
 cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
-  using S = Shape<D, MT>;
+  using S = Shape<D, NT, WARPS>;
   CUtensorMap map[2];
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.c.kv_heads * a.c.page_size, (uint64_t)a.c.num_pages};
   const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.c.page_stride};
@@ -650,23 +740,25 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
   if (!make_map3(&map[0], a.c.k_codes, dims, strides, box, swz) ||
       !make_map3(&map[1], a.c.v_codes, dims, strides, box, swz))
     return cudaErrorInvalidValue;
-  auto kern = attention_kernel<DT, S>;
+  auto kern = attention_kernel<S>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   int grid = num_sms() * S::kCtas;
   if (grid > kMaxGrid) grid = kMaxGrid;
-  kern<<<grid, kThreads, S::kSmem, s>>>(a, map[0], map[1]);
+  kern<<<grid, S::kThreads, S::kSmem, s>>>(a, map[0], map[1]);
   return cudaGetLastError();
 }
 
-template <int DT>
+template <int D>
 cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
-  // Two row tiles once the sequences' rows do not fit one on average: each pass over the keys
-  // then serves 32 rows (256-value heads keep one: their accumulators fill the registers).
-  const bool wide = (long long)a.T * (a.q_heads / a.c.kv_heads) > 16LL * a.b.B;
-  if (a.c.head_dim == 64) return wide ? launch_shape<DT, 64, 2>(a, s) : launch_shape<DT, 64, 1>(a, s);
-  if (a.c.head_dim == 128) return wide ? launch_shape<DT, 128, 2>(a, s) : launch_shape<DT, 128, 1>(a, s);
-  return launch_shape<DT, 256, 1>(a, s);
+  // Row tiles of a block: as many as hold the sequences' rows on average, so that one pass
+  // over the keys serves them (at most 32 rows; 16 where 256-value accumulators fill the
+  // registers).
+  const long long rows = ((long long)a.T * (a.q_heads / a.c.kv_heads) + a.b.B - 1) / a.b.B;
+  const bool few = (long long)a.b.B * a.c.kv_heads <= num_sms();
+  if (rows <= 8) return few ? launch_shape<D, 1, D == 256 ? 8 : 12>(a, s) : launch_shape<D, 1, 4>(a, s);
+  if (rows <= 16 || D == 256) return launch_shape<D, 2, 4>(a, s);
+  return launch_shape<D, D == 256 ? 2 : 4, 4>(a, s);
 }
 
 }  // namespace
@@ -675,8 +767,9 @@ size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim) {
   return align_up(kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4);
 }
 
-cudaError_t launch_attention(const AttentionArgs& a, int dtype, cudaStream_t s) {
-  return dtype == MOE_DTYPE_BF16 ? launch_dim<MOE_DTYPE_BF16>(a, s) : launch_dim<MOE_DTYPE_F16>(a, s);
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
+  if (a.c.head_dim == 64) return launch_dim<64>(a, s);
+  return a.c.head_dim == 128 ? launch_dim<128>(a, s) : launch_dim<256>(a, s);
 }
 
 }  // namespace moe

@@ -24,7 +24,7 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, cudaStream_t s);
 struct AttentionArgs {
   moe_kv_cache c;
   moe_seq_batch b;
-  int T, q_heads, window;
+  int T, q_heads, dtype, window;
   float scale;
   const uint16_t* q;
   uint16_t* out;
@@ -33,7 +33,7 @@ struct AttentionArgs {
   char* ws;
 };
 size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim);
-cudaError_t launch_attention(const AttentionArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
 
 struct LinearArgs {
   const uint16_t* x;

@@ -133,6 +133,7 @@ moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, 
   a.b = *batch;
   a.T = T;
   a.q_heads = q_heads;
+  a.dtype = dtype;
   a.window = window;
   a.scale = scale;
   a.q = static_cast<const uint16_t*>(q);
@@ -141,7 +142,7 @@ moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, 
   a.out_stride = out_stride;
   a.lse = lse;
   a.ws = static_cast<char*>(ws);
-  return from_cuda(launch_attention(a, dtype, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t K) {
