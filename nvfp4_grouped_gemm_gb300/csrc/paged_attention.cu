@@ -1,4 +1,5 @@
-// Causal attention of new tokens over the paged 8-bit cache (moe_attention_paged_e4m3).
+// Causal attention of new tokens over the paged 8-bit cache (moe_attention_paged_e4m3), the form
+// for few rows; prompt_attention.cu has the one for many.
 //
 // A sequence's n new tokens and the G query heads that share a key head are n*G rows over the
 // same keys and values; a segment is (sequence, key head, block of 16*MT such rows). Its keys
@@ -39,6 +40,10 @@ constexpr float kLazy = 8.0f;
 // What a segment costs beside its steps (queries, first copies, the warps' rows meeting), in
 // steps: pieces of the line are equal with it counted.
 constexpr int kSegmentCost = 6;
+
+// Rows of a sequence (new tokens times query heads per key head) from which on it goes to the
+// tensor-memory form of prompt_attention.cu.
+constexpr int kPromptRows = 48;
 
 // Workspace: error word; arrival counters [kMaxGrid]; partial maxima and sums
 // [2 * kMaxGrid][2][kMaxRows]; partial rows f32 [2 * kMaxGrid][kMaxRows][D].
@@ -110,6 +115,7 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
   q.row0 = min(max(a.b.q_offsets[b], 0), a.T);
   const int end = min(max(a.b.q_offsets[b + 1], q.row0), a.T);
   q.n = end - q.row0;
+  if (q.n * group > a.max_rows) q.n = 0;       // the other form's
   q.len = a.b.seq_lens[b];
   q.start = q.len - q.n;
   const int cap = a.b.max_pages * a.c.page_size;
@@ -262,8 +268,11 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
         for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int x = y; x < 4; x += 2)
-            if (!masked || sc[nt][h][x] > -INFINITY)
-              sc[nt][h][x] = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - to);
+            if (!masked || sc[nt][h][x] > -INFINITY) {
+              // scores so large that their rounding alone passes 2^8 end there (NaN stays)
+              const float v = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - to);
+              sc[nt][h][x] = v > kLazy ? kLazy : v;
+            }
       }
     }
 #pragma unroll
@@ -764,10 +773,21 @@ cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim) {
-  return align_up(kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4);
+  const size_t few = kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4;
+  const size_t many = head_dim <= 128 ? prompt_attention_ws_bytes(head_dim) : 0;
+  return align_up(few > many ? few : many);
 }
 
-cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
+cudaError_t launch_attention(const AttentionArgs& args, cudaStream_t s) {
+  AttentionArgs a = args;
+  a.max_rows = 0x7fffffff;
+  if (a.c.head_dim <= 128 && a.T > a.b.B && (long long)a.T * (a.q_heads / a.c.kv_heads) >= kPromptRows) {
+    // some sequence may have that many rows; which ones have is settled on the GPU
+    const bool all = a.b.B == 1;
+    const cudaError_t e = launch_prompt_attention(a, all ? 1 : kPromptRows, s);
+    if (e != cudaSuccess || all) return e;
+    a.max_rows = kPromptRows - 1;
+  }
   if (a.c.head_dim == 64) return launch_dim<64>(a, s);
   return a.c.head_dim == 128 ? launch_dim<128>(a, s) : launch_dim<256>(a, s);
 }

@@ -1,0 +1,735 @@
+// Causal attention over the paged 8-bit cache for sequences with many query rows (chunks of
+// prompts, long drafts): the tensor-memory form of moe_attention_paged_e4m3. paged_attention.cu
+// has the form for few rows and the definitions both share.
+//
+// Rows of a sequence that share a key head (n new tokens times the group of query heads) come in
+// blocks of 256, two tiles A and B of 128; keys come in tiles of 128. All segments' (sequence,
+// head, block) key tiles form one line that the grid cuts into equal pieces, one CTA per SM, as
+// in paged_attention.cu; a cut segment's partial rows are joined by the last CTA to arrive.
+//
+//   warps 0-3, 4-7   softmax of tile A, B: thread = row. S from tensor memory, the weights
+//                    2^(s f + v - M) as f16 back over S, the row's sum in f32; M moves only when
+//                    a weight would pass 2^8, and O is rescaled (in tensor memory) only then
+//   warps 8-11       keys and values: 16-byte pieces from the pages, widened to f16 (exact) and
+//                    stored as 128-byte-swizzled tiles; slots past the end or in pages out of
+//                    range become 0
+//   warp 12          one thread issues the tensor-core products (kind::f16, f32 accumulation):
+//                    S = Q K^T (K-major tiles), O += P V (P from tensor memory, V as the tile's
+//                    rows, i.e. with the value dimension contiguous)
+// While tile A's softmax runs, the tensor cores work on tile B and the other way round. A commit
+// covers every product issued before it, so a softmax that sees its S knows that the previous
+// O += P V is complete and may rescale O.
+//
+// Per key tile and SM the two products of both row tiles take 4 * 128 * 128 * D * 2 operations and
+// the exponentials 2 * 128 * 128 of 16 per clock: about the same time at D = 128, so the two
+// alternate near both limits.
+#include "serving.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 128;                     // keys per tile, rows per row tile
+constexpr int kBlock = 256;                    // rows per block
+constexpr int kThreads = 16 * 32;
+constexpr int kSoftmax = 256, kConvert = 128;
+// Registers per thread of the softmax, widening and issuing warpgroups: 2 * 168 + 112 + 64 =
+// 4 * 128, what the block is launched with.
+constexpr int kRegsSoftmax = 168, kRegsConvert = 112, kRegsIssue = 64;
+constexpr float kNoMax = -1e30f;
+constexpr float kLazy = 8.0f;
+// A segment's fixed cost (queries, first tiles, storing rows) in key tiles.
+constexpr int kSegmentCost = 3;
+
+// Workspace: arrival counters and partials follow those of the other form's header; rows are
+// stored [D/4][256][4].
+constexpr size_t kCountersAt = kAlign;
+constexpr size_t kStatsAt = kCountersAt + kPromptMaxGrid * 4;
+constexpr size_t kRowsAt = kStatsAt + (size_t)2 * kPromptMaxGrid * 2 * kBlock * 4;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// 32 consecutive 32-bit TMEM columns of this warp's 32 lanes, and the wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]),"r"(r[1]),"r"(r[2]),"r"(r[3]),"r"(r[4]),"r"(r[5]),"r"(r[6]),"r"(r[7]),"r"(r[8]),"r"(r[9]),"r"(r[10]),"r"(r[11]),"r"(r[12]),"r"(r[13]),"r"(r[14]),"r"(r[15]),"r"(r[16]),"r"(r[17]),"r"(r[18]),"r"(r[19]),"r"(r[20]),"r"(r[21]),"r"(r[22]),"r"(r[23]),"r"(r[24]),"r"(r[25]),"r"(r[26]),"r"(r[27]),"r"(r[28]),"r"(r[29]),"r"(r[30]),"r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Instruction descriptor, kind::f16: f32 accumulator (bit 4), A and B f16, B's major bit 16 (1:
+// its N dimension contiguous), N >> 3 at 17, M >> 4 at 24.
+constexpr uint32_t f16_idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D (+)= A B with A and B in shared memory, or A in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A sequence's rows and its share of the line.
+struct Seq {
+  int row0, n, start, len, blocks;
+  long long per_head;                          // line length of one key head
+};
+// Key tiles [x, y) that block `block` of a sequence can see.
+__device__ __forceinline__ int2 block_tiles(const Seq& q, int block, int group, int window) {
+  const int first = block * kBlock / group, last = (min((block + 1) * kBlock, q.n * group) - 1) / group;
+  const int hi = min(q.len, q.start + last + 1);
+  const int lo = window > 0 ? max(0, q.start + first - window + 1) : 0;
+  const int x = lo / kTile;
+  return make_int2(x, max(x, (max(hi, 0) + kTile - 1) / kTile));
+}
+__device__ __forceinline__ int block_line(const Seq& q, int block, int group, int window) {
+  const int2 t = block_tiles(q, block, group, window);
+  return max(t.y - t.x, 1) + kSegmentCost;
+}
+__device__ Seq read_seq(const AttentionArgs& a, int b, int group, int min_rows, uint32_t* err) {
+  Seq q;
+  q.row0 = min(max(a.b.q_offsets[b], 0), a.T);
+  const int end = min(max(a.b.q_offsets[b + 1], q.row0), a.T);
+  q.n = end - q.row0;
+  q.len = a.b.seq_lens[b];
+  q.start = q.len - q.n;
+  q.blocks = 0;
+  q.per_head = 0;
+  if (q.n * group < min_rows || q.n == 0) return q;        // the other form's, or nothing to do
+  const int cap = a.b.max_pages * a.c.page_size;
+  if ((q.start < 0 || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+  q.len = min(max(q.len, 0), cap);
+  q.blocks = (q.n * group + kBlock - 1) / kBlock;
+  for (int i = 0; i < q.blocks; ++i) q.per_head += block_line(q, i, group, a.window);
+  return q;
+}
+
+// One CTA's share of one segment.
+struct Piece {
+  int b, head, block, R;
+  int t0, t1;                                  // key tiles to work on (none if t0 >= t1)
+  bool opens, closes;                          // holds the segment's first / last tile
+  int c0, np;                                  // the CTAs the segment is spread over
+  int tok0;                                    // token of the block's first row
+};
+// Walks a CTA's piece of the line; every thread that needs it walks for itself.
+struct Walk {
+  long long pos, end, per, first;
+  int b, head, block;
+  long long at;                                // line position of (b, head, block)
+  Seq q;
+  __device__ void enter(const AttentionArgs& a, int group, int min_rows) {  // from (b, first)
+    q = read_seq(a, b, group, min_rows, nullptr);
+    head = q.per_head ? (int)((pos - first) / q.per_head) : 0;
+    block = 0;
+    at = first + head * q.per_head;
+  }
+  __device__ bool next(const AttentionArgs& a, int group, int min_rows, Piece& p) {
+    while (pos < end) {
+      while (pos >= first + q.per_head * a.c.kv_heads) {
+        first += q.per_head * a.c.kv_heads;
+        ++b;
+        enter(a, group, min_rows);
+      }
+      int line = block_line(q, block, group, a.window);
+      while (pos >= at + line) {
+        at += line;
+        if (++block == q.blocks) block = 0, ++head;
+        line = block_line(q, block, group, a.window);
+      }
+      const int2 t = block_tiles(q, block, group, a.window);
+      const int st0 = max(0, (int)(pos - at) - kSegmentCost);
+      const int st1 = (int)min((long long)line, end - at) - kSegmentCost;
+      pos = at + st1 + kSegmentCost;
+      if (st1 <= st0) continue;                // only the segment's fixed cost fell to this CTA
+      p.b = b, p.head = head, p.block = block;
+      p.R = min(kBlock, q.n * group - block * kBlock);
+      p.tok0 = block * kBlock / group;
+      p.t0 = t.x + st0, p.t1 = min(t.x + st1, t.y);
+      p.opens = st0 == 0, p.closes = st1 == line - kSegmentCost;
+      p.c0 = (int)((at + kSegmentCost) / per);
+      p.np = (int)((at + line - 1) / per) - p.c0 + 1;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kQ = 128 * D * 2;       // one row tile of queries
+  static constexpr int kKv = kTile * D * 2;    // one widened key or value tile
+  static constexpr int kHalf = 128 * 128;      // 64 values of 128 rows
+  static constexpr int kQAt = 0, kKAt = 2 * kQ, kVAt = kKAt + 2 * kKv;
+  static constexpr int kBytes = kVAt + 2 * kKv;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
+  using S = Smem<D>;
+  extern __shared__ char smem_raw[];
+  __shared__ uint64_t s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2], s_sfull[2], s_pfull[2], s_qfull[2], s_drain, s_join;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ long long s_sum[kThreads / 32], s_first;
+  __shared__ int s_seq, s_last;
+  __shared__ float4 s_coef[8][8];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size;
+  uint32_t* err = reinterpret_cast<uint32_t*>(a.ws);
+  volatile int* abort_flag = &s_abort;
+
+  // ---- this CTA's piece of the line (before any tensor memory is taken) ----
+  auto scan = [&](long long v, long long* before) {
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += up;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    long long base = 0, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += s_sum[w];
+      all += s_sum[w];
+    }
+    *before = base + x - v;
+    return all;
+  };
+  long long total = 0, at = 0;
+  for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
+    long long mine = 0;
+    if (b0 + tid < a.b.B)
+      mine = read_seq(a, b0 + tid, group, min_rows, blockIdx.x == 0 ? err : nullptr).per_head * heads;
+    total += scan(mine, &at);
+  }
+  Walk walk;
+  walk.per = (total + gridDim.x - 1) / gridDim.x;
+  if (walk.per < kSegmentCost + 1) walk.per = kSegmentCost + 1;
+  walk.pos = walk.per * blockIdx.x;
+  walk.end = min(walk.pos + walk.per, total);
+  if (walk.pos >= walk.end) return;
+  long long base = 0;
+  for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
+    long long mine = 0;
+    if (b0 + tid < a.b.B) mine = read_seq(a, b0 + tid, group, min_rows, nullptr).per_head * heads;
+    const long long sum = scan(mine, &at);
+    if (mine > 0 && base + at <= walk.pos && walk.pos < base + at + mine) s_seq = b0 + tid, s_first = base + at;
+    base += sum;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_kfull[i], kConvert);
+      mbar_init(&s_vfull[i], kConvert);
+      mbar_init(&s_kempty[i], 1);
+      mbar_init(&s_vempty[i], 1);
+      mbar_init(&s_sfull[i], 1);
+      mbar_init(&s_pfull[i], 128);
+      mbar_init(&s_qfull[i], 128);
+    }
+    mbar_init(&s_drain, 1);
+    mbar_init(&s_join, kSoftmax);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  walk.b = s_seq;
+  walk.first = s_first;
+  walk.enter(a, group, min_rows);
+  Piece p;
+
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // ---------------- products ----------------
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t id_s = f16_idesc(128, kTile, false), id_o = f16_idesc(128, D, true);
+      const uint32_t sm = smem_u32(smem);
+      uint32_t kv = 0, qph = 0, pph[2] = {0, 0};           // key tiles, pieces, softmax tiles so far
+      bool ok = true;
+      auto scores = [&](int tile, uint32_t t) {            // S of a row tile with key tile t
+        const uint64_t qd = smem_desc(sm + S::kQAt + tile * S::kQ, 16, 1024, 2);
+        const uint64_t kd = smem_desc(sm + S::kKAt + (t & 1) * S::kKv, 16, 1024, 2);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t o = (uint32_t)((i >> 2) * S::kHalf + (i & 3) * 32) >> 4;
+          mma_ss(tmem + tile * 128, qd + o, kd + o, id_s, i != 0);
+        }
+      };
+      auto values = [&](int tile, uint32_t t, bool add) {  // O += P V
+        const uint64_t vd = smem_desc(sm + S::kVAt + (t & 1) * S::kKv, S::kHalf, 1024, 2);
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          mma_ts(tmem + 256 + tile * D, tmem + tile * 128 + 8 * i, vd + (uint32_t)(i * 2048 >> 4), id_o,
+                 (add || i != 0) ? 1u : 0u);
+      };
+      while (ok && walk.next(a, group, min_rows, p)) {
+        const int nt = p.t1 - p.t0;
+        if (nt <= 0) continue;
+        const int tiles = p.R > 128 ? 2 : 1;
+        for (int i = 0; i < tiles && ok; ++i) ok = mbar_wait(&s_qfull[i], (qph >> i) & 1, abort_flag, err);
+        qph ^= tiles == 2 ? 3u : 1u;
+        if (ok) ok = mbar_wait(&s_kfull[kv & 1], (kv >> 1) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < tiles; ++i) {
+          scores(i, kv);
+          tc_commit(&s_sfull[i]);
+        }
+        tc_commit(&s_kempty[kv & 1]);
+        for (int t = 0; t < nt && ok; ++t, ++kv) {
+          ok = mbar_wait(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err);
+          const bool more = t + 1 < nt;
+          for (int i = 0; i < tiles && ok; ++i) {
+            ok = mbar_wait(&s_pfull[i], pph[i] & 1, abort_flag, err);
+            ++pph[i];
+            if (!ok) break;
+            tc_fence_after();
+            values(i, kv, t > 0);
+            if (i == tiles - 1) tc_commit(&s_vempty[kv & 1]);
+            if (more) {
+              if (i == 0) {
+                ok = mbar_wait(&s_kfull[(kv + 1) & 1], ((kv + 1) >> 1) & 1, abort_flag, err);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              scores(i, kv + 1);
+              if (i == tiles - 1) tc_commit(&s_kempty[(kv + 1) & 1]);
+            }
+            tc_commit(&s_sfull[i]);                        // S of the next tile, or the final O
+          }
+        }
+      }
+      // every product is done before the tensor memory is given back
+      tc_commit(&s_drain);
+      const uint64_t t0 = global_ns();
+      while (!mbar_try(&s_drain, 0) && global_ns() - t0 < 100000000ull) {
+      }
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    // ---------------- keys and values ----------------
+    const int ct = tid - kSoftmax;
+    constexpr int kPieces = D / 16;            // 16-byte pieces of a token's row, and per thread
+    const int piece = ct % kPieces, tok0 = ct / kPieces;
+    constexpr int kStride = kConvert / kPieces;            // tokens between a thread's pieces
+    uint32_t kv = 0;
+    bool ok = true;
+    while (ok && walk.next(a, group, min_rows, p)) {
+      const Seq& q = walk.q;
+      const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
+      int page[kPieces];
+      auto pages = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int j = t * kTile + tok0 + i * kStride;
+          page[i] = j < q.len ? __ldg(table + j / P) : -1;
+        }
+      };
+      auto fetch = [&](const uint8_t* plane, int t, uint4 (&r)[kPieces]) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int j = t * kTile + tok0 + i * kStride;
+          r[i] = make_uint4(0, 0, 0, 0);
+          if (page[i] >= 0 && page[i] < a.c.num_pages)
+            r[i] = __ldg(reinterpret_cast<const uint4*>(plane + (int64_t)page[i] * a.c.page_stride +
+                                                        ((int64_t)p.head * P + j % P) * D + piece * 16));
+        }
+      };
+      auto widen = [&](char* dst, const uint4 (&r)[kPieces]) {
+        // values 16*piece..: half piece/4, 16-byte columns 2*(piece%4) and the next; odd and even
+        // columns in opposite order for the two halves, so that a quarter warp hits every bank
+        const int flip = piece >> 2, col = 2 * (piece & 3);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int tok = tok0 + i * kStride;
+          char* row = dst + (piece >> 2) * S::kHalf + tok * 128;
+          uint4 lo, hi;
+          widen4(r[i].x, lo.x, lo.y);
+          widen4(r[i].y, lo.z, lo.w);
+          widen4(r[i].z, hi.x, hi.y);
+          widen4(r[i].w, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(row + (((col + flip) ^ (tok & 7)) * 16)) = flip ? hi : lo;
+          *reinterpret_cast<uint4*>(row + (((col + 1 - flip) ^ (tok & 7)) * 16)) = flip ? lo : hi;
+        }
+      };
+      uint4 kr[kPieces], vr[kPieces];
+      if (p.t0 < p.t1) {
+        pages(p.t0);
+        fetch(a.c.k_codes, p.t0, kr);
+      }
+      for (int t = p.t0; t < p.t1; ++t, ++kv) {
+        fetch(a.c.v_codes, t, vr);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (page[i] >= a.c.num_pages || (page[i] < 0 && t * kTile + tok0 + i * kStride < q.len))
+            atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+        if (!(ok = mbar_wait_warp(&s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err))) break;
+        widen(smem + S::kKAt + (kv & 1) * S::kKv, kr);
+        fence_async();
+        mbar_arrive(&s_kfull[kv & 1]);
+        if (t + 1 < p.t1) {
+          pages(t + 1);
+          fetch(a.c.k_codes, t + 1, kr);
+        }
+        if (!(ok = mbar_wait_warp(&s_vempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err))) break;
+        widen(smem + S::kVAt + (kv & 1) * S::kKv, vr);
+        fence_async();
+        mbar_arrive(&s_vfull[kv & 1]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ---------------- softmax: thread = row ----------------
+    const int tile = warp >> 2;
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + tile * 128 + quarter, o_col = tmem + 256 + tile * D + quarter;
+    const int r = tid;                                     // row of the block
+    const bool bf16 = a.dtype == MOE_DTYPE_BF16;
+    uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kCountersAt);
+    float* stats = reinterpret_cast<float*>(a.ws + kStatsAt);
+    float4* part = reinterpret_cast<float4*>(a.ws + kRowsAt);
+    uint32_t sph = 0, jph = 0;
+    bool ok = true;
+    // the softmax threads meet (bounded, like every wait here)
+    auto meet = [&] {
+      mbar_arrive(&s_join);
+      return mbar_wait_warp(&s_join, jph++ & 1, abort_flag, err);
+    };
+    while (walk.next(a, group, min_rows, p)) {
+      const Seq& q = walk.q;
+      const int nt = p.t1 - p.t0;
+      const bool live = p.R > 128 * tile;                  // this row tile is worked on
+      const bool warp_live = p.R > 32 * warp;              // this warp has rows
+      const int rr = p.block * kBlock + r;
+      const int place = q.start + rr / group;
+      const int64_t row = q.row0 + rr / group;
+      const int hq = p.head * group + rr % group;
+      float M = kNoMax, L = 0.0f, rowf = 1.0f;
+      if (live && nt > 0) {
+        // the row as f16 times a power of two, K-major, 128-byte swizzle
+        const uint16_t* src = a.q + row * a.q_stride + (int64_t)hq * D;
+        float amax = 0.0f;
+        if (r < p.R && bf16) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            float f[8];
+            unpack8<MOE_DTYPE_BF16>(__ldg(reinterpret_cast<const uint4*>(src) + i), f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(f[x]));
+          }
+        }
+        const int e = amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
+        const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
+        rowf = pow2f(e);
+        char* dst = smem + S::kQAt + tile * S::kQ + (r & 127) * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (r < p.R) {
+            w = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            if (bf16) {
+              float f[8];
+              unpack8<MOE_DTYPE_BF16>(w, f);
+              w.x = pack_f16(f[0] * s1 * s2, f[1] * s1 * s2), w.y = pack_f16(f[2] * s1 * s2, f[3] * s1 * s2);
+              w.z = pack_f16(f[4] * s1 * s2, f[5] * s1 * s2), w.w = pack_f16(f[6] * s1 * s2, f[7] * s1 * s2);
+            }
+          }
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * S::kHalf + (((i & 7) ^ (r & 7)) * 16)) = w;
+        }
+        fence_async();
+        mbar_arrive(&s_qfull[tile]);
+
+        // page factors of a tile's eight 16-key groups: lane g < 8 holds group g's
+        const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
+        auto page_of = [&](int t) {
+          const int j = t * kTile + (lane & 7) * 16;
+          const int page = t < p.t1 && j < q.len ? __ldg(table + j / P) : -1;
+          return page < a.c.num_pages ? page : -1;
+        };
+        auto coef_of = [&](int page) {
+          float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (page >= 0) {
+            const int64_t sc = (int64_t)page * heads + p.head;
+            const float vs = fminf(fmaxf(__ldg(a.c.v_scales + sc), 0x1p-100f), 0x1p120f);
+            c = make_float4(a.scale * 1.4426950408889634f * __ldg(a.c.k_scales + sc), log2f(vs),
+                            __fdividef(1.0f, vs), 1.0f);
+          }
+          return c;
+        };
+        float4 coef = coef_of(page_of(p.t0));
+        int page_next = page_of(p.t0 + 1);
+        const int place_lo = q.start + p.tok0;             // the block's first and last rows
+        const int place_hi = q.start + (p.block * kBlock + p.R - 1) / group;
+        for (int t = p.t0; t < p.t1; ++t) {
+          __syncwarp();
+          if (lane < 8) s_coef[warp][lane] = coef;
+          __syncwarp();
+          const bool gone = !__all_sync(0xffffffffu, coef.w > 0.0f);
+          coef = coef_of(page_next);
+          page_next = page_of(t + 2);
+          if (!(ok = mbar_wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) break;
+          ++sph;
+          tc_fence_after();
+          if (warp_live) {
+            const int j0 = t * kTile;
+            bool masked = gone || j0 + kTile > place_lo + 1 || j0 + kTile > q.len;
+            if (a.window > 0) masked |= j0 <= place_hi - a.window;
+            // keys j0 + x with x in [x0, x1) are the row's; groups without a page are nobody's
+            const int x1 = min(place + 1, q.len) - j0;
+            const int x0 = a.window > 0 ? place - a.window + 1 - j0 : 0;
+            uint32_t pw[64];
+            float lt;
+            for (int pass = 0;; ++pass) {
+              bool moved = false;
+              lt = 0.0f;
+#pragma unroll
+              for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                tmem_ld32(s_col + ch * 32, s);
+                float top = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float4 c = s_coef[warp][2 * ch + h];
+                  const float f = c.x * rowf, d = c.y - M;
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) s[16 * h + x] = fmaf(s[16 * h + x], f, d);
+                  if (masked) {
+                    const int y0 = x0 - ch * 32 - h * 16, y1 = c.w > 0.0f ? x1 - ch * 32 - h * 16 : 0;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                      if (x < y0 || x >= y1) s[16 * h + x] = -INFINITY;
+                  }
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) top = fmaxf(top, s[16 * h + x]);
+                }
+                if (__any_sync(0xffffffffu, top > kLazy)) {
+                  if (pass == 0) {
+                    moved = true;
+                    break;
+                  }
+                  // scores so large that their rounding alone passes 2^8
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) s[x] = s[x] > kLazy ? kLazy : s[x];
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float sum = 0.0f;
+#pragma unroll
+                  for (int x = 0; x < 16; x += 2) {
+                    const float e0 = exp2_approx(s[16 * h + x]), e1 = exp2_approx(s[16 * h + x + 1]);
+                    sum += e0 + e1;
+                    pw[ch * 16 + h * 8 + x / 2] = pack_f16(e0, e1);
+                  }
+                  lt = fmaf(s_coef[warp][2 * ch + h].z, sum, lt);
+                }
+              }
+              if (!moved) break;
+              // the row's maximum over the whole tile; then O and L follow and the tile restarts
+              float to = M;
+#pragma unroll 1
+              for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                tmem_ld32(s_col + ch * 32, s);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float4 c = s_coef[warp][2 * ch + h];
+                  const float f = c.x * rowf;
+                  const int y0 = x0 - ch * 32 - h * 16, y1 = c.w > 0.0f ? x1 - ch * 32 - h * 16 : 0;
+#pragma unroll
+                  for (int x = 0; x < 16; ++x)
+                    if (x >= y0 && x < y1) to = fmaxf(to, fmaf(s[16 * h + x], f, c.y));
+                }
+              }
+              const float keep = exp2_approx(M - to);
+              M = to;
+              L *= keep;
+              if (t > p.t0) {
+#pragma unroll 1
+                for (int i = 0; i < D / 32; ++i) {
+                  float o[32];
+                  uint32_t w[32];
+                  tmem_ld32(o_col + i * 32, o);
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x] * keep);
+                  tmem_st32(o_col + i * 32, w);
+                }
+              }
+            }
+            L += lt;
+            tmem_st32(s_col, pw);
+            tmem_st32(s_col + 32, pw + 32);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          mbar_arrive(&s_pfull[tile]);
+        }
+        if (ok && (ok = mbar_wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) {
+          ++sph;
+          tc_fence_after();
+        }
+      }
+      if (!ok) break;
+      // ---- the rows' results ----
+      const bool whole = p.opens && p.closes, mine = r < p.R;
+      const float inv = L > 0.0f ? 1.0f / L : L;           // 0 stays 0, NaN stays NaN
+      auto store8 = [&](int d, const float* v, float k) {  // values d..d+7 of the row
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) f[x] = v[x] * k;
+        *reinterpret_cast<uint4*>(a.out + row * a.out_stride + (int64_t)hq * D + d) =
+            bf16 ? pack8<MOE_DTYPE_BF16>(f) : pack8<MOE_DTYPE_F16>(f);
+      };
+      auto store_lse = [&](float top, float sum) {
+        if (a.lse)
+          a.lse[row * a.q_heads + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      };
+      const int slot = 2 * blockIdx.x + (p.opens ? 1 : 0);
+      if (live) {
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          if (nt > 0 && warp_live) {
+            tmem_ld32(o_col + i * 32, o);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+          }
+          if (mine) {
+            if (whole) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) store8(i * 32 + x, o + x, inv);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; x += 4)
+                part[((size_t)slot * (D / 4) + i * 8 + x / 4) * kBlock + r] =
+                    make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            }
+          }
+        }
+        if (mine && whole) store_lse(M, L);
+        if (mine && !whole) {
+          stats[(size_t)slot * 2 * kBlock + r] = M;
+          stats[((size_t)slot * 2 + 1) * kBlock + r] = L;
+        }
+        tc_fence_before();
+      }
+      if (!whole) {
+        // the last piece of the segment to arrive joins all of them
+        __threadfence();
+        if (!(ok = meet())) break;
+        if (tid == 0) {
+          const uint32_t before = atomicAdd(&counters[p.c0], 1u);
+          s_last = before == (uint32_t)(p.np - 1);
+          if (s_last) counters[p.c0] = 0;
+        }
+        if (!(ok = meet())) break;
+        if (s_last && mine) {
+          __threadfence();
+          auto slot_of = [&](int i) { return (size_t)2 * (p.c0 + i) + (i == 0); };
+          float top = kNoMax, sum = 0.0f;
+          for (int i = 0; i < p.np; ++i) top = fmaxf(top, __ldcg(stats + slot_of(i) * 2 * kBlock + r));
+          for (int i = 0; i < p.np; ++i)
+            sum = fmaf(__ldcg(stats + (slot_of(i) * 2 + 1) * kBlock + r),
+                       exp2_approx(__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top), sum);
+          const float k1 = sum > 0.0f ? 1.0f / sum : sum;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            float v[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = 0.0f;
+            for (int i = 0; i < p.np; ++i) {
+              const float k = exp2_approx(__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top);
+              float4 o[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) o[x] = __ldcg(part + (slot_of(i) * (D / 4) + d / 4 + x) * kBlock + r);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                v[4 * x] = fmaf(o[x].x, k, v[4 * x]), v[4 * x + 1] = fmaf(o[x].y, k, v[4 * x + 1]);
+                v[4 * x + 2] = fmaf(o[x].z, k, v[4 * x + 2]), v[4 * x + 3] = fmaf(o[x].w, k, v[4 * x + 3]);
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) store8(d + x, v + x, k1);
+          }
+          store_lse(top, sum);
+        }
+        if (!(ok = meet())) break;             // s_last is read before it is set again
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+}
+
+template <int D>
+cudaError_t launch_prompt(const AttentionArgs& a, int min_rows, cudaStream_t s) {
+  constexpr int smem = 1024 + Smem<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = num_sms() < kPromptMaxGrid ? num_sms() : kPromptMaxGrid;
+  prompt_kernel<D><<<grid, kThreads, smem, s>>>(a, min_rows);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t prompt_attention_ws_bytes(int head_dim) {
+  return kRowsAt + (size_t)2 * kPromptMaxGrid * kBlock * head_dim * 4;
+}
+
+cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, cudaStream_t s) {
+  return a.c.head_dim == 64 ? launch_prompt<64>(a, min_rows, s) : launch_prompt<128>(a, min_rows, s);
+}
+
+}  // namespace moe

@@ -25,6 +25,7 @@ struct AttentionArgs {
   moe_kv_cache c;
   moe_seq_batch b;
   int T, q_heads, dtype, window;
+  int max_rows;                // sequences with more rows are left to the other form
   float scale;
   const uint16_t* q;
   uint16_t* out;
@@ -34,6 +35,12 @@ struct AttentionArgs {
 };
 size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
+
+// The form for sequences of at least min_rows rows (new tokens times query heads per key head);
+// head_dim 64 or 128.
+constexpr int kPromptMaxGrid = 160;
+size_t prompt_attention_ws_bytes(int head_dim);
+cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, cudaStream_t s);
 
 struct LinearArgs {
   const uint16_t* x;
