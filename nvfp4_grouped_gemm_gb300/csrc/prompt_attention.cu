@@ -33,9 +33,9 @@ constexpr int kTile = 128;                     // keys per tile, rows per row ti
 constexpr int kBlock = 256;                    // rows per block
 constexpr int kThreads = 16 * 32;
 constexpr int kSoftmax = 256, kConvert = 128;
-// Registers per thread of the softmax, widening and issuing warpgroups: 2 * 168 + 112 + 64 =
+// Registers per thread of the softmax, widening and issuing warpgroups: 2 * 144 + 128 + 96 =
 // 4 * 128, what the block is launched with.
-constexpr int kRegsSoftmax = 168, kRegsConvert = 112, kRegsIssue = 64;
+constexpr int kRegsSoftmax = 144, kRegsConvert = 128, kRegsIssue = 96;
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
 // A segment's fixed cost (queries, first tiles, storing rows) in key tiles.
@@ -80,6 +80,39 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Pairs of f32 in one 64-bit register.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max16(const float* s) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m[i] = fmaxf(fmaxf(s[4 * i], s[4 * i + 1]), fmaxf(s[4 * i + 2], s[4 * i + 3]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// Scores of 32 keys: those outside [x0, x1), and of a group of 16 without a page, become -inf.
+__device__ __forceinline__ void hide(float (&s)[32], int x0, int x1, bool there0, bool there1) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (x < x0 || x >= x1 || !(x < 16 ? there0 : there1)) s[x] = -INFINITY;
 }
 
 // Instruction descriptor, kind::f16: f32 accumulator (bit 4), A and B f16, B's major bit 16 (1:
@@ -495,7 +528,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
           return page < a.c.num_pages ? page : -1;
         };
         auto coef_of = [&](int page) {
-          float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 c = make_float4(1.f, 0.f, 0.f, 0.f);      // no page: weights of -inf
           if (page >= 0) {
             const int64_t sc = (int64_t)page * heads + p.head;
             const float vs = fminf(fmaxf(__ldg(a.c.v_scales + sc), 0x1p-100f), 0x1p120f);
@@ -524,71 +557,20 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
             if (a.window > 0) masked |= j0 <= place_hi - a.window;
             // keys j0 + x with x in [x0, x1) are the row's; groups without a page are nobody's
             const int x1 = min(place + 1, q.len) - j0;
-            const int x0 = a.window > 0 ? place - a.window + 1 - j0 : 0;
-            uint32_t pw[64];
-            float lt;
-            for (int pass = 0;; ++pass) {
-              bool moved = false;
-              lt = 0.0f;
-#pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                float s[32];
-                tmem_ld32(s_col + ch * 32, s);
-                float top = -INFINITY;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float4 c = s_coef[warp][2 * ch + h];
-                  const float f = c.x * rowf, d = c.y - M;
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) s[16 * h + x] = fmaf(s[16 * h + x], f, d);
-                  if (masked) {
-                    const int y0 = x0 - ch * 32 - h * 16, y1 = c.w > 0.0f ? x1 - ch * 32 - h * 16 : 0;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                      if (x < y0 || x >= y1) s[16 * h + x] = -INFINITY;
-                  }
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) top = fmaxf(top, s[16 * h + x]);
-                }
-                if (__any_sync(0xffffffffu, top > kLazy)) {
-                  if (pass == 0) {
-                    moved = true;
-                    break;
-                  }
-                  // scores so large that their rounding alone passes 2^8
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) s[x] = s[x] > kLazy ? kLazy : s[x];
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float sum = 0.0f;
-#pragma unroll
-                  for (int x = 0; x < 16; x += 2) {
-                    const float e0 = exp2_approx(s[16 * h + x]), e1 = exp2_approx(s[16 * h + x + 1]);
-                    sum += e0 + e1;
-                    pw[ch * 16 + h * 8 + x / 2] = pack_f16(e0, e1);
-                  }
-                  lt = fmaf(s_coef[warp][2 * ch + h].z, sum, lt);
-                }
-              }
-              if (!moved) break;
-              // the row's maximum over the whole tile; then O and L follow and the tile restarts
-              float to = M;
+            const int x0 = a.window > 0 ? place - a.window + 1 - j0 : -j0;
+            // the largest s f + v of the row in this tile (f > 0: from each group's largest s)
+            float top = kNoMax;
 #pragma unroll 1
-              for (int ch = 0; ch < 4; ++ch) {
-                float s[32];
-                tmem_ld32(s_col + ch * 32, s);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float4 c = s_coef[warp][2 * ch + h];
-                  const float f = c.x * rowf;
-                  const int y0 = x0 - ch * 32 - h * 16, y1 = c.w > 0.0f ? x1 - ch * 32 - h * 16 : 0;
-#pragma unroll
-                  for (int x = 0; x < 16; ++x)
-                    if (x >= y0 && x < y1) to = fmaxf(to, fmaf(s[16 * h + x], f, c.y));
-                }
-              }
-              const float keep = exp2_approx(M - to);
+            for (int ch = 0; ch < 4; ++ch) {
+              float s[32];
+              tmem_ld32(s_col + ch * 32, s);
+              const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
+              if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+              top = fmaxf(top, fmaf(max16(s), c0.x * rowf, c0.y));
+              top = fmaxf(top, fmaf(max16(s + 16), c1.x * rowf, c1.y));
+            }
+            if (__any_sync(0xffffffffu, top > M + kLazy)) {
+              const float to = fmaxf(M, top), keep = exp2_approx(M - to);
               M = to;
               L *= keep;
               if (t > p.t0) {
@@ -603,9 +585,36 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
                 }
               }
             }
-            L += lt;
-            tmem_st32(s_col, pw);
-            tmem_st32(s_col + 32, pw + 32);
+            // scores so large that their rounding alone could pass 2^8 end there
+            const bool huge = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax);
+            // weights; columns 16 ch .. of P lie over columns of S that are already read
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              float s[32];
+              uint32_t w[16];
+              tmem_ld32(s_col + ch * 32, s);
+              const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
+              if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
+                const uint64_t ff = pair(f, f), dd = pair(d, d);
+                uint64_t sum = 0;
+#pragma unroll
+                for (int x = 0; x < 16; x += 2) {
+                  float e0, e1;
+                  unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
+                  if (huge) e0 = e0 > kLazy ? kLazy : e0, e1 = e1 > kLazy ? kLazy : e1;
+                  e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+                  sum = add2(sum, pair(e0, e1));
+                  w[h * 8 + x / 2] = pack_f16(e0, e1);
+                }
+                float l0, l1;
+                unpair(sum, l0, l1);
+                L = fmaf(h ? c1.z : c0.z, l0 + l1, L);
+              }
+              tc_st16(s_col + ch * 16, w);
+            }
             tmem_wait_st();
           }
           tc_fence_before();
