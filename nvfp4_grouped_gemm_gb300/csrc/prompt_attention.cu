@@ -33,9 +33,13 @@ constexpr int kTile = 128;                     // keys per tile, rows per row ti
 constexpr int kBlock = 256;                    // rows per block
 constexpr int kThreads = 16 * 32;
 constexpr int kSoftmax = 256, kConvert = 128;
-// Registers per thread of the softmax, widening and issuing warpgroups: 2 * 144 + 128 + 96 =
+// Registers per thread of the softmax, widening and issuing warpgroups: 2 * 136 + 136 + 104 =
 // 4 * 128, what the block is launched with.
-constexpr int kRegsSoftmax = 144, kRegsConvert = 128, kRegsIssue = 96;
+constexpr int kRegsLaunch = 65536 / kThreads;
+constexpr int kRegsSoftmax = 136, kRegsConvert = 136, kRegsIssue = 104;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 4 * kRegsLaunch, "more than the block has");
+// raising and lowering are different instructions, each legal in its own direction only
+static_assert(kRegsSoftmax >= kRegsLaunch && kRegsConvert >= kRegsLaunch && kRegsIssue <= kRegsLaunch, "");
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
 // A segment's fixed cost (queries, first tiles, storing rows) in key tiles.
@@ -327,21 +331,25 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
       const uint32_t sm = smem_u32(smem);
       uint32_t kv = 0, qph = 0, pph[2] = {0, 0};           // key tiles, pieces, softmax tiles so far
       bool ok = true;
+      // Loops, not unrolled: the issuing thread's instructions then stay in the nearest cache.
       auto scores = [&](int tile, uint32_t t) {            // S of a row tile with key tile t
-        const uint64_t qd = smem_desc(sm + S::kQAt + tile * S::kQ, 16, 1024, 2);
-        const uint64_t kd = smem_desc(sm + S::kKAt + (t & 1) * S::kKv, 16, 1024, 2);
-#pragma unroll
+        uint64_t qd = smem_desc(sm + S::kQAt + tile * S::kQ, 16, 1024, 2);
+        uint64_t kd = smem_desc(sm + S::kKAt + (t & 1) * S::kKv, 16, 1024, 2);
+#pragma unroll 1
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t o = (uint32_t)((i >> 2) * S::kHalf + (i & 3) * 32) >> 4;
-          mma_ss(tmem + tile * 128, qd + o, kd + o, id_s, i != 0);
+          mma_ss(tmem + tile * 128, qd, kd, id_s, i != 0);
+          const uint32_t step = (i & 3) == 3 ? (S::kHalf - 96) >> 4 : 2;
+          qd += step, kd += step;
         }
       };
       auto values = [&](int tile, uint32_t t, bool add) {  // O += P V
-        const uint64_t vd = smem_desc(sm + S::kVAt + (t & 1) * S::kKv, S::kHalf, 1024, 2);
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          mma_ts(tmem + 256 + tile * D, tmem + tile * 128 + 8 * i, vd + (uint32_t)(i * 2048 >> 4), id_o,
-                 (add || i != 0) ? 1u : 0u);
+        uint64_t vd = smem_desc(sm + S::kVAt + (t & 1) * S::kKv, S::kHalf, 1024, 2);
+        uint32_t pc = tmem + tile * 128;
+#pragma unroll 1
+        for (int i = 0; i < kTile / 16; ++i) {
+          mma_ts(tmem + 256 + tile * D, pc, vd, id_o, (add || i != 0) ? 1u : 0u);
+          pc += 8, vd += 2048 >> 4;
+        }
       };
       while (ok && walk.next(a, group, min_rows, p)) {
         const int nt = p.t1 - p.t0;
@@ -387,33 +395,40 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
       }
     }
   } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
     // ---------------- keys and values ----------------
     const int ct = tid - kSoftmax;
     constexpr int kPieces = D / 16;            // 16-byte pieces of a token's row, and per thread
-    const int piece = ct % kPieces, tok0 = ct / kPieces;
+    const int piece = ct % kPieces, tok0 = ct / kPieces, log_p = 31 - __clz(P);
     constexpr int kStride = kConvert / kPieces;            // tokens between a thread's pieces
     uint32_t kv = 0;
     bool ok = true;
     while (ok && walk.next(a, group, min_rows, p)) {
       const Seq& q = walk.q;
       const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
-      int page[kPieces];
-      auto pages = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int j = t * kTile + tok0 + i * kStride;
-          page[i] = j < q.len ? __ldg(table + j / P) : -1;
+      // lane l holds the page of a tile's 16-key group l % 8 (-1: past the end, or out of range)
+      auto page_of = [&](int t) {
+        const int j = t * kTile + (lane & 7) * 16;
+        int page = -1;
+        if (t < p.t1 && j < q.len) {
+          page = __ldg(table + (j >> log_p));
+          if (page < 0 || page >= a.c.num_pages) {
+            atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+            page = -1;
+          }
         }
+        return page;
       };
-      auto fetch = [&](const uint8_t* plane, int t, uint4 (&r)[kPieces]) {
+      const int64_t head_at = (int64_t)p.head * P * D + piece * 16;
+      auto fetch = [&](const uint8_t* plane, int t, int pages, uint4 (&r)[kPieces]) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int j = t * kTile + tok0 + i * kStride;
+          const int tok = tok0 + i * kStride, j = t * kTile + tok;
+          const int page = __shfl_sync(0xffffffffu, pages, tok >> 4);
           r[i] = make_uint4(0, 0, 0, 0);
-          if (page[i] >= 0 && page[i] < a.c.num_pages)
-            r[i] = __ldg(reinterpret_cast<const uint4*>(plane + (int64_t)page[i] * a.c.page_stride +
-                                                        ((int64_t)p.head * P + j % P) * D + piece * 16));
+          if (page >= 0 && j < q.len)
+            r[i] = __ldg(reinterpret_cast<const uint4*>(plane + page * a.c.page_stride + head_at +
+                                                        (j & (P - 1)) * D));
         }
       };
       auto widen = [&](char* dst, const uint4 (&r)[kPieces]) {
@@ -434,24 +449,17 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
         }
       };
       uint4 kr[kPieces], vr[kPieces];
-      if (p.t0 < p.t1) {
-        pages(p.t0);
-        fetch(a.c.k_codes, p.t0, kr);
-      }
+      int pages = page_of(p.t0), pages_next = page_of(p.t0 + 1);
+      fetch(a.c.k_codes, p.t0, pages, kr);
       for (int t = p.t0; t < p.t1; ++t, ++kv) {
-        fetch(a.c.v_codes, t, vr);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          if (page[i] >= a.c.num_pages || (page[i] < 0 && t * kTile + tok0 + i * kStride < q.len))
-            atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+        fetch(a.c.v_codes, t, pages, vr);
         if (!(ok = mbar_wait_warp(&s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err))) break;
         widen(smem + S::kKAt + (kv & 1) * S::kKv, kr);
         fence_async();
         mbar_arrive(&s_kfull[kv & 1]);
-        if (t + 1 < p.t1) {
-          pages(t + 1);
-          fetch(a.c.k_codes, t + 1, kr);
-        }
+        pages = pages_next;
+        pages_next = page_of(t + 2);
+        fetch(a.c.k_codes, t + 1, pages, kr);
         if (!(ok = mbar_wait_warp(&s_vempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err))) break;
         widen(smem + S::kVAt + (kv & 1) * S::kKv, vr);
         fence_async();
@@ -466,6 +474,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
     const uint32_t s_col = tmem + tile * 128 + quarter, o_col = tmem + 256 + tile * D + quarter;
     const int r = tid;                                     // row of the block
     const bool bf16 = a.dtype == MOE_DTYPE_BF16;
+    const int log_p = 31 - __clz(P);
     uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kCountersAt);
     float* stats = reinterpret_cast<float*>(a.ws + kStatsAt);
     float4* part = reinterpret_cast<float4*>(a.ws + kRowsAt);
@@ -524,7 +533,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
         const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
         auto page_of = [&](int t) {
           const int j = t * kTile + (lane & 7) * 16;
-          const int page = t < p.t1 && j < q.len ? __ldg(table + j / P) : -1;
+          const int page = t < p.t1 && j < q.len ? __ldg(table + (j >> log_p)) : -1;
           return page < a.c.num_pages ? page : -1;
         };
         auto coef_of = [&](int page) {
