@@ -10,10 +10,10 @@
 //   warps 0-3, 4-7   softmax of tile A, B: thread = row. S from tensor memory, the weights
 //                    2^(s f + v - M) as f16 back over S, the row's sum in f32; M moves only when
 //                    a weight would pass 2^8, and O is rescaled (in tensor memory) only then
-//   warps 8-11       keys and values: 16-byte pieces from the pages, widened to f16 (exact) and
+//   warps 8-15       keys and values: 16-byte pieces from the pages, widened to f16 (exact) and
 //                    stored as 128-byte-swizzled tiles; slots past the end or in pages out of
 //                    range become 0
-//   warp 12          one thread issues the tensor-core products (kind::f16, f32 accumulation):
+//   warp 16          one thread issues the tensor-core products (kind::f16, f32 accumulation):
 //                    S = Q K^T (K-major tiles), O += P V (P from tensor memory, V as the tile's
 //                    rows, i.e. with the value dimension contiguous)
 // While tile A's softmax runs, the tensor cores work on tile B and the other way round. A commit
@@ -23,6 +23,8 @@
 // Per key tile and SM the two products of both row tiles take 4 * 128 * 128 * D * 2 operations and
 // the exponentials 2 * 128 * 128 of 16 per clock: about the same time at D = 128, so the two
 // alternate near both limits.
+#include <climits>
+
 #include "serving.cuh"
 #include "tcgen05.cuh"
 
@@ -31,15 +33,15 @@ namespace {
 
 constexpr int kTile = 128;                     // keys per tile, rows per row tile
 constexpr int kBlock = 256;                    // rows per block
-constexpr int kThreads = 16 * 32;
-constexpr int kSoftmax = 256, kConvert = 128;
-// Registers per thread of the softmax, widening and issuing warpgroups: 2 * 136 + 136 + 104 =
-// 4 * 128, what the block is launched with.
-constexpr int kRegsLaunch = 65536 / kThreads;
-constexpr int kRegsSoftmax = 136, kRegsConvert = 136, kRegsIssue = 104;
-static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 4 * kRegsLaunch, "more than the block has");
+constexpr int kThreads = 20 * 32;
+constexpr int kSoftmax = 256, kConvert = 256;
+// Registers per thread of the two softmax, two widening and one issuing warpgroups: together not
+// more than the block is launched with.
+constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 64;
+static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue <= 5 * kRegsLaunch, "more than the block has");
 // raising and lowering are different instructions, each legal in its own direction only
-static_assert(kRegsSoftmax >= kRegsLaunch && kRegsConvert >= kRegsLaunch && kRegsIssue <= kRegsLaunch, "");
+static_assert(kRegsSoftmax >= kRegsLaunch && kRegsConvert <= kRegsLaunch && kRegsIssue <= kRegsLaunch, "");
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
 // A segment's fixed cost (queries, first tiles, storing rows) in key tiles.
@@ -76,11 +78,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]),"r"(r[1]),"r"(r[2]),"r"(r[3]),"r"(r[4]),"r"(r[5]),"r"(r[6]),"r"(r[7]),"r"(r[8]),"r"(r[9]),"r"(r[10]),"r"(r[11]),"r"(r[12]),"r"(r[13]),"r"(r[14]),"r"(r[15]),"r"(r[16]),"r"(r[17]),"r"(r[18]),"r"(r[19]),"r"(r[20]),"r"(r[21]),"r"(r[22]),"r"(r[23]),"r"(r[24]),"r"(r[25]),"r"(r[26]),"r"(r[27]),"r"(r[28]),"r"(r[29]),"r"(r[30]),"r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -141,6 +147,12 @@ __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// One arrival for the warp, after what all its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // A sequence's rows and its share of the line.
 struct Seq {
   int row0, n, start, len, blocks;
@@ -158,7 +170,7 @@ __device__ __forceinline__ int block_line(const Seq& q, int block, int group, in
   const int2 t = block_tiles(q, block, group, window);
   return max(t.y - t.x, 1) + kSegmentCost;
 }
-__device__ Seq read_seq(const AttentionArgs& a, int b, int group, int min_rows, uint32_t* err) {
+__device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group, int min_rows, uint32_t* err) {
   Seq q;
   q.row0 = min(max(a.b.q_offsets[b], 0), a.T);
   const int end = min(max(a.b.q_offsets[b + 1], q.row0), a.T);
@@ -178,54 +190,56 @@ __device__ Seq read_seq(const AttentionArgs& a, int b, int group, int min_rows, 
 
 // One CTA's share of one segment.
 struct Piece {
-  int b, head, block, R;
-  int t0, t1;                                  // key tiles to work on (none if t0 >= t1)
+  bool more;                                   // false: the CTA's line ended
   bool opens, closes;                          // holds the segment's first / last tile
+  int b, head, block, R;                       // sequence, key head, block of rows, rows in it
+  int row0, start, len;                        // of the sequence
+  int t0, t1;                                  // key tiles to work on (none if t0 >= t1)
   int c0, np;                                  // the CTAs the segment is spread over
-  int tok0;                                    // token of the block's first row
 };
-// Walks a CTA's piece of the line; every thread that needs it walks for itself.
+// A CTA's piece of the line. Every warp walks for itself, its first lane in shared memory.
 struct Walk {
   long long pos, end, per, first;
   int b, head, block;
   long long at;                                // line position of (b, head, block)
   Seq q;
-  __device__ void enter(const AttentionArgs& a, int group, int min_rows) {  // from (b, first)
-    q = read_seq(a, b, group, min_rows, nullptr);
-    head = q.per_head ? (int)((pos - first) / q.per_head) : 0;
-    block = 0;
-    at = first + head * q.per_head;
-  }
-  __device__ bool next(const AttentionArgs& a, int group, int min_rows, Piece& p) {
-    while (pos < end) {
-      while (pos >= first + q.per_head * a.c.kv_heads) {
-        first += q.per_head * a.c.kv_heads;
-        ++b;
-        enter(a, group, min_rows);
-      }
-      int line = block_line(q, block, group, a.window);
-      while (pos >= at + line) {
-        at += line;
-        if (++block == q.blocks) block = 0, ++head;
-        line = block_line(q, block, group, a.window);
-      }
-      const int2 t = block_tiles(q, block, group, a.window);
-      const int st0 = max(0, (int)(pos - at) - kSegmentCost);
-      const int st1 = (int)min((long long)line, end - at) - kSegmentCost;
-      pos = at + st1 + kSegmentCost;
-      if (st1 <= st0) continue;                // only the segment's fixed cost fell to this CTA
-      p.b = b, p.head = head, p.block = block;
-      p.R = min(kBlock, q.n * group - block * kBlock);
-      p.tok0 = block * kBlock / group;
-      p.t0 = t.x + st0, p.t1 = min(t.x + st1, t.y);
-      p.opens = st0 == 0, p.closes = st1 == line - kSegmentCost;
-      p.c0 = (int)((at + kSegmentCost) / per);
-      p.np = (int)((at + line - 1) / per) - p.c0 + 1;
-      return true;
-    }
-    return false;
-  }
 };
+__device__ __forceinline__ void walk_enter(Walk& w, const AttentionArgs& a, int group, int min_rows) {  // from (b, first)
+  w.q = read_seq(a, w.b, group, min_rows, nullptr);
+  w.head = w.q.per_head ? (int)((w.pos - w.first) / w.q.per_head) : 0;
+  w.block = 0;
+  w.at = w.first + w.head * w.q.per_head;
+}
+__device__ __forceinline__ void walk_next(Walk& w, Piece& p, const AttentionArgs& a, int group, int min_rows) {
+  p.more = false;
+  while (w.pos < w.end) {
+    while (w.pos >= w.first + w.q.per_head * a.c.kv_heads) {
+      w.first += w.q.per_head * a.c.kv_heads;
+      ++w.b;
+      walk_enter(w, a, group, min_rows);
+    }
+    int line = block_line(w.q, w.block, group, a.window);
+    while (w.pos >= w.at + line) {
+      w.at += line;
+      if (++w.block == w.q.blocks) w.block = 0, ++w.head;
+      line = block_line(w.q, w.block, group, a.window);
+    }
+    const int2 t = block_tiles(w.q, w.block, group, a.window);
+    const int st0 = max(0, (int)(w.pos - w.at) - kSegmentCost);
+    const int st1 = (int)min((long long)line, w.end - w.at) - kSegmentCost;
+    w.pos = w.at + st1 + kSegmentCost;
+    if (st1 <= st0) continue;                  // only the segment's fixed cost fell to this CTA
+    p.b = w.b, p.head = w.head, p.block = w.block;
+    p.R = min(kBlock, w.q.n * group - w.block * kBlock);
+    p.row0 = w.q.row0, p.start = w.q.start, p.len = w.q.len;
+    p.t0 = t.x + st0, p.t1 = min(t.x + st1, t.y);
+    p.opens = st0 == 0, p.closes = st1 == line - kSegmentCost;
+    p.c0 = (int)((w.at + kSegmentCost) / w.per);
+    p.np = (int)((w.at + line - 1) / w.per) - p.c0 + 1;
+    p.more = true;
+    return;
+  }
+}
 
 template <int D>
 struct Smem {
@@ -247,6 +261,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
   __shared__ long long s_sum[kThreads / 32], s_first;
   __shared__ int s_seq, s_last;
   __shared__ float4 s_coef[8][8];
+  __shared__ Walk s_walk[17];
+  __shared__ Piece s_piece[17];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size;
@@ -279,37 +295,35 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
       mine = read_seq(a, b0 + tid, group, min_rows, blockIdx.x == 0 ? err : nullptr).per_head * heads;
     total += scan(mine, &at);
   }
-  Walk walk;
-  walk.per = (total + gridDim.x - 1) / gridDim.x;
-  if (walk.per < kSegmentCost + 1) walk.per = kSegmentCost + 1;
-  walk.pos = walk.per * blockIdx.x;
-  walk.end = min(walk.pos + walk.per, total);
-  if (walk.pos >= walk.end) return;
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kSegmentCost + 1) per = kSegmentCost + 1;
+  const long long begin = per * blockIdx.x, end = min(begin + per, total);
+  if (begin >= end) return;
   long long base = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
     long long mine = 0;
     if (b0 + tid < a.b.B) mine = read_seq(a, b0 + tid, group, min_rows, nullptr).per_head * heads;
     const long long sum = scan(mine, &at);
-    if (mine > 0 && base + at <= walk.pos && walk.pos < base + at + mine) s_seq = b0 + tid, s_first = base + at;
+    if (mine > 0 && base + at <= begin && begin < base + at + mine) s_seq = b0 + tid, s_first = base + at;
     base += sum;
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_kfull[i], kConvert);
-      mbar_init(&s_vfull[i], kConvert);
+      mbar_init(&s_kfull[i], kConvert / 32);               // one arrival per warp
+      mbar_init(&s_vfull[i], kConvert / 32);
       mbar_init(&s_kempty[i], 1);
       mbar_init(&s_vempty[i], 1);
       mbar_init(&s_sfull[i], 1);
-      mbar_init(&s_pfull[i], 128);
-      mbar_init(&s_qfull[i], 128);
+      mbar_init(&s_pfull[i], 4);
+      mbar_init(&s_qfull[i], 4);
     }
     mbar_init(&s_drain, 1);
-    mbar_init(&s_join, kSoftmax);
+    mbar_init(&s_join, kSoftmax / 32);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(smem_u32(&s_tmem)), "n"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -318,40 +332,51 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  walk.b = s_seq;
-  walk.first = s_first;
-  walk.enter(a, group, min_rows);
-  Piece p;
+  if (warp < 17 && lane == 0) {
+    Walk& w = s_walk[warp];
+    w.pos = begin, w.end = end, w.per = per, w.first = s_first, w.b = s_seq;
+    walk_enter(w, a, group, min_rows);
+  }
+  __syncwarp();
+  const Piece& p = s_piece[warp < 17 ? warp : 0];          // this warp's
+  auto next_piece = [&] {                                  // all lanes of a warp
+    __syncwarp();
+    if (lane == 0) walk_next(s_walk[warp], s_piece[warp], a, group, min_rows);
+    __syncwarp();
+    return p.more;
+  };
 
-  if (warp >= 12) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ---------------- products ----------------
-    if (warp == 12 && lane == 0) {
+    // One thread issues both tiles' in turn, A's and then B's: it keeps the tiles half a period
+    // apart, so that one's softmax runs beside the other's products.
+    if (warp == 16 && lane == 0) {
       constexpr uint32_t id_s = f16_idesc(128, kTile, false), id_o = f16_idesc(128, D, true);
       const uint32_t sm = smem_u32(smem);
-      uint32_t kv = 0, qph = 0, pph[2] = {0, 0};           // key tiles, pieces, softmax tiles so far
+      const uint64_t q_desc = smem_desc(sm + S::kQAt, 16, 1024, 2);
+      const uint64_t k_desc = smem_desc(sm + S::kKAt, 16, 1024, 2);
+      const uint64_t v_desc = smem_desc(sm + S::kVAt, S::kHalf, 1024, 2);
+      uint32_t kv = 0, qph = 0, pph = 0;                   // key tiles; phases per row tile
       bool ok = true;
-      // Loops, not unrolled: the issuing thread's instructions then stay in the nearest cache.
       auto scores = [&](int tile, uint32_t t) {            // S of a row tile with key tile t
-        uint64_t qd = smem_desc(sm + S::kQAt + tile * S::kQ, 16, 1024, 2);
-        uint64_t kd = smem_desc(sm + S::kKAt + (t & 1) * S::kKv, 16, 1024, 2);
-#pragma unroll 1
+        const uint64_t qd = q_desc + tile * (S::kQ >> 4), kd = k_desc + (t & 1) * (S::kKv >> 4);
+#pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          mma_ss(tmem + tile * 128, qd, kd, id_s, i != 0);
-          const uint32_t step = (i & 3) == 3 ? (S::kHalf - 96) >> 4 : 2;
-          qd += step, kd += step;
+          const uint32_t o = (uint32_t)((i >> 2) * S::kHalf + (i & 3) * 32) >> 4;
+          mma_ss(tmem + tile * 128, qd + o, kd + o, id_s, i != 0);
         }
       };
       auto values = [&](int tile, uint32_t t, bool add) {  // O += P V
-        uint64_t vd = smem_desc(sm + S::kVAt + (t & 1) * S::kKv, S::kHalf, 1024, 2);
-        uint32_t pc = tmem + tile * 128;
-#pragma unroll 1
-        for (int i = 0; i < kTile / 16; ++i) {
-          mma_ts(tmem + 256 + tile * D, pc, vd, id_o, (add || i != 0) ? 1u : 0u);
-          pc += 8, vd += 2048 >> 4;
-        }
+        const uint64_t vd = v_desc + (t & 1) * (S::kKv >> 4);
+        const uint32_t o_col = tmem + 256 + tile * D, p_col = tmem + tile * 128;
+        mma_ts(o_col, p_col, vd, id_o, add ? 1u : 0u);
+#pragma unroll
+        for (int i = 1; i < kTile / 16; ++i) mma_ts(o_col, p_col + 8 * i, vd + (uint32_t)(i * 2048 >> 4), id_o, 1u);
       };
-      while (ok && walk.next(a, group, min_rows, p)) {
+      while (ok) {
+        walk_next(s_walk[warp], s_piece[warp], a, group, min_rows);
+        if (!p.more) break;
         const int nt = p.t1 - p.t0;
         if (nt <= 0) continue;
         const int tiles = p.R > 128 ? 2 : 1;
@@ -366,25 +391,24 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
         }
         tc_commit(&s_kempty[kv & 1]);
         for (int t = 0; t < nt && ok; ++t, ++kv) {
-          ok = mbar_wait(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err);
+          if (!(ok = mbar_wait(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
           const bool more = t + 1 < nt;
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = mbar_wait(&s_pfull[i], pph[i] & 1, abort_flag, err);
-            ++pph[i];
-            if (!ok) break;
+#pragma unroll 1
+          for (int i = 0; i < tiles; ++i) {
+            // K of the next tile first: usually long there, and the products below then follow
+            // each other without a check between them
+            if (more && i == 0 &&
+                !(ok = mbar_wait(&s_kfull[(kv + 1) & 1], ((kv + 1) >> 1) & 1, abort_flag, err))) break;
+            if (!(ok = mbar_wait(&s_pfull[i], (pph >> i) & 1, abort_flag, err))) break;
+            pph ^= 1u << i;
             tc_fence_after();
             values(i, kv, t > 0);
-            if (i == tiles - 1) tc_commit(&s_vempty[kv & 1]);
-            if (more) {
-              if (i == 0) {
-                ok = mbar_wait(&s_kfull[(kv + 1) & 1], ((kv + 1) >> 1) & 1, abort_flag, err);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              scores(i, kv + 1);
-              if (i == tiles - 1) tc_commit(&s_kempty[(kv + 1) & 1]);
-            }
+            if (more) scores(i, kv + 1);
             tc_commit(&s_sfull[i]);                        // S of the next tile, or the final O
+            if (i == tiles - 1) {
+              tc_commit(&s_vempty[kv & 1]);
+              if (more) tc_commit(&s_kempty[(kv + 1) & 1]);
+            }
           }
         }
       }
@@ -395,75 +419,88 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
       }
     }
   } else if (warp >= 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
     // ---------------- keys and values ----------------
+    // Half tiles in turn (K's two, V's two, the next tile's ...), each fetched three halves ahead.
     const int ct = tid - kSoftmax;
-    constexpr int kPieces = D / 16;            // 16-byte pieces of a token's row, and per thread
-    const int piece = ct % kPieces, tok0 = ct / kPieces, log_p = 31 - __clz(P);
+    constexpr int kPieces = D / 16;            // 16-byte pieces of a token's row
     constexpr int kStride = kConvert / kPieces;            // tokens between a thread's pieces
+    constexpr int kHalfN = 64 / kStride;       // a thread's pieces of 64 tokens
+    const int piece = ct % kPieces, tok0 = ct / kPieces, log_p = 31 - __clz(P);
+    const int64_t thread_at = (int64_t)(tok0 & 15) * D + piece * 16;
+    // values 16*piece..: half piece/4, 16-byte columns 2*(piece%4) and the next; odd and even
+    // columns in opposite order for the two halves, so that a quarter warp hits every bank
+    const int flip = piece >> 2, col = 2 * (piece & 3) + flip;
     uint32_t kv = 0;
     bool ok = true;
-    while (ok && walk.next(a, group, min_rows, p)) {
-      const Seq& q = walk.q;
+    while (ok && next_piece()) {
       const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
-      // lane l holds the page of a tile's 16-key group l % 8 (-1: past the end, or out of range)
+      // lane l holds where 16-key group l % 8 of a tile starts in either plane (-1: nowhere)
       auto page_of = [&](int t) {
         const int j = t * kTile + (lane & 7) * 16;
-        int page = -1;
-        if (t < p.t1 && j < q.len) {
-          page = __ldg(table + (j >> log_p));
-          if (page < 0 || page >= a.c.num_pages) {
-            atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
-            page = -1;
+        return t < p.t1 && j < p.len ? __ldg(table + (j >> log_p)) : INT_MIN;
+      };
+      auto start_of = [&](int t, int page) {
+        const int j = t * kTile + (lane & 7) * 16;
+        if (page >= 0 && page < a.c.num_pages)
+          return page * a.c.page_stride + ((int64_t)p.head * P + (j & (P - 1))) * D;
+        if (page != INT_MIN) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+        return (int64_t)-1;
+      };
+      int page_next = page_of(p.t0);           // of the tile after the one fetched from
+      int64_t start = -1;
+      auto fetch = [&](int t, int half, uint4 (&r)[kHalfN]) {   // half 0, 1: K's; 2, 3: V's
+        const uint8_t* plane = half & 2 ? a.c.v_codes : a.c.k_codes;
+        const int tok = (half & 1) * 64, there = p.len - t * kTile - tok;   // tokens that exist
+#pragma unroll
+        for (int i = 0; i < kHalfN; ++i) {
+          const int at_ = tok0 + i * kStride;
+          const int64_t from = __shfl_sync(0xffffffffu, start, (tok + at_) >> 4);
+          r[i] = make_uint4(0, 0, 0, 0);
+          if (from >= 0 && at_ < there) r[i] = __ldg(reinterpret_cast<const uint4*>(plane + from + thread_at));
+        }
+      };
+      uint4 r[4][kHalfN];                      // the four halves; never copied while a load is out
+      if (p.t0 < p.t1) {
+        start = start_of(p.t0, page_next);
+        page_next = page_of(p.t0 + 1);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) fetch(p.t0, h, r[h]);
+      }
+#pragma unroll 1
+      for (int t = p.t0; t < p.t1 && ok; ++t, ++kv) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (h == 0) {
+            fetch(t, 3, r[3]);
+          } else {
+            if (h == 1) {
+              start = start_of(t + 1, page_next);
+              page_next = page_of(t + 2);
+            }
+            if (t + 1 < p.t1) fetch(t + 1, h - 1, r[h - 1]);
+          }
+          if ((h & 1) == 0 && ok)
+            ok = mbar_wait_warp(h ? &s_vempty[kv & 1] : &s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err);
+          if (!ok) break;
+          char* dst = smem + (h & 2 ? S::kVAt : S::kKAt) + (kv & 1) * S::kKv + (piece >> 2) * S::kHalf;
+#pragma unroll
+          for (int i = 0; i < kHalfN; ++i) {
+            const int tok = (h & 1) * 64 + tok0 + i * kStride;
+            uint4 lo, hi;
+            widen4(r[h][i].x, lo.x, lo.y);
+            widen4(r[h][i].y, lo.z, lo.w);
+            widen4(r[h][i].z, hi.x, hi.y);
+            widen4(r[h][i].w, hi.z, hi.w);
+            char* row = dst + tok * 128;
+            *reinterpret_cast<uint4*>(row + ((col ^ (tok & 7)) * 16)) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (((col ^ 1) ^ (tok & 7)) * 16)) = flip ? lo : hi;
+          }
+          if (h & 1) {
+            fence_async();
+            warp_arrive(h & 2 ? &s_vfull[kv & 1] : &s_kfull[kv & 1]);
           }
         }
-        return page;
-      };
-      const int64_t head_at = (int64_t)p.head * P * D + piece * 16;
-      auto fetch = [&](const uint8_t* plane, int t, int pages, uint4 (&r)[kPieces]) {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int tok = tok0 + i * kStride, j = t * kTile + tok;
-          const int page = __shfl_sync(0xffffffffu, pages, tok >> 4);
-          r[i] = make_uint4(0, 0, 0, 0);
-          if (page >= 0 && j < q.len)
-            r[i] = __ldg(reinterpret_cast<const uint4*>(plane + page * a.c.page_stride + head_at +
-                                                        (j & (P - 1)) * D));
-        }
-      };
-      auto widen = [&](char* dst, const uint4 (&r)[kPieces]) {
-        // values 16*piece..: half piece/4, 16-byte columns 2*(piece%4) and the next; odd and even
-        // columns in opposite order for the two halves, so that a quarter warp hits every bank
-        const int flip = piece >> 2, col = 2 * (piece & 3);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int tok = tok0 + i * kStride;
-          char* row = dst + (piece >> 2) * S::kHalf + tok * 128;
-          uint4 lo, hi;
-          widen4(r[i].x, lo.x, lo.y);
-          widen4(r[i].y, lo.z, lo.w);
-          widen4(r[i].z, hi.x, hi.y);
-          widen4(r[i].w, hi.z, hi.w);
-          *reinterpret_cast<uint4*>(row + (((col + flip) ^ (tok & 7)) * 16)) = flip ? hi : lo;
-          *reinterpret_cast<uint4*>(row + (((col + 1 - flip) ^ (tok & 7)) * 16)) = flip ? lo : hi;
-        }
-      };
-      uint4 kr[kPieces], vr[kPieces];
-      int pages = page_of(p.t0), pages_next = page_of(p.t0 + 1);
-      fetch(a.c.k_codes, p.t0, pages, kr);
-      for (int t = p.t0; t < p.t1; ++t, ++kv) {
-        fetch(a.c.v_codes, t, pages, vr);
-        if (!(ok = mbar_wait_warp(&s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err))) break;
-        widen(smem + S::kKAt + (kv & 1) * S::kKv, kr);
-        fence_async();
-        mbar_arrive(&s_kfull[kv & 1]);
-        pages = pages_next;
-        pages_next = page_of(t + 2);
-        fetch(a.c.k_codes, t + 1, pages, kr);
-        if (!(ok = mbar_wait_warp(&s_vempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err))) break;
-        widen(smem + S::kVAt + (kv & 1) * S::kKv, vr);
-        fence_async();
-        mbar_arrive(&s_vfull[kv & 1]);
       }
     }
   } else {
@@ -482,17 +519,16 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
     bool ok = true;
     // the softmax threads meet (bounded, like every wait here)
     auto meet = [&] {
-      mbar_arrive(&s_join);
+      warp_arrive(&s_join);
       return mbar_wait_warp(&s_join, jph++ & 1, abort_flag, err);
     };
-    while (walk.next(a, group, min_rows, p)) {
-      const Seq& q = walk.q;
+    while (next_piece()) {
       const int nt = p.t1 - p.t0;
       const bool live = p.R > 128 * tile;                  // this row tile is worked on
       const bool warp_live = p.R > 32 * warp;              // this warp has rows
       const int rr = p.block * kBlock + r;
-      const int place = q.start + rr / group;
-      const int64_t row = q.row0 + rr / group;
+      const int place = p.start + rr / group;
+      const int64_t row = p.row0 + rr / group;
       const int hq = p.head * group + rr % group;
       float M = kNoMax, L = 0.0f, rowf = 1.0f;
       if (live && nt > 0) {
@@ -527,13 +563,13 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
           *reinterpret_cast<uint4*>(dst + (i >> 3) * S::kHalf + (((i & 7) ^ (r & 7)) * 16)) = w;
         }
         fence_async();
-        mbar_arrive(&s_qfull[tile]);
+        warp_arrive(&s_qfull[tile]);
 
         // page factors of a tile's eight 16-key groups: lane g < 8 holds group g's
         const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
         auto page_of = [&](int t) {
           const int j = t * kTile + (lane & 7) * 16;
-          const int page = t < p.t1 && j < q.len ? __ldg(table + (j >> log_p)) : -1;
+          const int page = t < p.t1 && j < p.len ? __ldg(table + (j >> log_p)) : -1;
           return page < a.c.num_pages ? page : -1;
         };
         auto coef_of = [&](int page) {
@@ -548,8 +584,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
         };
         float4 coef = coef_of(page_of(p.t0));
         int page_next = page_of(p.t0 + 1);
-        const int place_lo = q.start + p.tok0;             // the block's first and last rows
-        const int place_hi = q.start + (p.block * kBlock + p.R - 1) / group;
+        const int place_lo = p.start + p.block * kBlock / group;             // the block's first and last rows
+        const int place_hi = p.start + (p.block * kBlock + p.R - 1) / group;
         for (int t = p.t0; t < p.t1; ++t) {
           __syncwarp();
           if (lane < 8) s_coef[warp][lane] = coef;
@@ -562,10 +598,10 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
           tc_fence_after();
           if (warp_live) {
             const int j0 = t * kTile;
-            bool masked = gone || j0 + kTile > place_lo + 1 || j0 + kTile > q.len;
+            bool masked = gone || j0 + kTile > place_lo + 1 || j0 + kTile > p.len;
             if (a.window > 0) masked |= j0 <= place_hi - a.window;
             // keys j0 + x with x in [x0, x1) are the row's; groups without a page are nobody's
-            const int x1 = min(place + 1, q.len) - j0;
+            const int x1 = min(place + 1, p.len) - j0;
             const int x0 = a.window > 0 ? place - a.window + 1 - j0 : -j0;
             // the largest s f + v of the row in this tile (f > 0: from each group's largest s)
             float top = kNoMax;
@@ -584,13 +620,12 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
               L *= keep;
               if (t > p.t0) {
 #pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
-                  float o[32];
-                  uint32_t w[32];
-                  tmem_ld32(o_col + i * 32, o);
+                for (int i = 0; i < D / 16; ++i) {
+                  float o[16];
+                  tmem_ld16(o_col + i * 16, o);
 #pragma unroll
-                  for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x] * keep);
-                  tmem_st32(o_col + i * 32, w);
+                  for (int x = 0; x < 16; ++x) o[x] *= keep;
+                  tc_st16(o_col + i * 16, *reinterpret_cast<const uint32_t(*)[16]>(o));
                 }
               }
             }
@@ -604,22 +639,28 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
               tmem_ld32(s_col + ch * 32, s);
               const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
               if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+              if (huge) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                  const float most = (M + kLazy - (x < 16 ? c0.y : c1.y)) / ((x < 16 ? c0.x : c1.x) * rowf);
+                  s[x] = s[x] > most ? most : s[x];
+                }
+              }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
                 const uint64_t ff = pair(f, f), dd = pair(d, d);
-                uint64_t sum = 0;
+                uint64_t acc = 0;
 #pragma unroll
                 for (int x = 0; x < 16; x += 2) {
                   float e0, e1;
                   unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
-                  if (huge) e0 = e0 > kLazy ? kLazy : e0, e1 = e1 > kLazy ? kLazy : e1;
                   e0 = exp2_approx(e0), e1 = exp2_approx(e1);
-                  sum = add2(sum, pair(e0, e1));
+                  acc = add2(acc, pair(e0, e1));
                   w[h * 8 + x / 2] = pack_f16(e0, e1);
                 }
                 float l0, l1;
-                unpair(sum, l0, l1);
+                unpair(acc, l0, l1);
                 L = fmaf(h ? c1.z : c0.z, l0 + l1, L);
               }
               tc_st16(s_col + ch * 16, w);
@@ -627,7 +668,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
             tmem_wait_st();
           }
           tc_fence_before();
-          mbar_arrive(&s_pfull[tile]);
+          warp_arrive(&s_pfull[tile]);
         }
         if (ok && (ok = mbar_wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) {
           ++sph;
@@ -726,7 +767,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12)
+  if (warp == 16)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
