@@ -38,7 +38,7 @@ constexpr int kSoftmax = 256, kConvert = 256;
 // Registers per thread of the two softmax, two widening and one issuing warpgroups: together not
 // more than the block is launched with.
 constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
-constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 64;
+constexpr int kRegsSoftmax = 128, kRegsConvert = 80, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue <= 5 * kRegsLaunch, "more than the block has");
 // raising and lowering are different instructions, each legal in its own direction only
 static_assert(kRegsSoftmax >= kRegsLaunch && kRegsConvert <= kRegsLaunch && kRegsIssue <= kRegsLaunch, "");
@@ -111,12 +111,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max16(const float* s) {
-  float m[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    m[i] = fmaxf(fmaxf(s[4 * i], s[4 * i + 1]), fmaxf(s[4 * i + 2], s[4 * i + 3]));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  const float a = max3(s[0], s[1], s[2]), b = max3(s[3], s[4], s[5]), c = max3(s[6], s[7], s[8]);
+  const float d = max3(s[9], s[10], s[11]), e = max3(s[12], s[13], s[14]);
+  return max3(max3(a, b, c), max3(d, e, s[15]), s[15]);
 }
 // Scores of 32 keys: those outside [x0, x1), and of a group of 16 without a page, become -inf.
 __device__ __forceinline__ void hide(float (&s)[32], int x0, int x1, bool there0, bool there1) {
@@ -376,6 +379,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
       };
       while (ok) {
         walk_next(s_walk[warp], s_piece[warp], a, group, min_rows);
+        const Piece p = s_piece[warp];         // in registers
         if (!p.more) break;
         const int nt = p.t1 - p.t0;
         if (nt <= 0) continue;
@@ -426,14 +430,16 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
     constexpr int kPieces = D / 16;            // 16-byte pieces of a token's row
     constexpr int kStride = kConvert / kPieces;            // tokens between a thread's pieces
     constexpr int kHalfN = 64 / kStride;       // a thread's pieces of 64 tokens
-    const int piece = ct % kPieces, tok0 = ct / kPieces, log_p = 31 - __clz(P);
+    // Eight lanes take four pieces of one half (64 values) of two neighbouring tokens: their
+    // stores, 16-byte columns 2*(piece%4) and the next of the half, then hit every bank.
+    const int piece = (ct & 3) + (D == 128 ? (ct >> 3 & 1) * 4 : 0);
+    const int tok0 = (ct >> 2 & 1) + (ct >> (D == 128 ? 4 : 3)) * 2, log_p = 31 - __clz(P);
     const int64_t thread_at = (int64_t)(tok0 & 15) * D + piece * 16;
-    // values 16*piece..: half piece/4, 16-byte columns 2*(piece%4) and the next; odd and even
-    // columns in opposite order for the two halves, so that a quarter warp hits every bank
-    const int flip = piece >> 2, col = 2 * (piece & 3) + flip;
+    const int col = 2 * (piece & 3);
     uint32_t kv = 0;
     bool ok = true;
     while (ok && next_piece()) {
+      const Piece p = s_piece[warp];           // in registers
       const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
       // lane l holds where 16-key group l % 8 of a tile starts in either plane (-1: nowhere)
       auto page_of = [&](int t) {
@@ -493,8 +499,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
             widen4(r[h][i].z, hi.x, hi.y);
             widen4(r[h][i].w, hi.z, hi.w);
             char* row = dst + tok * 128;
-            *reinterpret_cast<uint4*>(row + ((col ^ (tok & 7)) * 16)) = flip ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (((col ^ 1) ^ (tok & 7)) * 16)) = flip ? lo : hi;
+            *reinterpret_cast<uint4*>(row + ((col ^ (tok & 7)) * 16)) = lo;
+            *reinterpret_cast<uint4*>(row + (((col + 1) ^ (tok & 7)) * 16)) = hi;
           }
           if (h & 1) {
             fence_async();
@@ -523,6 +529,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
       return mbar_wait_warp(&s_join, jph++ & 1, abort_flag, err);
     };
     while (next_piece()) {
+      const Piece p = s_piece[warp];           // in registers
       const int nt = p.t1 - p.t0;
       const bool live = p.R > 128 * tile;                  // this row tile is worked on
       const bool warp_live = p.R > 32 * warp;              // this warp has rows
