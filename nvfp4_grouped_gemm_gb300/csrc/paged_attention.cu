@@ -34,12 +34,12 @@ namespace moe {
 namespace {
 
 constexpr int kMaxGrid = 512;              // partial slots of the workspace
-constexpr int kMaxRows = 32;
+constexpr int kMaxRows = 48;
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
 // What a segment costs beside its steps (queries, first copies, the warps' rows meeting), in
 // steps: pieces of the line are equal with it counted.
-constexpr int kSegmentCost = 6;
+constexpr int kSegmentCost = 12;
 
 // Rows of a sequence (new tokens times query heads per key head) from which on it goes to the
 // tensor-memory form of prompt_attention.cu.
@@ -60,8 +60,8 @@ struct Shape {
   static constexpr int kRowB = D == 64 ? 64 : 128;       // bytes of a sub-tile row
   static constexpr int kPlaneB = kStep * D;              // a step's K (or V) bytes
   static constexpr int kStageB = 2 * kPlaneB;
-  static constexpr int kSlots = D == 64 ? 4 : NT == 4 ? 3 : 2;
-  static constexpr int kCtas = WARPS_ > 4 ? 1 : NT == 4 || (NT == 2 && D == 256) ? 2 : 3;   // per SM
+  static constexpr int kSlots = D == 64 ? 4 : NT > 2 ? 3 : 2;
+  static constexpr int kCtas = WARPS_ > 4 ? 1 : NT * D > 256 || NT > 3 ? 2 : 3;         // per SM
   static constexpr int kRows = 8 * NT;
   static constexpr int kRingB = kWarps * kSlots * kStageB;
   static constexpr int kMergeB = kWarps * kRows * D * 4; // aliases the ring
@@ -223,58 +223,53 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
     }
   }
 
-  // weights
-  uint32_t pb[NT][H][2];
+  // weights: s f + v - M, for all row tiles before one vote on whether M has to move
+  bool move = false;
+  float top[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float top[2] = {-INFINITY, -INFINITY};
-    float raw[H][4];
+    top[nt][0] = top[nt][1] = -INFINITY;
+    const float base[2] = {t.M[nt][0] == kNoMax ? 0.0f : t.M[nt][0], t.M[nt][1] == kNoMax ? 0.0f : t.M[nt][1]};
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        raw[h][x] = sc[nt][h][x];
         const int y = x & 1;
+        sc[nt][h][x] = fmaf(sc[nt][h][x], k.f[h] * t.rowf[nt][y], k.v[h] - base[y]);
         if (masked) {
           const int j = j0 + h * 16 + (x >> 1) * 8 + f.tau, pl = t.place[nt][y];
           const bool see = k.good[h] && j <= pl && j < len && (window == 0 || j > pl - window);
-          raw[h][x] = see ? raw[h][x] : __int_as_float(0x7fffffff);
-          sc[nt][h][x] = see ? fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - t.M[nt][y]) : -INFINITY;
-        } else {
-          sc[nt][h][x] = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - t.M[nt][y]);
+          if (!see) sc[nt][h][x] = -INFINITY;
         }
-        top[y] = fmaxf(top[y], sc[nt][h][x]);
+        top[nt][y] = fmaxf(top[nt][y], sc[nt][h][x]);
       }
-    if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > kLazy)) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      move |= top[nt][y] > (t.M[nt][y] == kNoMax ? -INFINITY : kLazy);
+  }
+  if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        // the maximum itself, from the scores: M may be far below it
-        float to = t.M[nt][y];
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int x = y; x < 4; x += 2) {
-            const float v = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h]);
-            if (!masked || sc[nt][h][x] > -INFINITY) to = fmaxf(to, v);
-          }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
-        const float keep = exp2_approx(t.M[nt][y] - to);
-        t.M[nt][y] = to;
+        for (int o = 4; o < 32; o <<= 1) top[nt][y] = fmaxf(top[nt][y], __shfl_xor_sync(0xffffffffu, top[nt][y], o));
+        const bool unset = t.M[nt][y] == kNoMax;           // no key of the row so far
+        const float up = unset ? (top[nt][y] > -INFINITY ? top[nt][y] : 0.0f) : fmaxf(top[nt][y], 0.0f);
+        const float keep = unset ? 0.0f : exp2_approx(-up);
+        if (!unset || top[nt][y] > -INFINITY) t.M[nt][y] = (unset ? 0.0f : t.M[nt][y]) + up;
         t.L[nt][y] *= keep;
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) t.O[nt][n][y] *= keep, t.O[nt][n][2 + y] *= keep;
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-          for (int x = y; x < 4; x += 2)
-            if (!masked || sc[nt][h][x] > -INFINITY) {
-              // scores so large that their rounding alone passes 2^8 end there (NaN stays)
-              const float v = fmaf(raw[h][x], k.f[h] * t.rowf[nt][y], k.v[h] - to);
-              sc[nt][h][x] = v > kLazy ? kLazy : v;
-            }
+          for (int x = y; x < 4; x += 2) sc[nt][h][x] -= up;
       }
-    }
+  }
+  uint32_t pb[NT][H][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
@@ -284,7 +279,6 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
       pb[nt][h][0] = transpose8(pack_f16(sc[nt][h][0], sc[nt][h][1]));
       pb[nt][h][1] = transpose8(pack_f16(sc[nt][h][2], sc[nt][h][3]));
     }
-  }
 
   // values
 #pragma unroll
@@ -491,43 +485,60 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       islot = islot + 1 == S::kSlots ? 0 : islot + 1;
       ++in_flight;
     };
-    for (int i = 0; i < min(count, S::kSlots); ++i) issue(i);
-
-    // ---- queries as B fragments: k-steps 2i and 2i+1 of row tile nt: lane 16 B ----
-    for (int r = warp; r < S::kRows; r += kWarps) {
-      constexpr int kQuads = (D / 4 + 31) / 32;
-      float v[kQuads][4];
-      float amax = 0.0f;
-      const int rr = block * S::kRows + r;
-      const uint16_t* src = a.q + (int64_t)(q.row0 + rr / group) * a.q_stride +
-                            (int64_t)(head * group + rr % group) * D;
+    // ---- queries as B fragments: k-steps 2i and 2i+1 of row tile nt: lane 16 B. The warp's rows
+    // come kAtOnce at a time, the first of them asked for before the keys' pages ----
+    constexpr int kQuads = (D / 4 + 31) / 32, kMine = (S::kRows + kWarps - 1) / kWarps;
+    constexpr int kAtOnce = kMine < 4 ? kMine : 4;
+    uint2 qv[kAtOnce][kQuads];
+    auto ask = [&](int i0) {
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const int u = lane + 32 * i;
-        uint2 w = make_uint2(0, 0);
-        if (r < R && u < D / 4) w = *reinterpret_cast<const uint2*>(src + 4 * u);
+      for (int n = 0; n < kAtOnce; ++n) {
+        const int r = warp + (i0 + n) * kWarps, rr = block * S::kRows + r;
+        const uint16_t* src = a.q + (int64_t)(q.row0 + rr / group) * a.q_stride +
+                              (int64_t)(head * group + rr % group) * D;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t bits = (x < 2 ? w.x : w.y) >> (16 * (x & 1)) & 0xffffu;
-          v[i][x] = bf16 ? act_to_f32<MOE_DTYPE_BF16>(bits) : act_to_f32<MOE_DTYPE_F16>(bits);
-          amax = fmaxf(amax, fabsf(v[i][x]));
+        for (int i = 0; i < kQuads; ++i) {
+          const int u = lane + 32 * i;
+          qv[n][i] = make_uint2(0, 0);
+          if (r < R && u < D / 4) qv[n][i] = *reinterpret_cast<const uint2*>(src + 4 * u);
         }
       }
+    };
+    ask(0);
+    for (int i = 0; i < min(count, S::kSlots); ++i) issue(i);
+#pragma unroll 1
+    for (int i0 = 0; i0 < kMine; i0 += kAtOnce) {
+      if (i0 > 0) ask(i0);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      // bf16 rows get the power of two that puts their largest magnitude below 2^15
-      const int e = bf16 && amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
-      const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
-      if (lane == 0) s_rowf[r] = pow2f(e);
+      for (int n = 0; n < kAtOnce; ++n) {
+        const int r = warp + (i0 + n) * kWarps;
+        if (r >= S::kRows) break;
+        float v[kQuads][4];
+        float amax = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const int u = lane + 32 * i;
-        if (u < D / 4) {
-          const int ks = (u >> 4) * 4 + (u & 3), cc = (u >> 2) & 3;
-          char* dst = s_q + ((ks >> 1) * NT + (r >> 3)) * 512 + ((r & 7) * 4 + cc) * 16 + (ks & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) =
-              make_uint2(pack_f16(v[i][0] * s1 * s2, v[i][1] * s1 * s2),
-                         pack_f16(v[i][2] * s1 * s2, v[i][3] * s1 * s2));
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t bits = (x < 2 ? qv[n][i].x : qv[n][i].y) >> (16 * (x & 1)) & 0xffffu;
+            v[i][x] = bf16 ? act_to_f32<MOE_DTYPE_BF16>(bits) : act_to_f32<MOE_DTYPE_F16>(bits);
+            amax = fmaxf(amax, fabsf(v[i][x]));
+          }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // bf16 rows get the power of two that puts their largest magnitude below 2^15
+        const int e = bf16 && amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
+        const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
+        if (lane == 0) s_rowf[r] = pow2f(e);
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const int u = lane + 32 * i;
+          if (u < D / 4) {
+            const int ks = (u >> 4) * 4 + (u & 3), cc = (u >> 2) & 3;
+            char* dst = s_q + ((ks >> 1) * NT + (r >> 3)) * 512 + ((r & 7) * 4 + cc) * 16 + (ks & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_f16(v[i][0] * s1 * s2, v[i][1] * s1 * s2),
+                           pack_f16(v[i][2] * s1 * s2, v[i][3] * s1 * s2));
+          }
         }
       }
     }
@@ -679,25 +690,38 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       // the last piece of the segment to arrive joins all of them
       const int c0 = (int)((seg_at + kSegmentCost) / per), c1 = (int)((seg_at + length - 1) / per);
       const int np = c1 - c0 + 1;
-      __threadfence();
-      __syncthreads();
+      __syncthreads();                         // the whole CTA's rows, then one thread's release
       if (tid == 0) {
-        const uint32_t before = atomicAdd(&counters[c0], 1u);
+        uint32_t before;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(&counters[c0]) : "memory");
         s_last = before == (uint32_t)(np - 1);
         if (s_last) counters[c0] = 0;
       }
       __syncthreads();
       if (s_last) {
-        __threadfence();
         // every piece's factor per row; the ring's memory holds them
         float* fac = reinterpret_cast<float*>(big);
         auto stat = [&](int p, int r) { return stats + (size_t)(2 * (c0 + p) + (p == 0)) * 2 * kMaxRows + r; };
-        for (int r = warp; r < R; r += kWarps) {
-          float top = kNoMax, sum = 0.0f;
-          for (int p = lane; p < np; p += 32) top = fmaxf(top, __ldcg(stat(p, r)));
+        float m[kMine], l[kMine];
+        // up to 32 pieces: a lane per piece, all the warp's rows in flight; more go round again
+#pragma unroll
+        for (int n = 0; n < kMine; ++n) {
+          const int r = warp + n * kWarps;
+          m[n] = kNoMax, l[n] = 0.0f;
+          if (r < R && lane < np) m[n] = __ldcg(stat(lane, r)), l[n] = __ldcg(stat(lane, r) + kMaxRows);
+        }
+#pragma unroll
+        for (int n = 0; n < kMine; ++n) {
+          const int r = warp + n * kWarps;
+          if (r >= R) break;
+          float top = m[n], sum;
+          for (int p = lane + 32; p < np; p += 32) top = fmaxf(top, __ldcg(stat(p, r)));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          for (int p = lane; p < np; p += 32) {
+          const float k0 = exp2_approx(m[n] - top);
+          sum = l[n] * k0;
+          if (lane < np) fac[lane * S::kRows + r] = k0;
+          for (int p = lane + 32; p < np; p += 32) {
             const float k = exp2_approx(__ldcg(stat(p, r)) - top);
             fac[p * S::kRows + r] = k;
             sum = fmaf(__ldcg(stat(p, r) + kMaxRows), k, sum);
@@ -707,19 +731,19 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
           if (lane == 0) s_m[0][r] = top, s_l[0][r] = sum;
         }
         __syncthreads();
+        constexpr size_t kSlot = (size_t)kMaxRows * D;
+        constexpr int kBatch = 16;             // loads in flight per thread
         for (int u = tid; u < R * (D / 4); u += kThreads) {
           const int r = u / (D / 4), d = (u % (D / 4)) * 4;
           const float* src = part + ((size_t)(2 * c0) * kMaxRows + r) * D + d;
-          constexpr size_t kSlot = (size_t)kMaxRows * D;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int kBatch = 8;
           for (int p0 = 0; p0 < np; p0 += kBatch) {
             float4 o[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
               const int p = p0 + i;
-              o[i] = p < np ? __ldcg(reinterpret_cast<const float4*>(src + (2 * p + (p == 0)) * kSlot))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+              o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p < np) o[i] = __ldcg(reinterpret_cast<const float4*>(src + (2 * p + (p == 0)) * kSlot));
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -760,14 +784,24 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
-  // Row tiles of a block: as many as hold the sequences' rows on average, so that one pass
-  // over the keys serves them (at most 32 rows; 16 where 256-value accumulators fill the
-  // registers).
+  // Row tiles of a block: as few as hold the sequences' rows on average in one pass over the keys,
+  // or in equal passes beyond the most whose accumulators fit in registers.
+  constexpr int kMost = D == 64 ? 6 : D == 128 ? 4 : 2;
   const long long rows = ((long long)a.T * (a.q_heads / a.c.kv_heads) + a.b.B - 1) / a.b.B;
+  const long long tiles = (rows + 7) / 8, passes = (tiles + kMost - 1) / kMost;
+  const int nt = (int)((tiles + passes - 1) / passes);
+  if constexpr (D == 64) {
+    if (nt == 5) return launch_shape<D, 5, 4>(a, s);
+    if (nt == 6) return launch_shape<D, 6, 4>(a, s);
+  }
+  if constexpr (D <= 128) {
+    if (nt == 3) return launch_shape<D, 3, 4>(a, s);
+    if (nt == 4) return launch_shape<D, 4, 4>(a, s);
+  }
+  if (nt == 2) return launch_shape<D, 2, 4>(a, s);
+  // Few segments: more warps per CTA, so that fewer partial rows have to be joined.
   const bool few = (long long)a.b.B * a.c.kv_heads <= num_sms();
-  if (rows <= 8) return few ? launch_shape<D, 1, D == 256 ? 8 : 12>(a, s) : launch_shape<D, 1, 4>(a, s);
-  if (rows <= 16 || D == 256) return launch_shape<D, 2, 4>(a, s);
-  return launch_shape<D, D == 256 ? 2 : 4, 4>(a, s);
+  return few ? launch_shape<D, 1, D == 256 ? 8 : 12>(a, s) : launch_shape<D, 1, 4>(a, s);
 }
 
 }  // namespace

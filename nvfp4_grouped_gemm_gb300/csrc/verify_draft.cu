@@ -37,9 +37,14 @@ __device__ __forceinline__ float prob(const void* row, int64_t at) {
   return act_to_f32<DT>(__ldg(static_cast<const uint16_t*>(row) + at));
 }
 
-// floor(min(w, 1) * 2^40); 0 for NaN and negative weights.
+// floor(min(w, 1) * 2^40); 0 for NaN and negative weights. On whole numbers: a conversion from
+// f32 to 64-bit integers runs on the double-precision pipe, a sixty-fourth of this one's rate.
 __device__ __forceinline__ unsigned long long mass_of(float w) {
-  return __float2ull_rz(fminf(fmaxf(w, 0.0f), 1.0f) * 1099511627776.0f);
+  const uint32_t bits = __float_as_uint(fminf(fmaxf(w, 0.0f), 1.0f));       // 0 <= w <= 1
+  // w = m * 2^(e - 150), m the mantissa with its leading bit (w = 0 and subnormals fall below)
+  const uint32_t down = 127u - (bits >> 23);                                // 0 .. 127
+  const unsigned long long m = (unsigned long long)((bits & 0x7fffffu) | 0x800000u) << 17;
+  return down < 64u ? m >> down : 0ull;
 }
 
 template <class T>
