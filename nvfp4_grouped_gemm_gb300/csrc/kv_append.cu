@@ -189,25 +189,50 @@ __device__ __forceinline__ void page_chunk(const KvAppendArgs& a, const Item& it
   }
 }
 
-template <int DT>
-__device__ void page_block(const KvAppendArgs& a, int it_index, int head, bool is_k) {
+// v / scale for E4M3: a power-of-two scale divides exactly like a product with its reciprocal.
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], float scale, float inv, bool pow2) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = pow2 ? __fmul_rn(v[i], inv) : __fdiv_rn(v[i], scale);
+  return make_uint2(f32x2_to_e4m3x2(q[0], q[1]) | (f32x2_to_e4m3x2(q[2], q[3]) << 16),
+                    f32x2_to_e4m3x2(q[4], q[5]) | (f32x2_to_e4m3x2(q[6], q[7]) << 16));
+}
+
+// KEEP: chunks per thread that stay in registers between the largest magnitude and the codes (a
+// page of up to KEEP * 256 chunks; larger ones are read and rotated twice).
+template <int DT, int KEEP>
+__device__ __forceinline__ void page_block(const KvAppendArgs& a, int it_index, int head, bool is_k) {
   __shared__ uint32_t s_peak;
   if (threadIdx.x == 0) s_peak = 0;
   const Item it = find_item(a, it_index);
   if (it.page < 0) return;                      // the same for the whole block
-  const int D = a.c.head_dim, P = a.c.page_size, per = D / 16;
-  const int rotary = is_k ? a.rotary : 0, inter = a.interleaved;
+  const int D = a.c.head_dim, P = a.c.page_size, per = D / 16, log_per = 31 - __clz(per);
+  const int rotary = is_k ? a.rotary : 0, inter = a.interleaved, count = it.rows * per;
   float* scale_at = (is_k ? a.c.k_scales : a.c.v_scales) + it.page * a.c.kv_heads + head;
   uint8_t* codes = (is_k ? a.c.k_codes : a.c.v_codes) + it.page * a.c.page_stride +
                    (int64_t)head * P * D;
   const float old = *scale_at;
+  const bool kept = count <= KEEP * kThreads;
+  float lo[KEEP][8], hi[KEEP][8];
   float peak = 0.0f;
-  for (int u = threadIdx.x; u < it.rows * per; u += kThreads) {
-    const Chunk c = chunk_at(u % per, rotary, inter);
-    float lo[8], hi[8];
-    page_chunk<DT>(a, it, head, is_k, u / per, c, lo, hi);
+  auto raise = [&](const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) peak = fmaxf(peak, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    for (int i = 0; i < 8; ++i) peak = fmaxf(peak, fmaxf(fabsf(x[i]), fabsf(y[i])));
+  };
+  if (kept) {
+#pragma unroll
+    for (int n = 0; n < KEEP; ++n) {
+      const int u = threadIdx.x + n * kThreads;
+      if (u < count) {
+        page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), rotary, inter), lo[n], hi[n]);
+        raise(lo[n], hi[n]);
+      }
+    }
+  } else {
+    for (int u = threadIdx.x; u < count; u += kThreads) {
+      page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), rotary, inter), lo[0], hi[0]);
+      raise(lo[0], hi[0]);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
@@ -231,22 +256,27 @@ __device__ void page_block(const KvAppendArgs& a, int it_index, int head, bool i
       *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  for (int u = threadIdx.x; u < it.rows * per; u += kThreads) {
-    const int tok = u / per;
-    const Chunk c = chunk_at(u % per, rotary, inter);
-    float lo[8], hi[8];
-    page_chunk<DT>(a, it, head, is_k, tok, c, lo, hi);
-    uint32_t w[4];
+  // 2^-126 .. 2^126: the reciprocal is a normal float too
+  const uint32_t bits = __float_as_uint(scale);
+  const bool pow2 = (bits & 0x807fffffu) == 0 && bits >= 0x00800000u && bits <= 0x7e800000u;
+  const float inv = pow2 ? __uint_as_float(0x7f000000u - bits) : 0.0f;
+  auto put = [&](int u, const float (&x)[8], const float (&y)[8]) {
+    const Chunk c = chunk_at(u & (per - 1), rotary, inter);
+    uint8_t* dst = codes + (int64_t)(it.slot0 + (u >> log_per)) * D;
+    *reinterpret_cast<uint2*>(dst + c.lo) = quant8(x, scale, inv, pow2);
+    *reinterpret_cast<uint2*>(dst + c.hi) = quant8(y, scale, inv, pow2);
+  };
+  if (kept) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i] = f32x2_to_e4m3x2(__fdiv_rn(lo[4 * i], scale), __fdiv_rn(lo[4 * i + 1], scale)) |
-             (f32x2_to_e4m3x2(__fdiv_rn(lo[4 * i + 2], scale), __fdiv_rn(lo[4 * i + 3], scale)) << 16);
-      w[2 + i] = f32x2_to_e4m3x2(__fdiv_rn(hi[4 * i], scale), __fdiv_rn(hi[4 * i + 1], scale)) |
-                 (f32x2_to_e4m3x2(__fdiv_rn(hi[4 * i + 2], scale), __fdiv_rn(hi[4 * i + 3], scale)) << 16);
+    for (int n = 0; n < KEEP; ++n) {
+      const int u = threadIdx.x + n * kThreads;
+      if (u < count) put(u, lo[n], hi[n]);
     }
-    uint8_t* dst = codes + (int64_t)(it.slot0 + tok) * D;
-    *reinterpret_cast<uint2*>(dst + c.lo) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(dst + c.hi) = make_uint2(w[2], w[3]);
+  } else {
+    for (int u = threadIdx.x; u < count; u += kThreads) {
+      page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), rotary, inter), lo[0], hi[0]);
+      put(u, lo[0], hi[0]);
+    }
   }
   if (threadIdx.x == 0) *scale_at = scale;
 }
@@ -264,37 +294,55 @@ __device__ __forceinline__ int sequence_of(const moe_seq_batch& b, int t) {
 
 template <int DT>
 __device__ void query_block(const KvAppendArgs& a, int block, int heads_per) {
-  const int D = a.c.head_dim, per = D / 16;
+  const int D = a.c.head_dim, per = D / 16, log_per = 31 - __clz(per);
   const int groups = (a.q_heads + heads_per - 1) / heads_per;
   const int64_t u = (int64_t)block * kThreads + threadIdx.x;
-  const int ch = (int)(u % per);
-  const int64_t tg = u / per;
-  const int g = (int)(tg % groups);
-  const int64_t t = tg / groups;
+  const int ch = (int)(u & (per - 1));
+  const int tg = (int)(u >> log_per);           // T * q_heads < 2^31 is checked by the host
+  const int g = tg % groups, t = tg / groups;
   if (t >= a.T) return;
   const Chunk c = chunk_at(ch, a.rotary, a.interleaved);
+  const int h0 = g * heads_per, h1 = min(a.q_heads, h0 + heads_per);
+  const uint16_t* src = a.q + (int64_t)t * a.q_stride;
+  uint16_t* dst = a.q_out + (int64_t)t * a.q_out_stride;
+  constexpr int kAhead = 4;                     // heads in flight
+  uint4 lo[kAhead], hi[kAhead];
+  auto ask = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (h + i < h1) {
+        lo[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(h + i) * D + c.lo);
+        hi[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(h + i) * D + c.hi);
+      }
+  };
+  ask(h0);
   Turn turn;
   if (c.col >= 0) {
     int pos;
     if (a.positions) {
       pos = a.positions[t];
     } else {
-      const int b = sequence_of(a.b, (int)t);
-      pos = a.b.seq_lens[b] - a.b.q_offsets[b + 1] + (int)t;
+      const int b = sequence_of(a.b, t);
+      pos = a.b.seq_lens[b] - a.b.q_offsets[b + 1] + t;
     }
     pos = clamp_position(pos, a.max_pos, a.err);
     load_turn(turn, a.cos, a.sin, (int64_t)pos * (a.rotary / 2) + c.col);
   }
-  const int h1 = min(a.q_heads, (g + 1) * heads_per);
-  for (int h = g * heads_per; h < h1; ++h) {
-    const uint16_t* src = a.q + t * a.q_stride + (int64_t)h * D;
-    uint16_t* dst = a.q_out + t * a.q_out_stride + (int64_t)h * D;
-    float lo[8], hi[8];
-    unpack8<DT>(*reinterpret_cast<const uint4*>(src + c.lo), lo);
-    unpack8<DT>(*reinterpret_cast<const uint4*>(src + c.hi), hi);
-    if (c.col >= 0) turn_chunk(lo, hi, turn, a.interleaved);
-    *reinterpret_cast<uint4*>(dst + c.lo) = pack8<DT>(lo);
-    *reinterpret_cast<uint4*>(dst + c.hi) = pack8<DT>(hi);
+  for (int h = h0; h < h1; h += kAhead) {
+    if (h > h0) ask(h);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (h + i < h1) {
+        if (c.col >= 0) {
+          float x[8], y[8];
+          unpack8<DT>(lo[i], x);
+          unpack8<DT>(hi[i], y);
+          turn_chunk(x, y, turn, a.interleaved);
+          lo[i] = pack8<DT>(x), hi[i] = pack8<DT>(y);
+        }
+        *reinterpret_cast<uint4*>(dst + (int64_t)(h + i) * D + c.lo) = lo[i];
+        *reinterpret_cast<uint4*>(dst + (int64_t)(h + i) * D + c.hi) = hi[i];
+      }
   }
 }
 
@@ -303,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
                                                             int heads_per) {
   if ((int)blockIdx.x < page_blocks) {
     const int plane = blockIdx.x % (2 * a.c.kv_heads);
-    page_block<DT>(a, blockIdx.x / (2 * a.c.kv_heads), plane >> 1, (plane & 1) == 0);
+    page_block<DT, 2>(a, blockIdx.x / (2 * a.c.kv_heads), plane >> 1, (plane & 1) == 0);
   } else {
     query_block<DT>(a, blockIdx.x - page_blocks, heads_per);
   }

@@ -34,7 +34,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxGrid = 512;              // partial slots of the workspace
-constexpr int kMaxRows = 48;
+constexpr int kMaxRows = 32;
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
 // What a segment costs beside its steps (queries, first copies, the warps' rows meeting), in
@@ -785,15 +785,12 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
 template <int D>
 cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
   // Row tiles of a block: as few as hold the sequences' rows on average in one pass over the keys,
-  // or in equal passes beyond the most whose accumulators fit in registers.
-  constexpr int kMost = D == 64 ? 6 : D == 128 ? 4 : 2;
+  // or in equal passes beyond four (five tiles of 64-value heads in one pass: fewer warps fit, and
+  // 16 sequences of 8 new tokens and 5 heads took 49.0 us against 45.5 in two passes of three).
+  constexpr int kMost = D == 256 ? 2 : 4;
   const long long rows = ((long long)a.T * (a.q_heads / a.c.kv_heads) + a.b.B - 1) / a.b.B;
   const long long tiles = (rows + 7) / 8, passes = (tiles + kMost - 1) / kMost;
   const int nt = (int)((tiles + passes - 1) / passes);
-  if constexpr (D == 64) {
-    if (nt == 5) return launch_shape<D, 5, 4>(a, s);
-    if (nt == 6) return launch_shape<D, 6, 4>(a, s);
-  }
   if constexpr (D <= 128) {
     if (nt == 3) return launch_shape<D, 3, 4>(a, s);
     if (nt == 4) return launch_shape<D, 4, 4>(a, s);

@@ -74,6 +74,7 @@ moe_status moe_kv_append_rope_e4m3(const moe_kv_cache* cache, const moe_seq_batc
     if (q_heads <= 0 || q_heads > 65536) return MOE_ERR_INVALID_ARG;
     if ((st = check_rows(q, q_stride, (int64_t)q_heads * D)) != MOE_OK) return st;
     if ((st = check_rows(q_out, q_out_stride, (int64_t)q_heads * D)) != MOE_OK) return st;
+    if ((int64_t)T * q_heads >= (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   }
   if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16 != 0) return MOE_ERR_INVALID_ARG;
   if (rotary_dim > 0 && (!cos || !sin || !aligned(cos, 16) || !aligned(sin, 16) || max_pos <= 0))

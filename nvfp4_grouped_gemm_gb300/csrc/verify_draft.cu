@@ -1,10 +1,10 @@
 // Verification of drafted tokens with given random numbers (moe_verify_draft).
 //
 // Bound by one row of the target's probabilities (and one of the draft's after a refusal) per
-// sequence. The row is cut into chunks, a block each, so that few sequences still fill the GPU.
+// sequence. The row is cut into chunks for several blocks, so that few sequences still fill the GPU.
 // Every block finds the row for itself (lane i of its first warp tests drafted tokens i and
-// 32 + i; the first refusal is the lowest bit of two ballots), sums the masses of its chunk and
-// leaves the sum in the workspace. The last block of a sequence to arrive finds the chunk that
+// 32 + i; the first refusal is the lowest bit of two ballots), sums the masses of its chunks and
+// leaves the sums in the workspace. The last block of a sequence to arrive finds the chunk that
 // holds the goal and walks that chunk alone (and in the rare case that nothing is left after a
 // refusal's difference, sums the row itself first). Masses are whole numbers and their sums wrap
 // nowhere (V <= 2^22 masses of at most 2^40), so neither the order of summation nor that of
@@ -17,14 +17,23 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Tokens per chunk: the least power of two from 1024 that leaves at most 16 blocks per SM of a
-// 152-SM GPU (smaller chunks shorten the walk of the last block, more blocks cost launches).
-constexpr int kBlocks = 16 * 152;
-constexpr int kMaxChunk = 8192;
-int chunk_tokens(int B, int V) {
-  int chunk = 1024;
-  while (chunk < kMaxChunk && (long long)B * ((V + chunk - 1) / chunk) > kBlocks) chunk *= 2;
-  return chunk;
+// The row is cut into chunks whose sums the last block chooses from, and a block takes `per` of them
+// in turn: 1024 tokens and one each while that leaves at most 8 blocks per SM of a 152-SM GPU,
+// else 2048 and as many as bring the grid down to that (the test of the drafts and the arrival
+// are then paid once for several chunks: 64 sequences of 151937 took 35.6 us with a block per
+// 4096 tokens, four waves of them).
+constexpr int kBlocks = 8 * 152;
+struct Cut {
+  int chunk, chunks, per;
+};
+Cut cut_of(int B, int V) {
+  Cut c = {1024, (V + 1023) / 1024, 1};
+  if ((long long)B * c.chunks > kBlocks) {
+    c.chunk = 2048;
+    c.chunks = (V + 2047) / 2048;
+    c.per = (int)(((long long)B * c.chunks + kBlocks - 1) / kBlocks);
+  }
+  return c;
 }
 
 // Workspace: error word, arrival counters of up to 2^16 sequences (their place does not depend
@@ -59,7 +68,7 @@ struct Row {
   int left_out;                    // a token without its unit of draft mass, or -1
 };
 template <int DT, int EACH>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, int chunks) {
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, int chunks, int per) {
   constexpr int kChunk = EACH * kThreads;
   constexpr int kBatch = EACH < 8 ? EACH : 8;    // loads in flight per thread (and row)
   __shared__ unsigned long long s_warp[kWarps];
@@ -152,19 +161,19 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
     return block_total(sum);
   };
 
-  // ---- this block's chunk ----
-  {
-    const unsigned long long sum = chunk_total(blockIdx.x);
-    if (tid == 0) {
-      sums[blockIdx.x] = sum;
-      __threadfence();
-      s_last = atomicAdd(&arrived[b], 1u) == (uint32_t)chunks - 1;
-      if (s_last) arrived[b] = 0;                // ready for the next call
-      s_token = -1;
-      s_chunk = -1;
-    }
-    __syncthreads();
+  // ---- this block's chunks ----
+  for (int x = blockIdx.x * per; x < min((int)(blockIdx.x + 1) * per, chunks); ++x) {
+    const unsigned long long sum = chunk_total(x);
+    if (tid == 0) sums[x] = sum;
   }
+  if (tid == 0) {
+    __threadfence();
+    s_last = atomicAdd(&arrived[b], 1u) == gridDim.x - 1;
+    if (s_last) arrived[b] = 0;                  // ready for the next call
+    s_token = -1;
+    s_chunk = -1;
+  }
+  __syncthreads();
   if (!s_last) return;
   __threadfence();
 
@@ -254,20 +263,18 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
 
 template <int DT>
 cudaError_t launch_chunk(const VerifyArgs& a, cudaStream_t s) {
-  const int chunk = chunk_tokens(a.B, a.V), chunks = (a.V + chunk - 1) / chunk;
-  const dim3 grid(chunks, a.B);
-  if (chunk == 1024) verify_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a, chunks);
-  else if (chunk == 2048) verify_kernel<DT, 8><<<grid, kThreads, 0, s>>>(a, chunks);
-  else if (chunk == 4096) verify_kernel<DT, 16><<<grid, kThreads, 0, s>>>(a, chunks);
-  else verify_kernel<DT, 32><<<grid, kThreads, 0, s>>>(a, chunks);
+  const Cut c = cut_of(a.B, a.V);
+  const dim3 grid((c.chunks + c.per - 1) / c.per, a.B);
+  if (c.chunk == 1024) verify_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a, c.chunks, c.per);
+  else verify_kernel<DT, 8><<<grid, kThreads, 0, s>>>(a, c.chunks, c.per);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t verify_ws_bytes(int B, int V) {
-  // enough for any smaller B and V: with chunks below the largest there are at most kBlocks
-  const size_t most = (size_t)B * ((V + kMaxChunk - 1) / kMaxChunk);
+  // enough for any smaller B and V: with the smaller chunks there are at most kBlocks
+  const size_t most = (size_t)B * ((V + 2047) / 2048);
   return align_up(kSumsAt + (most > kBlocks ? most : kBlocks) * 8);
 }
 
