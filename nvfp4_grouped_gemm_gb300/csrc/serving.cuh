@@ -45,14 +45,14 @@ cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, cudaSt
 struct LinearArgs {
   const uint16_t* x;
   int64_t x_stride, y_stride;
-  int T, N, K;
+  int T, N, K, x_dtype, y_dtype;
   const uint8_t *codes, *scales;
   const float* alpha;
   void* y;
   char* ws;
 };
 size_t linear_ws_bytes(int T, int N, int K);
-cudaError_t launch_linear(const LinearArgs& a, int x_dtype, int y_dtype, cudaStream_t s);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 
 struct VerifyArgs {
   const int32_t *draft_ids, *n_draft;

@@ -173,12 +173,14 @@ moe_status moe_linear_nvfp4(const void* x, int64_t x_stride, int32_t x_dtype, in
   a.T = T;
   a.N = w->rows;
   a.K = w->in_f;
+  a.x_dtype = x_dtype;
+  a.y_dtype = y_dtype;
   a.codes = w->codes;
   a.scales = w->scales;
   a.alpha = w->alpha;
   a.y = y;
   a.ws = static_cast<char*>(ws);
-  return from_cuda(launch_linear(a, x_dtype, y_dtype, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_linear(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_verify_workspace_bytes(int32_t B, int32_t V) {
