@@ -44,6 +44,7 @@ constexpr int kSegmentCost = 12;
 // Rows of a sequence (new tokens times query heads per key head) from which on it goes to the
 // tensor-memory form of prompt_attention.cu.
 constexpr int kPromptRows = 48;
+constexpr int kAllRows = 0x7fffffff;
 
 // Workspace: error word; arrival counters [kMaxGrid]; partial maxima and sums
 // [2 * kMaxGrid][2][kMaxRows]; partial rows f32 [2 * kMaxGrid][kMaxRows][D].
@@ -358,7 +359,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   long long per = (total + gridDim.x - 1) / gridDim.x;
   if (per < kWarps + kSegmentCost) per = kWarps + kSegmentCost;
   const long long begin = per * blockIdx.x, end = min(begin + per, total);
-  if (begin >= end) return;
+  if (begin >= end) {
+    pdl_wait();
+    return;
+  }
   if (a.b.B <= kThreads) {
     if (mine > 0 && at <= begin && begin < at + mine) s_seq = tid, s_first = at;
   } else {
@@ -619,7 +623,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         }
       }
     __syncthreads();                           // also: every warp is done with the ring
-    if (s_abort) return;                       // the same for the whole block
+    if (s_abort) break;                        // the same for the whole block
     float* merge = reinterpret_cast<float*>(big);
     // 16-byte units of a row are permuted so that a quarter warp's stores differ in bank
     auto unit_of = [](int r, int d) {
@@ -760,6 +764,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
   }
+  // Where the other form runs before this one, this one may start beside it: what follows both
+  // then waits for both.
+  pdl_wait();
 }
 
 template <int D, int NT, int WARPS>
@@ -778,6 +785,7 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   int grid = num_sms() * S::kCtas;
   if (grid > kMaxGrid) grid = kMaxGrid;
+  if (a.max_rows != kAllRows) return launch_pdl(kern, dim3(grid), dim3(S::kThreads), S::kSmem, s, a, map[0], map[1]);
   kern<<<grid, S::kThreads, S::kSmem, s>>>(a, map[0], map[1]);
   return cudaGetLastError();
 }
@@ -803,19 +811,23 @@ cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+size_t few_rows_ws_bytes(int head_dim) {
+  return align_up(kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4);
+}
+}  // namespace
+
 size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim) {
-  const size_t few = kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4;
-  const size_t many = head_dim <= 128 ? prompt_attention_ws_bytes(head_dim) : 0;
-  return align_up(few > many ? few : many);
+  return few_rows_ws_bytes(head_dim) + (head_dim <= 128 ? prompt_attention_ws_bytes(head_dim) : 0);
 }
 
 cudaError_t launch_attention(const AttentionArgs& args, cudaStream_t s) {
   AttentionArgs a = args;
-  a.max_rows = 0x7fffffff;
+  a.max_rows = kAllRows;
   if (a.c.head_dim <= 128 && a.T > a.b.B && (long long)a.T * (a.q_heads / a.c.kv_heads) >= kPromptRows) {
     // some sequence may have that many rows; which ones have is settled on the GPU
     const bool all = a.b.B == 1;
-    const cudaError_t e = launch_prompt_attention(a, all ? 1 : kPromptRows, s);
+    const cudaError_t e = launch_prompt_attention(a, all ? 1 : kPromptRows, few_rows_ws_bytes(a.c.head_dim), s);
     if (e != cudaSuccess || all) return e;
     a.max_rows = kPromptRows - 1;
   }

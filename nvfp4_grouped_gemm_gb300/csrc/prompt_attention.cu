@@ -47,9 +47,8 @@ constexpr float kLazy = 8.0f;
 // A segment's fixed cost (queries, first tiles, storing rows) in key tiles.
 constexpr int kSegmentCost = 3;
 
-// Workspace: arrival counters and partials follow those of the other form's header; rows are
-// stored [D/4][256][4].
-constexpr size_t kCountersAt = kAlign;
+// Workspace, from the end of the other form's: arrival counters, maxima and sums, rows [D/4][256][4].
+constexpr size_t kCountersAt = 0;
 constexpr size_t kStatsAt = kCountersAt + kPromptMaxGrid * 4;
 constexpr size_t kRowsAt = kStatsAt + (size_t)2 * kPromptMaxGrid * 2 * kBlock * 4;
 
@@ -255,7 +254,7 @@ struct Smem {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
+prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   using S = Smem<D>;
   extern __shared__ char smem_raw[];
   __shared__ uint64_t s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2], s_sfull[2], s_pfull[2], s_qfull[2], s_drain, s_join;
@@ -271,6 +270,9 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
   const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size;
   uint32_t* err = reinterpret_cast<uint32_t*>(a.ws);
   volatile int* abort_flag = &s_abort;
+  // With the other form behind it, which waits for this one at its end, that may start beside it;
+  // alone it must not let a successor start on unfinished rows.
+  if (min_rows > 1) pdl_trigger();
 
   // ---- this CTA's piece of the line (before any tensor memory is taken) ----
   auto scan = [&](long long v, long long* before) {
@@ -518,9 +520,9 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
     const int r = tid;                                     // row of the block
     const bool bf16 = a.dtype == MOE_DTYPE_BF16;
     const int log_p = 31 - __clz(P);
-    uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kCountersAt);
-    float* stats = reinterpret_cast<float*>(a.ws + kStatsAt);
-    float4* part = reinterpret_cast<float4*>(a.ws + kRowsAt);
+    uint32_t* counters = reinterpret_cast<uint32_t*>(ws + kCountersAt);
+    float* stats = reinterpret_cast<float*>(ws + kStatsAt);
+    float4* part = reinterpret_cast<float4*>(ws + kRowsAt);
     uint32_t sph = 0, jph = 0;
     bool ok = true;
     // the softmax threads meet (bounded, like every wait here)
@@ -779,23 +781,24 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows) {
 }
 
 template <int D>
-cudaError_t launch_prompt(const AttentionArgs& a, int min_rows, cudaStream_t s) {
+cudaError_t launch_prompt(const AttentionArgs& a, int min_rows, char* ws, cudaStream_t s) {
   constexpr int smem = 1024 + Smem<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = num_sms() < kPromptMaxGrid ? num_sms() : kPromptMaxGrid;
-  prompt_kernel<D><<<grid, kThreads, smem, s>>>(a, min_rows);
+  prompt_kernel<D><<<grid, kThreads, smem, s>>>(a, min_rows, ws);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t prompt_attention_ws_bytes(int head_dim) {
-  return kRowsAt + (size_t)2 * kPromptMaxGrid * kBlock * head_dim * 4;
+  return align_up(kRowsAt + (size_t)2 * kPromptMaxGrid * kBlock * head_dim * 4);
 }
 
-cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, cudaStream_t s) {
-  return a.c.head_dim == 64 ? launch_prompt<64>(a, min_rows, s) : launch_prompt<128>(a, min_rows, s);
+cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, size_t ws_at, cudaStream_t s) {
+  char* ws = a.ws + ws_at;
+  return a.c.head_dim == 64 ? launch_prompt<64>(a, min_rows, ws, s) : launch_prompt<128>(a, min_rows, ws, s);
 }
 
 }  // namespace moe

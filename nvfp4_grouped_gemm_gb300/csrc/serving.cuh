@@ -37,10 +37,10 @@ size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
 
 // The form for sequences of at least min_rows rows (new tokens times query heads per key head);
-// head_dim 64 or 128.
+// head_dim 64 or 128. Its workspace begins ws_at bytes into a.ws.
 constexpr int kPromptMaxGrid = 160;
 size_t prompt_attention_ws_bytes(int head_dim);
-cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, cudaStream_t s);
+cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, size_t ws_at, cudaStream_t s);
 
 struct LinearArgs {
   const uint16_t* x;

@@ -207,3 +207,77 @@ def test_repeated_calls_graph_replays_and_another_stream_agree():
     d, ld, _ = run(q, cache, dev, 16, 128, 0.09)
     assert torch.equal(d, out) and torch.equal(ld, lse)
     assert moe.get_device_error(ws) == 0
+
+
+# ---- sequences of many rows (the tensor-memory form), alone and beside short ones ----
+@pytest.mark.parametrize("D,page,heads,group,dtype,pairs", [
+    (128, 64, 1, 4, "bf16", [(5000, 70), (0, 300)]),
+    (64, 32, 2, 4, "f16", [(0, 512), (1000, 12), (3, 1)]),
+    (128, 16, 2, 1, "bf16", [(129, 257), (40, 2), (0, 48), (0, 47)]),
+    (128, 128, 1, 3, "f16", [(255, 171)]),
+    (64, 16, 1, 16, "bf16", [(2000, 3), (2000, 8), (0, 33)]),
+    (128, 64, 3, 8, "bf16", [(64, 6), (1000, 6), (0, 6), (127, 7)])])
+def test_many_rows_per_sequence(D, page, heads, group, dtype, pairs):
+    check(np.random.default_rng(D + group), pairs, page, heads, group, D, dtype)
+
+
+def test_many_rows_that_see_nothing():
+    rng = np.random.default_rng(31)
+
+    def edit(b):
+        b.lens[0], b.lens[2] = 20, 0
+    check(rng, [(0, 90), (30, 80), (0, 70)], 16, 1, 2, 64, "bf16", edit=edit, err=moe.DEVERR_PAGE)
+
+
+def test_many_rows_over_bad_pages_far_scales_and_sharp_scores():
+    rng = np.random.default_rng(32)
+
+    def edit(b):
+        b.table[0, 1], b.table[0, 9] = -1, b.num_pages
+    check(rng, [(100, 80)], 16, 2, 2, 128, "bf16", edit=edit, err=moe.DEVERR_PAGE)
+
+    def planes(batch):
+        p = list(cache_planes(rng, batch.num_pages, 1, 16, 64))
+        p[3] = (2.0 ** rng.integers(-40, 41, p[3].shape)).astype(np.float32)
+        p[2][::3] = 0
+        p[3][::3] = np.float32(2.0 ** -64)
+        return tuple(p)
+    check(rng, [(300, 100)], 16, 1, 3, 64, "bf16", planes=planes)
+    check(rng, [(300, 100)], 64, 1, 2, 128, "bf16", amp=40.0)
+    check(rng, [(300, 100)], 64, 1, 2, 128, "f16", amp=0.0)
+    check(rng, [(90, 60)], 16, 1, 2, 64, "bf16", amp=1e20, scale=1e-21)
+
+
+def test_many_rows_repeat_bit_for_bit_and_in_graphs():
+    rng = np.random.default_rng(33)
+    batch = Batch(rng, [(700, 200), (90, 1), (0, 400)], 64)
+    cache = device_cache(cache_planes(rng, batch.num_pages, 2, 64, 128))
+    dev = batch.device()
+    q = activations(rng, (batch.T, 8, 128), "bf16").cuda()
+    a, la, ws = run(q, cache, dev, 8, 128, 0.09)
+    for _ in range(3):
+        b, lb, _ = run(q, cache, dev, 8, 128, 0.09, ws=ws)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    out, lse = torch.empty_like(a), torch.empty_like(la)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_attention_paged_e4m3(q, cache, dev, out, ws, scale=0.09, lse=lse)
+    for _ in range(2):
+        graph.replay()
+        assert torch.equal(a, out) and torch.equal(la, lse)
+    assert moe.get_device_error(ws) == 0
+
+
+def test_nan_and_infinite_queries_stay_in_their_rows():
+    rng = np.random.default_rng(34)
+    for pairs in ([(100, 1), (40, 1)], [(100, 60), (40, 1)]):
+        batch = Batch(rng, pairs, 16)
+        cache = device_cache(cache_planes(rng, batch.num_pages, 1, 16, 64))
+        q = activations(rng, (batch.T, 2, 64), "bf16")
+        a, la, _ = run(q.cuda(), cache, batch.device(), 2, 64, 0.1)
+        q[0, 1, 3] = float("nan")
+        b, lb, _ = run(q.cuda(), cache, batch.device(), 2, 64, 0.1)
+        assert torch.isnan(b[0, 1]).all() and torch.isnan(lb[0, 1])
+        keep = torch.ones(batch.T, 2, dtype=torch.bool)
+        keep[0, 1] = False
+        assert torch.equal(a[keep.cuda()], b[keep.cuda()]) and torch.equal(la[keep.cuda()], lb[keep.cuda()])
