@@ -122,6 +122,7 @@ __device__ __forceinline__ float max16(const float* s) {
 }
 // Scores of 32 keys: those outside [x0, x1), and of a group of 16 without a page, become -inf.
 __device__ __forceinline__ void hide(float (&s)[32], int x0, int x1, bool there0, bool there1) {
+  asm volatile("" ::: "memory");               // a real branch: not selects on every tile
 #pragma unroll
   for (int x = 0; x < 32; ++x)
     if (x < x0 || x >= x1 || !(x < 16 ? there0 : there1)) s[x] = -INFINITY;
@@ -149,10 +150,51 @@ __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Waits as mbar_wait's, for a hand-off that is usually short: the clock is not read before the wait
+// has been long, and a warp's lanes all ask, so that none has to be told.
+__device__ __forceinline__ bool long_wait(uint32_t tries, uint64_t& since, volatile int* abort_flag, uint32_t* err) {
+  if (*abort_flag) return false;
+  const uint64_t now = global_ns();
+  if (tries == 64) since = now;
+  if (now - since <= kWaitBudgetNs) return true;
+  *abort_flag = 1;
+  atomicOr(err, (uint32_t)MOE_DEVERR_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  uint64_t since = 0;
+  for (uint32_t tries = 1; !mbar_try(bar, parity); ++tries)
+    if ((tries & 63) == 0 && !long_wait(tries, since, abort_flag, err)) return false;
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  uint64_t since = 0;
+  for (uint32_t tries = 1; !__all_sync(0xffffffffu, mbar_try(bar, parity)); ++tries)
+    if ((tries & 63) == 0 && !__all_sync(0xffffffffu, long_wait(tries, since, abort_flag, err))) return false;
+  return true;
+}
+
 // One arrival for the warp, after what all its lanes did before.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Loads that stay where they are written: the compiler may move an ordinary load behind a wait, next
+// to its use, and expose its latency there.
+__device__ __forceinline__ uint4 load_ahead(const void* at, bool there) {   // zeros if not there
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at), "r"((int)there) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load_ahead(const void* at, bool there, uint32_t other) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+               : "=r"(v) : "l"(at), "r"((int)there), "r"(other) : "memory");
+  return v;
 }
 
 // A sequence's rows and its share of the line.
@@ -386,35 +428,26 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         const int nt = p.t1 - p.t0;
         if (nt <= 0) continue;
         const int tiles = p.R > 128 ? 2 : 1;
-        for (int i = 0; i < tiles && ok; ++i) ok = mbar_wait(&s_qfull[i], (qph >> i) & 1, abort_flag, err);
+        for (int i = 0; i < tiles && ok; ++i) ok = wait_thread(&s_qfull[i], (qph >> i) & 1, abort_flag, err);
         qph ^= tiles == 2 ? 3u : 1u;
-        if (ok) ok = mbar_wait(&s_kfull[kv & 1], (kv >> 1) & 1, abort_flag, err);
+        if (ok) ok = wait_thread(&s_kfull[kv & 1], (kv >> 1) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
         for (int i = 0; i < tiles; ++i) {
           scores(i, kv);
           tc_commit(&s_sfull[i]);
         }
-        tc_commit(&s_kempty[kv & 1]);
         for (int t = 0; t < nt && ok; ++t, ++kv) {
-          if (!(ok = mbar_wait(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
           const bool more = t + 1 < nt;
 #pragma unroll 1
           for (int i = 0; i < tiles; ++i) {
-            // K of the next tile first: usually long there, and the products below then follow
-            // each other without a check between them
-            if (more && i == 0 &&
-                !(ok = mbar_wait(&s_kfull[(kv + 1) & 1], ((kv + 1) >> 1) & 1, abort_flag, err))) break;
-            if (!(ok = mbar_wait(&s_pfull[i], (pph >> i) & 1, abort_flag, err))) break;
+            // the weights, and with tile A's V and the next K: its softmax warps have seen them
+            if (!(ok = wait_thread(&s_pfull[i], (pph >> i) & 1, abort_flag, err))) break;
             pph ^= 1u << i;
             tc_fence_after();
             values(i, kv, t > 0);
             if (more) scores(i, kv + 1);
             tc_commit(&s_sfull[i]);                        // S of the next tile, or the final O
-            if (i == tiles - 1) {
-              tc_commit(&s_vempty[kv & 1]);
-              if (more) tc_commit(&s_kempty[(kv + 1) & 1]);
-            }
           }
         }
       }
@@ -446,7 +479,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       // lane l holds where 16-key group l % 8 of a tile starts in either plane (-1: nowhere)
       auto page_of = [&](int t) {
         const int j = t * kTile + (lane & 7) * 16;
-        return t < p.t1 && j < p.len ? __ldg(table + (j >> log_p)) : INT_MIN;
+        return (int)load_ahead(table + (j >> log_p), t < p.t1 && j < p.len, (uint32_t)INT_MIN);
       };
       auto start_of = [&](int t, int page) {
         const int j = t * kTile + (lane & 7) * 16;
@@ -464,8 +497,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         for (int i = 0; i < kHalfN; ++i) {
           const int at_ = tok0 + i * kStride;
           const int64_t from = __shfl_sync(0xffffffffu, start, (tok + at_) >> 4);
-          r[i] = make_uint4(0, 0, 0, 0);
-          if (from >= 0 && at_ < there) r[i] = __ldg(reinterpret_cast<const uint4*>(plane + from + thread_at));
+          r[i] = load_ahead(plane + from + thread_at, from >= 0 && at_ < there);
         }
       };
       uint4 r[4][kHalfN];                      // the four halves; never copied while a load is out
@@ -489,7 +521,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
             if (t + 1 < p.t1) fetch(t + 1, h - 1, r[h - 1]);
           }
           if ((h & 1) == 0 && ok)
-            ok = mbar_wait_warp(h ? &s_vempty[kv & 1] : &s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err);
+            ok = wait_warp(h ? &s_vempty[kv & 1] : &s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err);
           if (!ok) break;
           char* dst = smem + (h & 2 ? S::kVAt : S::kKAt) + (kv & 1) * S::kKv + (piece >> 2) * S::kHalf;
 #pragma unroll
@@ -523,12 +555,12 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
     uint32_t* counters = reinterpret_cast<uint32_t*>(ws + kCountersAt);
     float* stats = reinterpret_cast<float*>(ws + kStatsAt);
     float4* part = reinterpret_cast<float4*>(ws + kRowsAt);
-    uint32_t sph = 0, jph = 0;
+    uint32_t sph = 0, jph = 0, kv = 0;         // phases; key tiles
     bool ok = true;
     // the softmax threads meet (bounded, like every wait here)
     auto meet = [&] {
       warp_arrive(&s_join);
-      return mbar_wait_warp(&s_join, jph++ & 1, abort_flag, err);
+      return wait_warp(&s_join, jph++ & 1, abort_flag, err);
     };
     while (next_piece()) {
       const Piece p = s_piece[warp];           // in registers
@@ -540,6 +572,10 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       const int64_t row = p.row0 + rr / group;
       const int hq = p.head * group + rr % group;
       float M = kNoMax, L = 0.0f, rowf = 1.0f;
+      // The issuing thread's waits and commits are the block's bottleneck: what these warps can wait
+      // for and signal in its place they do. The last row tile's products come last, so its S tells
+      // that K and the V before it are read.
+      const bool frees = warp == (p.R > 128 ? 4 : 0) && lane == 0;
       if (live && nt > 0) {
         // the row as f16 times a power of two, K-major, 128-byte swizzle
         const uint16_t* src = a.q + row * a.q_stride + (int64_t)hq * D;
@@ -578,33 +614,41 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
         auto page_of = [&](int t) {
           const int j = t * kTile + (lane & 7) * 16;
-          const int page = t < p.t1 && j < p.len ? __ldg(table + (j >> log_p)) : -1;
-          return page < a.c.num_pages ? page : -1;
+          return (int)load_ahead(table + (j >> log_p), t < p.t1 && j < p.len, 0xffffffffu);
         };
-        auto coef_of = [&](int page) {
-          float4 c = make_float4(1.f, 0.f, 0.f, 0.f);      // no page: weights of -inf
-          if (page >= 0) {
-            const int64_t sc = (int64_t)page * heads + p.head;
-            const float vs = fminf(fmaxf(__ldg(a.c.v_scales + sc), 0x1p-100f), 0x1p120f);
-            c = make_float4(a.scale * 1.4426950408889634f * __ldg(a.c.k_scales + sc), log2f(vs),
-                            __fdividef(1.0f, vs), 1.0f);
-          }
-          return c;
+        // a tile's pages are read two tiles ahead, its scales one
+        struct Scales { float k, v; };
+        auto scales_of = [&](int page) {
+          const bool there = page >= 0 && page < a.c.num_pages;
+          const int64_t sc = (int64_t)page * heads + p.head;
+          return Scales{__uint_as_float(load_ahead(a.c.k_scales + sc, there, 0u)),
+                        __uint_as_float(load_ahead(a.c.v_scales + sc, there, 0u))};
         };
-        float4 coef = coef_of(page_of(p.t0));
-        int page_next = page_of(p.t0 + 1);
+        int page = page_of(p.t0), page_next = page_of(p.t0 + 1);
+        Scales scales = scales_of(page);
         const int place_lo = p.start + p.block * kBlock / group;             // the block's first and last rows
         const int place_hi = p.start + (p.block * kBlock + p.R - 1) / group;
         for (int t = p.t0; t < p.t1; ++t) {
+          const bool there = page >= 0 && page < a.c.num_pages;
           __syncwarp();
-          if (lane < 8) s_coef[warp][lane] = coef;
+          if (lane < 8) {
+            const float vs = fminf(fmaxf(scales.v, 0x1p-100f), 0x1p120f);
+            s_coef[warp][lane] = there ? make_float4(a.scale * 1.4426950408889634f * scales.k, log2f(vs),
+                                                     __fdividef(1.0f, vs), 1.0f)
+                                       : make_float4(1.f, 0.f, 0.f, 0.f);   // no page: weights of -inf
+          }
           __syncwarp();
-          const bool gone = !__all_sync(0xffffffffu, coef.w > 0.0f);
-          coef = coef_of(page_next);
+          const bool gone = !__all_sync(0xffffffffu, there);
+          page = page_next;
+          scales = scales_of(page);
           page_next = page_of(t + 2);
-          if (!(ok = mbar_wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) break;
+          if (!(ok = wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) break;
           ++sph;
           tc_fence_after();
+          if (frees) {
+            mbar_arrive(&s_kempty[kv & 1]);
+            if (t > p.t0) mbar_arrive(&s_vempty[~kv & 1]);
+          }
           if (warp_live) {
             const int j0 = t * kTile;
             bool masked = gone || j0 + kTile > place_lo + 1 || j0 + kTile > p.len;
@@ -612,77 +656,122 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
             // keys j0 + x with x in [x0, x1) are the row's; groups without a page are nobody's
             const int x1 = min(place + 1, p.len) - j0;
             const int x0 = a.window > 0 ? place - a.window + 1 - j0 : -j0;
-            // the largest s f + v of the row in this tile (f > 0: from each group's largest s)
-            float top = kNoMax;
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              float s[32];
-              tmem_ld32(s_col + ch * 32, s);
-              const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
-              if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
-              top = fmaxf(top, fmaf(max16(s), c0.x * rowf, c0.y));
-              top = fmaxf(top, fmaf(max16(s + 16), c1.x * rowf, c1.y));
-            }
-            if (__any_sync(0xffffffffu, top > M + kLazy)) {
-              const float to = fmaxf(M, top), keep = exp2_approx(M - to);
-              M = to;
-              L *= keep;
-              if (t > p.t0) {
-#pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
-                  float o[16];
-                  tmem_ld16(o_col + i * 16, o);
+            // The weights are taken with the M that there is, from one reading of S, and stand if none
+            // passes 2^8. Tiles where that is not to be expected, or with hidden keys, take two.
+            bool twice = masked || t == p.t0 || __any_sync(0xffffffffu, fabsf(M) > 1e6f);
+            if (!twice) {
+              uint32_t w[64];
+              float most = -INFINITY, sum = L;
 #pragma unroll
-                  for (int x = 0; x < 16; ++x) o[x] *= keep;
-                  tc_st16(o_col + i * 16, *reinterpret_cast<const uint32_t(*)[16]>(o));
+              for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                tmem_ld32(s_col + ch * 32, s);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float4 c = s_coef[warp][2 * ch + h];
+                  const float f = c.x * rowf, d = c.y - M;
+                  const uint64_t ff = pair(f, f), dd = pair(d, d);
+                  uint64_t acc = 0;
+#pragma unroll
+                  for (int x = 0; x < 16; x += 2) {
+                    float e0, e1;
+                    unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
+                    most = max3(most, e0, e1);
+                    e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+                    acc = add2(acc, pair(e0, e1));
+                    w[ch * 16 + h * 8 + x / 2] = pack_f16(e0, e1);
+                  }
+                  float l0, l1;
+                  unpair(acc, l0, l1);
+                  sum = fmaf(c.z, l0 + l1, sum);
                 }
+              }
+              twice = __any_sync(0xffffffffu, most > kLazy);
+              if (!twice) {
+                L = sum;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) tc_st16(s_col + ch * 16, *reinterpret_cast<const uint32_t(*)[16]>(w + ch * 16));
               }
             }
-            // scores so large that their rounding alone could pass 2^8 end there
-            const bool huge = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax);
-            // weights; columns 16 ch .. of P lie over columns of S that are already read
+            if (__builtin_expect(twice, 0)) {
+              // the largest s f + v of the row in this tile (f > 0: from each group's largest s)
+              float top = kNoMax;
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              float s[32];
-              uint32_t w[16];
-              tmem_ld32(s_col + ch * 32, s);
-              const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
-              if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
-              if (huge) {
+              for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                tmem_ld32(s_col + ch * 32, s);
+                const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
+                if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+                top = fmaxf(top, fmaf(max16(s), c0.x * rowf, c0.y));
+                top = fmaxf(top, fmaf(max16(s + 16), c1.x * rowf, c1.y));
+              }
+              if (__any_sync(0xffffffffu, top > M + kLazy)) {
+                const float to = fmaxf(M, top), keep = exp2_approx(M - to);
+                M = to;
+                L *= keep;
+                if (t > p.t0) {
+#pragma unroll 1
+                  for (int i = 0; i < D / 16; ++i) {
+                    float o[16];
+                    tmem_ld16(o_col + i * 16, o);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                  const float most = (M + kLazy - (x < 16 ? c0.y : c1.y)) / ((x < 16 ? c0.x : c1.x) * rowf);
-                  s[x] = s[x] > most ? most : s[x];
+                    for (int x = 0; x < 16; ++x) o[x] *= keep;
+                    tc_st16(o_col + i * 16, *reinterpret_cast<const uint32_t(*)[16]>(o));
+                  }
                 }
               }
+              // scores so large that their rounding alone could pass 2^8 end there
+              const bool huge = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax);
+              // weights; columns 16 ch .. of P lie over columns of S that are already read
+#pragma unroll 1
+              for (int ch = 0; ch < 4; ++ch) {
+                float s[32];
+                uint32_t w[16];
+                tmem_ld32(s_col + ch * 32, s);
+                const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
+                if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+                if (huge) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
-                const uint64_t ff = pair(f, f), dd = pair(d, d);
-                uint64_t acc = 0;
-#pragma unroll
-                for (int x = 0; x < 16; x += 2) {
-                  float e0, e1;
-                  unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
-                  e0 = exp2_approx(e0), e1 = exp2_approx(e1);
-                  acc = add2(acc, pair(e0, e1));
-                  w[h * 8 + x / 2] = pack_f16(e0, e1);
+                  for (int x = 0; x < 32; ++x) {
+                    const float most = (M + kLazy - (x < 16 ? c0.y : c1.y)) / ((x < 16 ? c0.x : c1.x) * rowf);
+                    s[x] = s[x] > most ? most : s[x];
+                  }
                 }
-                float l0, l1;
-                unpair(acc, l0, l1);
-                L = fmaf(h ? c1.z : c0.z, l0 + l1, L);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
+                  const uint64_t ff = pair(f, f), dd = pair(d, d);
+                  uint64_t acc = 0;
+#pragma unroll
+                  for (int x = 0; x < 16; x += 2) {
+                    float e0, e1;
+                    unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
+                    e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+                    acc = add2(acc, pair(e0, e1));
+                    w[h * 8 + x / 2] = pack_f16(e0, e1);
+                  }
+                  float l0, l1;
+                  unpair(acc, l0, l1);
+                  L = fmaf(h ? c1.z : c0.z, l0 + l1, L);
+                }
+                tc_st16(s_col + ch * 16, w);
               }
-              tc_st16(s_col + ch * 16, w);
             }
             tmem_wait_st();
           }
+          if (warp == 1 && !(ok = wait_warp(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
+          ++kv;
+          if (warp == 2 && t + 1 < p.t1 && !(ok = wait_warp(&s_kfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
           tc_fence_before();
           warp_arrive(&s_pfull[tile]);
         }
-        if (ok && (ok = mbar_wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) {
+        if (ok && (ok = wait_warp(&s_sfull[tile], sph & 1, abort_flag, err))) {
           ++sph;
           tc_fence_after();
+          if (frees) mbar_arrive(&s_vempty[~kv & 1]);
         }
+      } else if (nt > 0) {
+        kv += nt;
       }
       if (!ok) break;
       // ---- the rows' results ----
