@@ -214,6 +214,7 @@ __device__ __forceinline__ int block_line(const Seq& q, int block, int group, in
   const int2 t = block_tiles(q, block, group, window);
   return max(t.y - t.x, 1) + kSegmentCost;
 }
+// By a warp: its lanes take the blocks in turn.
 __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group, int min_rows, uint32_t* err) {
   Seq q;
   q.row0 = min(max(a.b.q_offsets[b], 0), a.T);
@@ -224,11 +225,13 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
   q.blocks = 0;
   q.per_head = 0;
   if (q.n * group < min_rows || q.n == 0) return q;        // the other form's, or nothing to do
-  const int cap = a.b.max_pages * a.c.page_size;
-  if ((q.start < 0 || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+  const int cap = a.b.max_pages * a.c.page_size, lane = threadIdx.x & 31;
+  if ((q.start < 0 || q.len > cap) && err && lane == 0) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
   q.blocks = (q.n * group + kBlock - 1) / kBlock;
-  for (int i = 0; i < q.blocks; ++i) q.per_head += block_line(q, i, group, a.window);
+  for (int i = lane; i < q.blocks; i += 32) q.per_head += block_line(q, i, group, a.window);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) q.per_head += __shfl_xor_sync(0xffffffffu, q.per_head, o);
   return q;
 }
 
@@ -241,7 +244,7 @@ struct Piece {
   int t0, t1;                                  // key tiles to work on (none if t0 >= t1)
   int c0, np;                                  // the CTAs the segment is spread over
 };
-// A CTA's piece of the line. Every warp walks for itself, its first lane in shared memory.
+// A CTA's piece of the line. Every warp walks for itself, its lanes side by side over the blocks.
 struct Walk {
   long long pos, end, per, first;
   int b, head, block;
@@ -254,7 +257,11 @@ __device__ __forceinline__ void walk_enter(Walk& w, const AttentionArgs& a, int 
   w.block = 0;
   w.at = w.first + w.head * w.q.per_head;
 }
-__device__ __forceinline__ void walk_next(Walk& w, Piece& p, const AttentionArgs& a, int group, int min_rows) {
+__device__ __forceinline__ Piece walk_next(Walk* state, const AttentionArgs& a, int group, int min_rows) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  Walk w = *state;                             // the same in every lane
+  Piece p;
   p.more = false;
   while (w.pos < w.end) {
     while (w.pos >= w.first + w.q.per_head * a.c.kv_heads) {
@@ -262,11 +269,28 @@ __device__ __forceinline__ void walk_next(Walk& w, Piece& p, const AttentionArgs
       ++w.b;
       walk_enter(w, a, group, min_rows);
     }
-    int line = block_line(w.q, w.block, group, a.window);
-    while (w.pos >= w.at + line) {
-      w.at += line;
-      if (++w.block == w.q.blocks) w.block = 0, ++w.head;
-      line = block_line(w.q, w.block, group, a.window);
+    // the block that pos is in: 32 at a time, by a running sum of their lines
+    int line = 0;
+    while (true) {
+      const int mine = w.block + lane < w.q.blocks ? block_line(w.q, w.block + lane, group, a.window) : 0;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, w.at + upto > w.pos);
+      const int j = past ? __ffs(past) - 1 : 31;
+      upto = __shfl_sync(0xffffffffu, upto, j);
+      line = __shfl_sync(0xffffffffu, mine, j);
+      if (past) {
+        w.at += upto - line;
+        w.block += j;
+        break;
+      }
+      w.at += upto;
+      w.block += 32;
+      if (w.block >= w.q.blocks) w.block = 0, ++w.head;
     }
     const int2 t = block_tiles(w.q, w.block, group, a.window);
     const int st0 = max(0, (int)(w.pos - w.at) - kSegmentCost);
@@ -281,8 +305,11 @@ __device__ __forceinline__ void walk_next(Walk& w, Piece& p, const AttentionArgs
     p.c0 = (int)((w.at + kSegmentCost) / w.per);
     p.np = (int)((w.at + line - 1) / w.per) - p.c0 + 1;
     p.more = true;
-    return;
+    break;
   }
+  __syncwarp();
+  if (lane == 0) *state = w;
+  return p;
 }
 
 template <int D>
@@ -305,8 +332,9 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   __shared__ long long s_sum[kThreads / 32], s_first;
   __shared__ int s_seq, s_last;
   __shared__ float4 s_coef[8][8];
-  __shared__ Walk s_walk[17];
-  __shared__ Piece s_piece[17];
+  __shared__ Walk s_walk[16];
+  __shared__ int2 s_issue;                     // the issuing thread's piece: key tiles (0: no more), row tiles
+  __shared__ long long s_line[kThreads];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size;
@@ -335,11 +363,19 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
     *before = base + x - v;
     return all;
   };
-  long long total = 0, at = 0;
+  // line lengths of kThreads sequences at a time, a warp per sequence
+  auto lines = [&](int b0, uint32_t* err) {
+    __syncthreads();
+    for (int b = b0 + warp; b < min(b0 + kThreads, a.b.B); b += kThreads / 32) {
+      const long long line = read_seq(a, b, group, min_rows, err).per_head * heads;
+      if (lane == 0) s_line[b - b0] = line;
+    }
+    __syncthreads();
+    return b0 + tid < a.b.B ? s_line[tid] : 0;
+  };
+  long long total = 0, at = 0, mine = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
-    long long mine = 0;
-    if (b0 + tid < a.b.B)
-      mine = read_seq(a, b0 + tid, group, min_rows, blockIdx.x == 0 ? err : nullptr).per_head * heads;
+    mine = lines(b0, blockIdx.x == 0 ? err : nullptr);
     total += scan(mine, &at);
   }
   long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -348,9 +384,11 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   if (begin >= end) return;
   long long base = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
-    long long mine = 0;
-    if (b0 + tid < a.b.B) mine = read_seq(a, b0 + tid, group, min_rows, nullptr).per_head * heads;
-    const long long sum = scan(mine, &at);
+    long long sum = total;
+    if (a.b.B > kThreads) {                    // else known from the sum above
+      mine = lines(b0, nullptr);
+      sum = scan(mine, &at);
+    }
     if (mine > 0 && base + at <= begin && begin < base + at + mine) s_seq = b0 + tid, s_first = base + at;
     base += sum;
   }
@@ -379,19 +417,12 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  if (warp < 17 && lane == 0) {
-    Walk& w = s_walk[warp];
+  if (warp < 16) {
+    Walk w;
     w.pos = begin, w.end = end, w.per = per, w.first = s_first, w.b = s_seq;
     walk_enter(w, a, group, min_rows);
+    if (lane == 0) s_walk[warp] = w;
   }
-  __syncwarp();
-  const Piece& p = s_piece[warp < 17 ? warp : 0];          // this warp's
-  auto next_piece = [&] {                                  // all lanes of a warp
-    __syncwarp();
-    if (lane == 0) walk_next(s_walk[warp], s_piece[warp], a, group, min_rows);
-    __syncwarp();
-    return p.more;
-  };
 
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -422,13 +453,11 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         for (int i = 1; i < kTile / 16; ++i) mma_ts(o_col, p_col + 8 * i, vd + (uint32_t)(i * 2048 >> 4), id_o, 1u);
       };
       while (ok) {
-        walk_next(s_walk[warp], s_piece[warp], a, group, min_rows);
-        const Piece p = s_piece[warp];         // in registers
-        if (!p.more) break;
-        const int nt = p.t1 - p.t0;
-        if (nt <= 0) continue;
-        const int tiles = p.R > 128 ? 2 : 1;
-        for (int i = 0; i < tiles && ok; ++i) ok = wait_thread(&s_qfull[i], (qph >> i) & 1, abort_flag, err);
+        // tile A's queries are there, and with them the piece; then B's
+        if (!(ok = wait_thread(&s_qfull[0], qph & 1, abort_flag, err))) break;
+        const int nt = s_issue.x, tiles = s_issue.y;
+        if (nt == 0) break;
+        if (tiles == 2) ok = wait_thread(&s_qfull[1], qph >> 1 & 1, abort_flag, err);
         qph ^= tiles == 2 ? 3u : 1u;
         if (ok) ok = wait_thread(&s_kfull[kv & 1], (kv >> 1) & 1, abort_flag, err);
         if (!ok) break;
@@ -473,8 +502,9 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
     const int col = 2 * (piece & 3);
     uint32_t kv = 0;
     bool ok = true;
-    while (ok && next_piece()) {
-      const Piece p = s_piece[warp];           // in registers
+    while (ok) {
+      const Piece p = walk_next(&s_walk[warp], a, group, min_rows);
+      if (!p.more) break;
       const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
       // lane l holds where 16-key group l % 8 of a tile starts in either plane (-1: nowhere)
       auto page_of = [&](int t) {
@@ -562,8 +592,9 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       warp_arrive(&s_join);
       return wait_warp(&s_join, jph++ & 1, abort_flag, err);
     };
-    while (next_piece()) {
-      const Piece p = s_piece[warp];           // in registers
+    while (true) {
+      const Piece p = walk_next(&s_walk[warp], a, group, min_rows);
+      if (!p.more) break;
       const int nt = p.t1 - p.t0;
       const bool live = p.R > 128 * tile;                  // this row tile is worked on
       const bool warp_live = p.R > 32 * warp;              // this warp has rows
@@ -576,38 +607,56 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       // for and signal in its place they do. The last row tile's products come last, so its S tells
       // that K and the V before it are read.
       const bool frees = warp == (p.R > 128 ? 4 : 0) && lane == 0;
+      // A warp's rows go between memory and the tile of queries with D / 8 lanes per row; a thread
+      // has its own row's 16-byte columns there at column_at.
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+      const int col = lane % kLanes, sub = lane / kLanes;
+      char* tile_at = smem + S::kQAt + tile * S::kQ;
+      auto column_at = [&](int row_, int i) {
+        return reinterpret_cast<uint4*>(tile_at + (i >> 3) * S::kHalf + (row_ & 127) * 128 + ((i & 7) ^ (row_ & 7)) * 16);
+      };
       if (live && nt > 0) {
-        // the row as f16 times a power of two, K-major, 128-byte swizzle
-        const uint16_t* src = a.q + row * a.q_stride + (int64_t)hq * D;
-        float amax = 0.0f;
-        if (r < p.R && bf16) {
+        // the rows as f16 times a power of two, K-major, 128-byte swizzle
+        const uint64_t src = reinterpret_cast<uint64_t>(a.q + row * a.q_stride + (int64_t)hq * D);
+        // (code that runs once per piece is kept short: fetching it costs more than running it)
+#pragma unroll 1
+        for (int k0 = 0; k0 < kLanes; k0 += 8) {
+          uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            float f[8];
-            unpack8<MOE_DTYPE_BF16>(__ldg(reinterpret_cast<const uint4*>(src) + i), f);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(f[x]));
+          for (int k = 0; k < 8; ++k) {
+            const int from = kRows * (k0 + k) + sub;
+            const uint64_t at = __shfl_sync(0xffffffffu, src, from);
+            w[k] = load_ahead(reinterpret_cast<const uint4*>(at) + col, r - lane + from < p.R);
           }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) *column_at(r - lane + kRows * (k0 + k) + sub, col) = w[k];
         }
-        const int e = amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
-        const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
-        rowf = pow2f(e);
-        char* dst = smem + S::kQAt + tile * S::kQ + (r & 127) * 128;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (r < p.R) {
-            w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-            if (bf16) {
-              float f[8];
-              unpack8<MOE_DTYPE_BF16>(w, f);
-              w.x = pack_f16(f[0] * s1 * s2, f[1] * s1 * s2), w.y = pack_f16(f[2] * s1 * s2, f[3] * s1 * s2);
-              w.z = pack_f16(f[4] * s1 * s2, f[5] * s1 * s2), w.w = pack_f16(f[6] * s1 * s2, f[7] * s1 * s2);
-            }
+        __syncwarp();
+        if (bf16) {                            // here a thread has its own row
+          uint32_t most = 0;                   // of the magnitudes' bits, in pairs
+#pragma unroll 4
+          for (int i = 0; i < kLanes; ++i) {
+            const uint4 w = *column_at(r, i);
+            most = __vimax3_u16x2(most, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+            most = __vimax3_u16x2(most, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
           }
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * S::kHalf + (((i & 7) ^ (r & 7)) * 16)) = w;
+          const float amax = __uint_as_float(max(most << 16, most & 0xffff0000u));
+          const int e = amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
+          const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
+          rowf = pow2f(e);
+#pragma unroll 2
+          for (int i = 0; i < kLanes; ++i) {
+            uint4* at = column_at(r, i);
+            uint4 w = *at;
+            float f[8];
+            unpack8<MOE_DTYPE_BF16>(w, f);
+            w.x = pack_f16(f[0] * s1 * s2, f[1] * s1 * s2), w.y = pack_f16(f[2] * s1 * s2, f[3] * s1 * s2);
+            w.z = pack_f16(f[4] * s1 * s2, f[5] * s1 * s2), w.w = pack_f16(f[6] * s1 * s2, f[7] * s1 * s2);
+            *at = w;
+          }
         }
         fence_async();
+        if (tid == 0) s_issue = make_int2(nt, p.R > 128 ? 2 : 1);
         warp_arrive(&s_qfull[tile]);
 
         // page factors of a tile's eight 16-key groups: lane g < 8 holds group g's
@@ -721,7 +770,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 }
               }
               // scores so large that their rounding alone could pass 2^8 end there
-              const bool huge = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax);
+              const float cap = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax) ? kLazy : INFINITY;
               // weights; columns 16 ch .. of P lie over columns of S that are already read
 #pragma unroll 1
               for (int ch = 0; ch < 4; ++ch) {
@@ -730,13 +779,6 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 tmem_ld32(s_col + ch * 32, s);
                 const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
                 if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
-                if (huge) {
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) {
-                    const float most = (M + kLazy - (x < 16 ? c0.y : c1.y)) / ((x < 16 ? c0.x : c1.x) * rowf);
-                    s[x] = s[x] > most ? most : s[x];
-                  }
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
@@ -746,6 +788,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                   for (int x = 0; x < 16; x += 2) {
                     float e0, e1;
                     unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
+                    e0 = e0 > cap ? cap : e0, e1 = e1 > cap ? cap : e1;
                     e0 = exp2_approx(e0), e1 = exp2_approx(e1);
                     acc = add2(acc, pair(e0, e1));
                     w[h * 8 + x / 2] = pack_f16(e0, e1);
@@ -777,12 +820,22 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       // ---- the rows' results ----
       const bool whole = p.opens && p.closes, mine = r < p.R;
       const float inv = L > 0.0f ? 1.0f / L : L;           // 0 stays 0, NaN stays NaN
-      auto store8 = [&](int d, const float* v, float k) {  // values d..d+7 of the row
+      auto stage8 = [&](int d, const float* v, float k) {  // values d..d+7 of the row
         float f[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) f[x] = v[x] * k;
-        *reinterpret_cast<uint4*>(a.out + row * a.out_stride + (int64_t)hq * D + d) =
-            bf16 ? pack8<MOE_DTYPE_BF16>(f) : pack8<MOE_DTYPE_F16>(f);
+        *column_at(r, d / 8) = bf16 ? pack8<MOE_DTYPE_BF16>(f) : pack8<MOE_DTYPE_F16>(f);
+      };
+      auto store_rows = [&] {                              // the warp's staged rows
+        const uint64_t dst = reinterpret_cast<uint64_t>(a.out + row * a.out_stride + (int64_t)hq * D);
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < kLanes; ++k) {
+          const int from = kRows * k + sub;
+          const uint64_t at = __shfl_sync(0xffffffffu, dst, from);
+          if (r - lane + from < p.R) reinterpret_cast<uint4*>(at)[col] = *column_at(r - lane + from, col);
+        }
+        __syncwarp();
       };
       auto store_lse = [&](float top, float sum) {
         if (a.lse)
@@ -799,18 +852,17 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = 0.0f;
           }
-          if (mine) {
-            if (whole) {
+          if (whole) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 8) store8(i * 32 + x, o + x, inv);
-            } else {
+            for (int x = 0; x < 32; x += 8) stage8(i * 32 + x, o + x, inv);
+          } else if (mine) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 4)
-                part[((size_t)slot * (D / 4) + i * 8 + x / 4) * kBlock + r] =
-                    make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-            }
+            for (int x = 0; x < 32; x += 4)
+              part[((size_t)slot * (D / 4) + i * 8 + x / 4) * kBlock + r] =
+                  make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
           }
         }
+        if (whole) store_rows();
         if (mine && whole) store_lse(M, L);
         if (mine && !whole) {
           stats[(size_t)slot * 2 * kBlock + r] = M;
@@ -828,11 +880,13 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
           if (s_last) counters[p.c0] = 0;
         }
         if (!(ok = meet())) break;
-        if (s_last && mine) {
+        if (s_last && warp_live) {
           __threadfence();
           auto slot_of = [&](int i) { return (size_t)2 * (p.c0 + i) + (i == 0); };
           float top = kNoMax, sum = 0.0f;
+#pragma unroll 2
           for (int i = 0; i < p.np; ++i) top = fmaxf(top, __ldcg(stats + slot_of(i) * 2 * kBlock + r));
+#pragma unroll 2
           for (int i = 0; i < p.np; ++i)
             sum = fmaf(__ldcg(stats + (slot_of(i) * 2 + 1) * kBlock + r),
                        exp2_approx(__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top), sum);
@@ -842,6 +896,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
             float v[32];
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = 0.0f;
+#pragma unroll 2
             for (int i = 0; i < p.np; ++i) {
               const float k = exp2_approx(__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top);
               float4 o[8];
@@ -854,13 +909,16 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
               }
             }
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) store8(d + x, v + x, k1);
+            for (int x = 0; x < 32; x += 8) stage8(d + x, v + x, k1);
           }
-          store_lse(top, sum);
+          store_rows();
+          if (mine) store_lse(top, sum);
         }
         if (!(ok = meet())) break;             // s_last is read before it is set again
       }
     }
+    if (tid == 0) s_issue = make_int2(0, 0);
+    if (warp < 4) warp_arrive(&s_qfull[0]);
   }
   tc_fence_before();
   __syncthreads();
