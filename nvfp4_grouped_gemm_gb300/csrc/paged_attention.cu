@@ -42,8 +42,10 @@ constexpr float kLazy = 8.0f;
 constexpr int kSegmentCost = 12;
 
 // Rows of a sequence (new tokens times query heads per key head) from which on it goes to the
-// tensor-memory form of prompt_attention.cu.
-constexpr int kPromptRows = 48;
+// tensor-memory form of prompt_attention.cu. That form's time hardly depends on the rows up to 128,
+// this one's grows with every 24. 16 sequences of 500 to 9000 tokens, 8 key heads, this form and the
+// other, us: D = 128: 64 rows 97 / 116, 80 rows 131 / 122; D = 64: 70 rows 60 / 67, 80 rows 83 / 67.
+constexpr int kPromptRows = 73;
 constexpr int kAllRows = 0x7fffffff;
 
 // Workspace: error word; arrival counters [kMaxGrid]; partial maxima and sums
@@ -155,8 +157,7 @@ __device__ long long block_scan(long long v, long long* s_sum, long long* before
 // A warp's keys: which page each half-step (16 tokens) lies in, its scales, for 32 of them at a
 // time (lane l holds half-step l of the batch).
 struct Keys {
-  int page;                     // -1: outside the sequence or out of range
-  float f, v, inv;              // scale * k_scale * log2 e; log2 v_scale; 1 / v_scale
+  float f, v, inv;              // (all 0 without a page) scale * k_scale * log2 e; log2 v_scale; 1 / v_scale
 };
 
 // A lane's share of a block of rows: query fragments, accumulators, and what the running softmax
@@ -423,25 +424,38 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
 
     // ---- this warp's stream ----
     const int count = w1 > w0 + warp ? (w1 - w0 - warp + kWarps - 1) / kWarps : 0;
-    Keys cur = {-1, 0.f, 0.f, 0.f}, nxt = cur;
+    // A batch's pages are read a batch ahead, its scales as its first copy is issued; they become
+    // factors when its first step is taken.
+    Keys cur = {0.f, 0.f, 0.f};
+    int page_of_lane = -1, page_ahead = -1;
+    float k_scale = 0.0f, v_scale = 0.0f;
+    auto key_of = [&](int batch) {             // the lane's first key of a batch, -1: none
+      const int i = batch * kPer + lane / H, j = (w0 + warp + i * kWarps) * S::kStep + (lane % H) * 16;
+      return i < count && j < q.len ? j : -1;
+    };
+    auto read_page = [&](int batch) {
+      const int j = key_of(batch);
+      return (int)load_ahead(a.b.page_table + (int64_t)b * a.b.table_stride + j / P, j >= 0, 0xffffffffu);
+    };
     auto load_keys = [&](int batch) {
-      Keys k = {-1, 0.f, 0.f, 0.f};
-      const int i = batch * kPer + lane / H;
-      if (i < count) {
-        const int j = (w0 + warp + i * kWarps) * S::kStep + (lane % H) * 16;
-        if (j < q.len) {
-          const int page = __ldg(a.b.page_table + (int64_t)b * a.b.table_stride + j / P);
-          if (page >= 0 && page < a.c.num_pages) {
-            k.page = page;
-            const int64_t sc = (int64_t)page * heads + head;
-            k.f = a.scale * 1.4426950408889634f * __ldg(a.c.k_scales + sc);
-            const float vs = fminf(fmaxf(__ldg(a.c.v_scales + sc), 0x1p-100f), 0x1p120f);
-            k.v = log2f(vs);
-            k.inv = __fdividef(1.0f, vs);
-          } else {
-            atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
-          }
-        }
+      if (batch == 0) page_ahead = read_page(0);
+      page_of_lane = page_ahead;
+      page_ahead = read_page(batch + 1);
+      if (page_of_lane < 0 || page_of_lane >= a.c.num_pages) {
+        if (key_of(batch) >= 0) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+        page_of_lane = -1;
+      }
+      const int64_t sc = (int64_t)page_of_lane * heads + head;
+      k_scale = __uint_as_float(load_ahead(a.c.k_scales + sc, page_of_lane >= 0, 0u));
+      v_scale = __uint_as_float(load_ahead(a.c.v_scales + sc, page_of_lane >= 0, 0u));
+    };
+    auto factors = [&] {
+      Keys k = {0.f, 0.f, 0.f};
+      if (page_of_lane >= 0) {
+        const float vs = fminf(fmaxf(v_scale, 0x1p-100f), 0x1p120f);
+        k.f = a.scale * 1.4426950408889634f * k_scale;
+        k.v = log2f(vs);
+        k.inv = __fdividef(1.0f, vs);
       }
       return k;
     };
@@ -449,14 +463,12 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     auto issue = [&](int i) {                  // all lanes: step i of this warp into the next slot
       const int batch = i / kPer, src = (i % kPer) * H;
       if (batch >= have) {
-        cur = nxt;
-        nxt = load_keys(batch);
-        if (have == 0) cur = nxt;
+        load_keys(batch);
         ++have;
       }
       int page[H];
 #pragma unroll
-      for (int h = 0; h < H; ++h) page[h] = __shfl_sync(0xffffffffu, nxt.page, src + h);
+      for (int h = 0; h < H; ++h) page[h] = __shfl_sync(0xffffffffu, page_of_lane, src + h);
       if (lane == 0) {
         char* st = ring + islot * S::kStageB;
         uint64_t* bar = &full[islot];
@@ -580,15 +592,17 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       if (!ok) break;
       const int j0 = (w0 + warp + i * kWarps) * S::kStep;
       const int src = (i % kPer) * H;
-      const bool newer = i / kPer == have - 1;             // which key batch this step is in
+      // the newest batch is this step's: copies are issued fewer steps ahead than a batch has
+      static_assert(S::kSlots <= kPer, "");
+      if (src == 0) cur = factors();
       StepKeys<H> k;
       bool masked = j0 + S::kStep > place_lo + 1 || j0 + S::kStep > q.len;
       if (a.window > 0) masked |= j0 <= place_hi - a.window;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        k.f[h] = __shfl_sync(0xffffffffu, newer ? nxt.f : cur.f, src + h);
-        k.v[h] = __shfl_sync(0xffffffffu, newer ? nxt.v : cur.v, src + h);
-        k.inv[h] = __shfl_sync(0xffffffffu, newer ? nxt.inv : cur.inv, src + h);
+        k.f[h] = __shfl_sync(0xffffffffu, cur.f, src + h);
+        k.v[h] = __shfl_sync(0xffffffffu, cur.v, src + h);
+        k.inv[h] = __shfl_sync(0xffffffffu, cur.inv, src + h);
         k.good[h] = k.inv[h] > 0.0f;
         masked |= !k.good[h];
       }

@@ -23,8 +23,6 @@
 // Per key tile and SM the two products of both row tiles take 4 * 128 * 128 * D * 2 operations and
 // the exponentials 2 * 128 * 128 of 16 per clock: about the same time at D = 128, so the two
 // alternate near both limits.
-#include <climits>
-
 #include "serving.cuh"
 #include "tcgen05.cuh"
 
@@ -178,23 +176,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-// Loads that stay where they are written: the compiler may move an ordinary load behind a wait, next
-// to its use, and expose its latency there.
-__device__ __forceinline__ uint4 load_ahead(const void* at, bool there) {   // zeros if not there
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
-      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at), "r"((int)there) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t load_ahead(const void* at, bool there, uint32_t other) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
-               : "=r"(v) : "l"(at), "r"((int)there), "r"(other) : "memory");
-  return v;
 }
 
 // A sequence's rows and its share of the line.
@@ -509,13 +490,13 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       // lane l holds where 16-key group l % 8 of a tile starts in either plane (-1: nowhere)
       auto page_of = [&](int t) {
         const int j = t * kTile + (lane & 7) * 16;
-        return (int)load_ahead(table + (j >> log_p), t < p.t1 && j < p.len, (uint32_t)INT_MIN);
+        return (int)load_ahead(table + (j >> log_p), t < p.t1 && j < p.len, 0xffffffffu);
       };
       auto start_of = [&](int t, int page) {
         const int j = t * kTile + (lane & 7) * 16;
         if (page >= 0 && page < a.c.num_pages)
           return page * a.c.page_stride + ((int64_t)p.head * P + (j & (P - 1))) * D;
-        if (page != INT_MIN) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+        if (t < p.t1 && j < p.len) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
         return (int64_t)-1;
       };
       int page_next = page_of(p.t0);           // of the tile after the one fetched from

@@ -105,4 +105,21 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Loads that stay where they are written: the compiler may move an ordinary load behind a wait, next
+// to its use, and expose its latency there.
+__device__ __forceinline__ uint4 load_ahead(const void* at, bool there) {   // zeros if not there
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at), "r"((int)there) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load_ahead(const void* at, bool there, uint32_t other) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+               : "=r"(v) : "l"(at), "r"((int)there), "r"(other) : "memory");
+  return v;
+}
+
 }  // namespace moe
