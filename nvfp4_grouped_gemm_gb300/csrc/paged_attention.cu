@@ -34,7 +34,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxGrid = 512;              // partial slots of the workspace
-constexpr int kMaxRows = 32;
+constexpr int kMaxRows = 24;
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
 // What a segment costs beside its steps (queries, first copies, the warps' rows meeting), in
@@ -43,8 +43,9 @@ constexpr int kSegmentCost = 12;
 
 // Rows of a sequence (new tokens times query heads per key head) from which on it goes to the
 // tensor-memory form of prompt_attention.cu. That form's time hardly depends on the rows up to 128,
-// this one's grows with every 24. 16 sequences of 500 to 9000 tokens, 8 key heads, this form and the
-// other, us: D = 128: 64 rows 97 / 116, 80 rows 131 / 122; D = 64: 70 rows 60 / 67, 80 rows 83 / 67.
+// this one's grows with every 24. Sequences of 500 to 9000 tokens, 8 key heads, this form and the
+// other, us: 16 sequences, D = 128: 64 rows 92 / 116, 96 rows 121 / 115; D = 64: 70 rows 63 / 67, 80
+// rows 74 / 67; 64 sequences of up to 4000, 80 rows: D = 128 258 / 229, D = 64 167 / 145.
 constexpr int kPromptRows = 73;
 constexpr int kAllRows = 0x7fffffff;
 
@@ -64,7 +65,7 @@ struct Shape {
   static constexpr int kPlaneB = kStep * D;              // a step's K (or V) bytes
   static constexpr int kStageB = 2 * kPlaneB;
   static constexpr int kSlots = D == 64 ? 4 : NT > 2 ? 3 : 2;
-  static constexpr int kCtas = WARPS_ > 4 ? 1 : NT * D > 256 || NT > 3 ? 2 : 3;         // per SM
+  static constexpr int kCtas = WARPS_ > 4 ? 1 : NT * D > 256 || (NT == 2 && D == 128) ? 2 : 3;   // per SM
   static constexpr int kRows = 8 * NT;
   static constexpr int kRingB = kWarps * kSlots * kStageB;
   static constexpr int kMergeB = kWarps * kRows * D * 4; // aliases the ring
@@ -807,15 +808,15 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
 template <int D>
 cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
   // Row tiles of a block: as few as hold the sequences' rows on average in one pass over the keys,
-  // or in equal passes beyond four (five tiles of 64-value heads in one pass: fewer warps fit, and
-  // 16 sequences of 8 new tokens and 5 heads took 49.0 us against 45.5 in two passes of three).
-  constexpr int kMost = D == 256 ? 2 : 4;
+  // or in equal passes beyond three: a fourth tile does not fit into the registers. 16 sequences of
+  // 500 to 9000 tokens, 32 rows: 54 us in two passes of two tiles, 67 in one of four (D = 128); 30
+  // rows of D = 64: 37 and 42; 40 rows of D = 64 in one pass of five: 49 against 47 in two of three.
+  constexpr int kMost = D == 256 ? 2 : 3;
   const long long rows = ((long long)a.T * (a.q_heads / a.c.kv_heads) + a.b.B - 1) / a.b.B;
   const long long tiles = (rows + 7) / 8, passes = (tiles + kMost - 1) / kMost;
   const int nt = (int)((tiles + passes - 1) / passes);
   if constexpr (D <= 128) {
     if (nt == 3) return launch_shape<D, 3, 4>(a, s);
-    if (nt == 4) return launch_shape<D, 4, 4>(a, s);
   }
   if (nt == 2) return launch_shape<D, 2, 4>(a, s);
   // Few segments: more warps per CTA, so that fewer partial rows have to be joined.
