@@ -132,7 +132,8 @@ size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t K);
  * or f16) [T][K], rows x_stride elements apart (16-byte aligned as above); y: y_dtype (bf16, f16
  * or f32) [T][N], rows y_stride elements apart. Products are exact (x as f16 times a power of
  * two, exact for values within 2^-28 of the row's largest; E2M1 * UE4M3 in f16), sums are f32.
- * The weights are read once for every 8 tokens or more; the call is made for few tokens. */
+ * The weights are read once per pass of as many tokens as 128 KiB of x in f16 hold, at most 32 (a
+ * power of two: 16 at K = 4096, 4 at 16384); the call is made for few tokens. */
 moe_status moe_linear_nvfp4(const void* x, int64_t x_stride, int32_t x_dtype, int32_t T,
                             const moe_nvfp4_bank* w, void* y, int64_t y_stride, int32_t y_dtype,
                             void* ws, size_t ws_bytes, void* stream);

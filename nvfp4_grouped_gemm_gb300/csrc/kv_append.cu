@@ -11,6 +11,11 @@
 // Rotation and rounding use single correctly rounded operations in a fixed order (no fused
 // multiply-add), so codes and scales are the same bits wherever the definition is evaluated in
 // f32.
+//
+// Bound by the rows' bytes (2 read and 2 written per query value, 2 read and 1 written per key or
+// value): six prompts of up to 2048 tokens, 32 query and 8 key heads of 128 (127 MB), take 31 us, 4.1
+// TB/s; what does not stream are a page's dependent steps (largest magnitude, then codes). One
+// token of one sequence takes 3.3 us, a launch and a few dependent loads.
 #include "serving.cuh"
 
 namespace moe {

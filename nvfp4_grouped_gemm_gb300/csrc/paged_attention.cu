@@ -27,6 +27,12 @@
 //
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
 // weight 0, and V's bytes there are replaced by 0 (they may be NaN codes).
+//
+// Bound by the cache's bytes: 64 sequences of 100 to 16000 tokens, 32 query and 8 key heads of 128,
+// one new token each: 73.7 us, 5.7 TB/s (0.84 of the copy rate). One sequence of 32767: 23.6 us, of
+// which about 12 are fixed: the line's scan, the first keys and queries, the warps' rows meeting,
+// and the join of the segment's pieces. With more rows the products and the softmax's instructions
+// are the limit: 16 sequences, 8 tokens and 5 heads of 64 (40 rows): 46.6 us.
 #include "serving.cuh"
 #include "tma_sync.cuh"
 

@@ -20,9 +20,17 @@
 // covers every product issued before it, so a softmax that sees its S knows that the previous
 // O += P V is complete and may rescale O.
 //
-// Per key tile and SM the two products of both row tiles take 4 * 128 * 128 * D * 2 operations and
-// the exponentials 2 * 128 * 128 of 16 per clock: about the same time at D = 128, so the two
-// alternate near both limits.
+// Tensor memory is full at D = 128 (two S, two O of 128 columns), so a tile's weights lie over its
+// S and its chain (softmax, O += P V, the next S) is serial; two tiles in flight hide each other's
+// softmax. 2048 new tokens after 6144, 32 query and 8 key heads of 128, bf16: 275 us, 0.87 PFLOP/s
+// of unmasked products. A period of both tiles takes about 4400 clocks: 2 * 1400 of products (1024
+// without the widening warps' stores beside their operand reads in shared memory), and a softmax
+// of about 2000 with hand-offs of about 400. What its steps gave: the weights from one reading of
+// S (before, a pass for the maximum came first) and waits that neither read the clock nor tell
+// lanes the outcome 361 -> 288 us; the line walked by whole warps, rows staged and stored
+// coalesced 288 -> 275. Slower: two threads per row (a barrier per tile between them and fewer
+// registers), S held in registers (the widening warps, short of them, then spill), key tiles of 64
+// with two S in flight (394 us when this form took 361).
 #include "serving.cuh"
 #include "tcgen05.cuh"
 
