@@ -5,15 +5,17 @@
 // find the page's new tokens, take the largest rotated magnitude, settle the page's scale, rescale
 // the page's earlier codes if it grew, and write the new codes. The other blocks rotate
 // queries. A head's D values are handled as D/16 chunks of 16 values that rotate among
-// themselves: in the half-split order values [8i, 8i+8) with [rotary/2 + 8i, ...), in the
-// interleaved order (and past rotary_dim) 16 consecutive values.
+// themselves: values [8i, 8i+8) with [rotary/2 + 8i, ...), in the interleaved order too (whose pairs
+// lie inside the groups of eight), and past rotary_dim likewise, so that neighbouring lanes' 16-byte
+// accesses are neighbours in memory (16 consecutive values per lane took 31.1 us against 30.5 for
+// six interleaved prompts of up to 2048 tokens).
 //
 // Rotation and rounding use single correctly rounded operations in a fixed order (no fused
 // multiply-add), so codes and scales are the same bits wherever the definition is evaluated in
 // f32.
 //
 // Bound by the rows' bytes (2 read and 2 written per query value, 2 read and 1 written per key or
-// value): six prompts of up to 2048 tokens, 32 query and 8 key heads of 128 (127 MB), take 31 us, 4.1
+// value): six prompts of up to 2048 tokens, 32 query and 8 key heads of 128 (127 MB), take 30.5 us, 4.2
 // TB/s; what does not stream are a page's dependent steps (largest magnitude, then codes). One
 // token of one sequence takes 3.3 us, a launch and a few dependent loads.
 #include "serving.cuh"
@@ -23,33 +25,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Where chunk `ch` of a head keeps its two groups of eight values, and which table columns
-// rotate it (col < 0: not rotated).
+// Where chunk `ch` of a head keeps its two groups of eight values, and which table columns turn
+// the first and the last four of their pairs (col < 0: not rotated).
 struct Chunk {
-  int lo, hi, col;
+  int lo, hi, col, col4;
 };
-__device__ __forceinline__ Chunk chunk_at(int ch, int rotary, int interleaved) {
+__device__ __forceinline__ Chunk chunk_at(int ch, int D, int rotary, int interleaved) {
+  const bool turned = 16 * ch < rotary;
+  const int first = turned ? 0 : rotary, i = ch - first / 16;
   Chunk r;
-  const int rot = rotary / 16;
-  if (ch < rot && !interleaved) {
-    r.lo = 8 * ch;
-    r.hi = rotary / 2 + 8 * ch;
-  } else {
-    r.lo = 16 * ch;
-    r.hi = 16 * ch + 8;
-  }
-  r.col = ch < rot ? 8 * ch : -1;
+  r.lo = first + 8 * i;
+  r.hi = r.lo + (turned ? rotary : D - rotary) / 2;
+  r.col = !turned ? -1 : interleaved ? 4 * i : 8 * i;
+  r.col4 = interleaved ? rotary / 4 + 4 * i : 8 * i + 4;
   return r;
 }
 
 struct Turn {
   float c[8], s[8];
 };
-__device__ __forceinline__ void load_turn(Turn& t, const float* cos, const float* sin, int64_t at) {
+// Of the table row that starts at `at`.
+__device__ __forceinline__ void load_turn(Turn& t, const float* cos, const float* sin, int64_t at, const Chunk& ch) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(cos + at) + i);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(sin + at) + i);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(cos + at + (i ? ch.col4 : ch.col)));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(sin + at + (i ? ch.col4 : ch.col)));
     t.c[4 * i] = a.x, t.c[4 * i + 1] = a.y, t.c[4 * i + 2] = a.z, t.c[4 * i + 3] = a.w;
     t.s[4 * i] = b.x, t.s[4 * i + 1] = b.y, t.s[4 * i + 2] = b.z, t.s[4 * i + 3] = b.w;
   }
@@ -189,7 +189,7 @@ __device__ __forceinline__ void page_chunk(const KvAppendArgs& a, const Item& it
   if (is_k && c.col >= 0) {
     const int pos = clamp_position(a.positions ? a.positions[row] : it.place0 + tok, a.max_pos, a.err);
     Turn t;
-    load_turn(t, a.cos, a.sin, (int64_t)pos * (a.rotary / 2) + c.col);
+    load_turn(t, a.cos, a.sin, (int64_t)pos * (a.rotary / 2), c);
     turn_chunk(lo, hi, t, a.interleaved);
   }
 }
@@ -229,13 +229,13 @@ __device__ __forceinline__ void page_block(const KvAppendArgs& a, int it_index, 
     for (int n = 0; n < KEEP; ++n) {
       const int u = threadIdx.x + n * kThreads;
       if (u < count) {
-        page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), rotary, inter), lo[n], hi[n]);
+        page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), D, rotary, inter), lo[n], hi[n]);
         raise(lo[n], hi[n]);
       }
     }
   } else {
     for (int u = threadIdx.x; u < count; u += kThreads) {
-      page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), rotary, inter), lo[0], hi[0]);
+      page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), D, rotary, inter), lo[0], hi[0]);
       raise(lo[0], hi[0]);
     }
   }
@@ -266,7 +266,7 @@ __device__ __forceinline__ void page_block(const KvAppendArgs& a, int it_index, 
   const bool pow2 = (bits & 0x807fffffu) == 0 && bits >= 0x00800000u && bits <= 0x7e800000u;
   const float inv = pow2 ? __uint_as_float(0x7f000000u - bits) : 0.0f;
   auto put = [&](int u, const float (&x)[8], const float (&y)[8]) {
-    const Chunk c = chunk_at(u & (per - 1), rotary, inter);
+    const Chunk c = chunk_at(u & (per - 1), D, rotary, inter);
     uint8_t* dst = codes + (int64_t)(it.slot0 + (u >> log_per)) * D;
     *reinterpret_cast<uint2*>(dst + c.lo) = quant8(x, scale, inv, pow2);
     *reinterpret_cast<uint2*>(dst + c.hi) = quant8(y, scale, inv, pow2);
@@ -279,7 +279,7 @@ __device__ __forceinline__ void page_block(const KvAppendArgs& a, int it_index, 
     }
   } else {
     for (int u = threadIdx.x; u < count; u += kThreads) {
-      page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), rotary, inter), lo[0], hi[0]);
+      page_chunk<DT>(a, it, head, is_k, u >> log_per, chunk_at(u & (per - 1), D, rotary, inter), lo[0], hi[0]);
       put(u, lo[0], hi[0]);
     }
   }
@@ -306,7 +306,7 @@ __device__ void query_block(const KvAppendArgs& a, int block, int heads_per) {
   const int tg = (int)(u >> log_per);           // T * q_heads < 2^31 is checked by the host
   const int g = tg % groups, t = tg / groups;
   if (t >= a.T) return;
-  const Chunk c = chunk_at(ch, a.rotary, a.interleaved);
+  const Chunk c = chunk_at(ch, D, a.rotary, a.interleaved);
   const int h0 = g * heads_per, h1 = min(a.q_heads, h0 + heads_per);
   const uint16_t* src = a.q + (int64_t)t * a.q_stride;
   uint16_t* dst = a.q_out + (int64_t)t * a.q_out_stride;
@@ -331,7 +331,7 @@ __device__ void query_block(const KvAppendArgs& a, int block, int heads_per) {
       pos = a.b.seq_lens[b] - a.b.q_offsets[b + 1] + t;
     }
     pos = clamp_position(pos, a.max_pos, a.err);
-    load_turn(turn, a.cos, a.sin, (int64_t)pos * (a.rotary / 2) + c.col);
+    load_turn(turn, a.cos, a.sin, (int64_t)pos * (a.rotary / 2), c);
   }
   for (int h = h0; h < h1; h += kAhead) {
     if (h > h0) ask(h);
