@@ -281,3 +281,26 @@ def test_nan_and_infinite_queries_stay_in_their_rows():
         keep = torch.ones(batch.T, 2, dtype=torch.bool)
         keep[0, 1] = False
         assert torch.equal(a[keep.cuda()], b[keep.cuda()]) and torch.equal(la[keep.cuda()], lb[keep.cuda()])
+
+
+def test_more_sequences_than_a_block_has_threads():
+    rng = np.random.default_rng(35)
+    pairs = [(int(rng.integers(0, 40)), int(rng.choice([0, 1, 2, 9, 10, 17]))) for _ in range(1400)]
+    check(rng, pairs, 16, 1, 8, 64, "bf16")
+
+
+@pytest.mark.parametrize("window", [0, 50])
+def test_more_blocks_of_rows_than_a_warp_has_lanes(window):
+    check(np.random.default_rng(36), [(0, 300), (37, 280), (5, 1)], 16, 1, 33, 64, "f16", window=window)
+
+
+def test_many_rows_whose_largest_score_comes_late():
+    rng = np.random.default_rng(37)
+    check(rng, [(2500, 80)], 64, 1, 2, 128, "bf16", amp=40.0)
+
+    def planes(batch):                           # every page's keys four times the one's before
+        p = list(cache_planes(rng, batch.num_pages, 1, 64, 64))
+        for i, page in enumerate(batch.table[0][:20]):
+            p[1][page] = np.float32(2.0 ** (2 * i - 30))
+        return tuple(p)
+    check(rng, [(1100, 90)], 64, 1, 2, 64, "f16", planes=planes)
