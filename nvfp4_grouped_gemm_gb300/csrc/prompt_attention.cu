@@ -732,7 +732,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
               }
             }
             if (__builtin_expect(twice, 0)) {
-              // the largest s f + v of the row in this tile (f > 0: from each group's largest s)
+              // the largest s f + v of the row in this tile (f >= 0: from each group's largest s; a group
+              // without one may give NaN, which fmaxf passes over)
               float top = kNoMax;
 #pragma unroll 1
               for (int ch = 0; ch < 4; ++ch) {
@@ -767,16 +768,21 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 uint32_t w[16];
                 tmem_ld32(s_col + ch * 32, s);
                 const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
-                if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
                   const uint64_t ff = pair(f, f), dd = pair(d, d);
+#pragma unroll
+                  for (int x = 16 * h; x < 16 * h + 16; x += 2) unpair(fma2(pair(s[x], s[x + 1]), ff, dd), s[x], s[x + 1]);
+                }
+                // hidden as exponents: a factor that underflows to 0 would make NaN of a score of -inf
+                if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                   uint64_t acc = 0;
 #pragma unroll
                   for (int x = 0; x < 16; x += 2) {
-                    float e0, e1;
-                    unpair(fma2(pair(s[16 * h + x], s[16 * h + x + 1]), ff, dd), e0, e1);
+                    float e0 = s[16 * h + x], e1 = s[16 * h + x + 1];
                     e0 = e0 > cap ? cap : e0, e1 = e1 > cap ? cap : e1;
                     e0 = exp2_approx(e0), e1 = exp2_approx(e1);
                     acc = add2(acc, pair(e0, e1));

@@ -304,3 +304,19 @@ def test_many_rows_whose_largest_score_comes_late():
             p[1][page] = np.float32(2.0 ** (2 * i - 30))
         return tuple(p)
     check(rng, [(1100, 90)], 64, 1, 2, 64, "f16", planes=planes)
+
+
+# ---- factors of the scores below the least float32 ----
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("pairs", [[(100, 3), (20, 1)], [(100, 90), (0, 140), (7, 2)]])
+def test_tiny_queries_and_zero_keys_hide_what_a_row_does_not_see(pairs, window):
+    """scale * k_scale times a row's power of two may underflow to 0; hidden keys stay hidden."""
+    rng = np.random.default_rng(38)
+    check(rng, pairs, 16, 1, 2, 64, "bf16", window=window, amp=2.0 ** -130)
+
+    def planes(batch):                           # the scale that an append gives zero keys
+        p = list(cache_planes(rng, batch.num_pages, 2, 64, 128))
+        p[0][:], p[1][:] = 0, np.float32(2.0 ** -64)
+        return tuple(p)
+    check(rng, pairs, 64, 2, 2, 128, "bf16", window=window, amp=2.0 ** -72, planes=planes)
+    check(rng, pairs, 64, 2, 2, 128, "bf16", window=window, amp=0.0, planes=planes)
