@@ -285,28 +285,41 @@ def _prob_rows(dev: int, t: torch.Tensor, dtype: torch.dtype, shape: tuple, what
 
 
 class NvFp4Linear:
-    """One projection with NVFP4 weights: the bank (one expert) plus its buffers per token count,
-    allocated once and reused, so repeated calls allocate nothing."""
+    """One projection with NVFP4 weights: the bank (one expert) plus its buffers per token count
+    and stream, allocated once and reused, so repeated calls allocate nothing.  The rows that
+    ``forward`` returns are such a buffer: the next call of as many tokens on the same stream
+    overwrites them.  A call that is captured in a graph uses the buffers of an earlier call of as
+    many tokens, if there was one; replays must not overlap that stream's calls."""
 
     def __init__(self, bank, out_dtype: torch.dtype = torch.bfloat16):
         if bank.E != 1:
             raise ValueError("a linear layer's bank has one expert")
         self.bank, self.out_dtype = bank, out_dtype
-        self._bufs = {}
+        self._bufs = {}                          # by (tokens, stream handle)
 
-    def buffers(self, T: int) -> dict:
-        if T not in self._bufs:
-            dev = self.bank.codes.device
-            n = linear_workspace_bytes(T, self.bank.rows, self.bank.in_f)
-            if n == 0:
-                raise MoeError(2, "linear_workspace_bytes")
-            self._bufs[T] = {
+    def buffers(self, T: int, stream=None) -> dict:
+        key = T, _queue(_device(), stream)
+        return self._bufs.get(key) or self._new_buffers(key, stream)
+
+    def _new_buffers(self, key: tuple, stream) -> dict:
+        T, dev = key[0], self.bank.codes.device
+        n = linear_workspace_bytes(T, self.bank.rows, self.bank.in_f)
+        if n == 0:
+            raise MoeError(2, "linear_workspace_bytes")
+        # on the call's stream: its kernels come behind the fill, and behind whatever used the
+        # memory before
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                for (t, _), b in self._bufs.items():
+                    if t == T:
+                        return b
+            b = self._bufs[key] = {
                 "ws": torch.zeros(n, dtype=torch.uint8, device=dev),
                 "y": torch.empty(T, self.bank.rows, dtype=self.out_dtype, device=dev),
             }
-        return self._bufs[T]
+        return b
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
-        b = self.buffers(x.shape[0])
+        b = self.buffers(x.shape[0], stream)
         moe_linear_nvfp4(x, self.bank, b["y"], b["ws"], stream)
         return b["y"]

@@ -93,3 +93,74 @@ def test_the_layer_object_keeps_its_buffers():
     want, tol = oracle.linear(x.double().cpu().numpy(), w)
     assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol)
     assert lin.forward(x).data_ptr() == y.data_ptr()
+
+
+def busy():
+    """Some tens of milliseconds of work on the current stream."""
+    a = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    for _ in range(30):
+        a @ a
+
+
+def test_the_layer_object_s_buffers_belong_to_the_call_s_stream():
+    """A call on another stream than the current one: neither the zero fill of a new workspace nor
+    memory that the current stream still writes may come behind it."""
+    rng = np.random.default_rng(8)
+    T, N, K = 16, 3001, 2048
+    bank, w = bank_of(rng, N, K)
+    x = activations(rng, (T, K), "bf16")
+    want, tol = oracle.linear(x.double().numpy(), w)
+    tol = tol + ROUND["f32"][0] * (np.abs(want) + tol)
+    x, side = x.cuda(), torch.cuda.Stream()
+    ws_bytes = moe.linear_workspace_bytes(T, N, K)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        # blocks of the sizes the object asks for, last written by work that is still queued
+        busy()
+        for rows in (16, 32):
+            y = torch.full((rows, N), 7.0, device="cuda")
+            del y
+        for n in (ws_bytes, moe.linear_workspace_bytes(32, N, K)):
+            ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+            del ws
+        lin = moe.NvFp4Linear(bank, torch.float32)
+        y = lin.forward(x, stream=side)
+        torch.cuda.synchronize()
+        assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol)
+
+
+def test_the_layer_object_s_calls_on_two_streams_do_not_share_buffers():
+    rng = np.random.default_rng(9)
+    bank, w = bank_of(rng, 500, 4096)
+    lin = moe.NvFp4Linear(bank, torch.float32)
+    xs = [activations(rng, (16, 4096), "bf16") for _ in range(2)]
+    wants = [oracle.linear(x.double().numpy(), w) for x in xs]
+    xs, streams = [x.cuda() for x in xs], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        ys = [lin.forward(x, stream=s) for x, s in zip(xs, streams)]
+    torch.cuda.synchronize()
+    assert ys[0].data_ptr() != ys[1].data_ptr()
+    for y, (want, tol) in zip(ys, wants):
+        assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol + 2.0 ** -24 * (np.abs(want) + tol))
+
+
+def test_the_layer_object_captures_with_the_buffers_of_the_call_before():
+    """A warm-up call's buffers serve the capture, and calls of other sizes leave them alone."""
+    rng = np.random.default_rng(10)
+    bank, w = bank_of(rng, 300, 1024)
+    lin = moe.NvFp4Linear(bank, torch.float32)
+    x = activations(rng, (3, 1024), "bf16").cuda()
+    warm = lin.forward(x)
+    first = warm.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin.forward(x)
+    assert y.data_ptr() == warm.data_ptr()
+    for T in (40, 1, 200):                       # buffers of other sizes; the graph's stay its own
+        lin.forward(activations(rng, (T, 1024), "bf16").cuda())
+    y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, first)
