@@ -285,38 +285,47 @@ def _prob_rows(dev: int, t: torch.Tensor, dtype: torch.dtype, shape: tuple, what
 
 
 class NvFp4Linear:
-    """One projection with NVFP4 weights: the bank (one expert) plus its buffers per token count
-    and stream, allocated once and reused, so repeated calls allocate nothing.  The rows that
-    ``forward`` returns are such a buffer: the next call of as many tokens on the same stream
-    overwrites them.  A call that is captured in a graph uses the buffers of an earlier call of as
-    many tokens, if there was one; replays must not overlap that stream's calls."""
+    """One projection with NVFP4 weights: the bank (one expert) plus its buffers, allocated once
+    and reused, so repeated calls allocate nothing.
+
+    Buffers are kept per stream and for powers of two of tokens (calls of any sizes up to T keep at
+    most four times what one of T needs).  The rows that ``forward`` returns are the first of such
+    a buffer: the stream's next call whose tokens round up to the same power of two overwrites
+    them.  A call that is captured in a graph uses the buffers of an earlier call of its size, if
+    there was one; replays must not overlap that stream's calls."""
 
     def __init__(self, bank, out_dtype: torch.dtype = torch.bfloat16):
         if bank.E != 1:
             raise ValueError("a linear layer's bank has one expert")
         self.bank, self.out_dtype = bank, out_dtype
-        self._bufs = {}                          # by (tokens, stream handle)
+        self._kept = {}                          # by (tokens, a power of two; stream handle)
+        self._bufs = {}                          # their first rows by (tokens, stream handle)
 
     def buffers(self, T: int, stream=None) -> dict:
         key = T, _queue(_device(), stream)
         return self._bufs.get(key) or self._new_buffers(key, stream)
 
     def _new_buffers(self, key: tuple, stream) -> dict:
-        T, dev = key[0], self.bank.codes.device
-        n = linear_workspace_bytes(T, self.bank.rows, self.bank.in_f)
-        if n == 0:
+        T, handle = key
+        if linear_workspace_bytes(T, self.bank.rows, self.bank.in_f) == 0:
             raise MoeError(2, "linear_workspace_bytes")
+        most = 1 << (T - 1).bit_length()
         # on the call's stream: its kernels come behind the fill, and behind whatever used the
         # memory before
         with torch.cuda.stream(stream):
-            if torch.cuda.is_current_stream_capturing():
-                for (t, _), b in self._bufs.items():
-                    if t == T:
-                        return b
-            b = self._bufs[key] = {
-                "ws": torch.zeros(n, dtype=torch.uint8, device=dev),
-                "y": torch.empty(T, self.bank.rows, dtype=self.out_dtype, device=dev),
-            }
+            kept = self._kept.get((most, handle))
+            if kept is None and torch.cuda.is_current_stream_capturing():
+                for (m, _), other in self._kept.items():
+                    if m == most:                # lent to the capture only
+                        return {"ws": other["ws"], "y": other["y"][:T]}
+            if kept is None:
+                n = linear_workspace_bytes(most, self.bank.rows, self.bank.in_f)
+                dev = self.bank.codes.device
+                kept = self._kept[most, handle] = {
+                    "ws": torch.zeros(n, dtype=torch.uint8, device=dev),
+                    "y": torch.empty(most, self.bank.rows, dtype=self.out_dtype, device=dev),
+                }
+        b = self._bufs[key] = {"ws": kept["ws"], "y": kept["y"][:T]}
         return b
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:

@@ -164,3 +164,24 @@ def test_the_layer_object_captures_with_the_buffers_of_the_call_before():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, first)
+
+
+def test_the_layer_object_s_memory_follows_the_largest_call():
+    """Calls of every size up to T keep no more than a few times the largest one's buffers."""
+    rng = np.random.default_rng(11)
+    bank, w = bank_of(rng, 20011, 512)
+    lin = moe.NvFp4Linear(bank, torch.float32)
+    xs = activations(rng, (96, 512), "bf16")
+    want, tol = oracle.linear(xs.double().numpy(), w)
+    tol = tol + 2.0 ** -24 * (np.abs(want) + tol)
+    xs = xs.cuda()
+    largest = 128 * 20011 * 4 + moe.linear_workspace_bytes(128, 20011, 512)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for T in range(1, 97):
+        y = lin.forward(xs[:T])
+        assert y.shape == (T, 20011)
+    assert torch.cuda.memory_allocated() - before <= 2.5 * largest
+    for T in (96, 5, 64, 1):
+        y = lin.forward(xs[:T])
+        assert np.all(np.abs(y.double().cpu().numpy() - want[:T]) <= tol[:T])
