@@ -26,7 +26,9 @@
 // the accumulators rare. w is rounded to f16 (2^-11), sums and accumulators are f32.
 //
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
-// weight 0, and V's bytes there are replaced by 0 (they may be NaN codes).
+// weight 0. V's bytes that are nobody's are replaced by 0 (they may be NaN codes). NaN codes of
+// keys that some rows of the block see and others do not are kept out of the products, and NaN is
+// put into the sums of the rows that see them when the rows meet.
 //
 // Bound by the cache's bytes: 64 sequences of 100 to 16000 tokens, 32 query and 8 key heads of 128,
 // one new token each: 73.7 us, 5.7 TB/s (0.84 of the copy rate). One sequence of 32767: 23.6 us, of
@@ -327,6 +329,58 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
     }
 }
 
+// Makes the NaN codes among a step's values finite (a lane per token, two at D = 256; `there`: the token
+// is). Whether there were any. A pass of its own over the stage, so that the products' registers stay theirs.
+template <class S>
+__device__ __forceinline__ bool keep_nan_out(char* st, int lane, bool there) {
+  constexpr int kChunks = S::kPlaneB / 16 / 32;
+  char* row = st + S::kPlaneB + (S::D == 256 ? (lane >> 4) * (S::kStep * 128) + (lane & 15) * 128 : lane * S::kRowB);
+  uint32_t bad = 0;
+#pragma unroll 2
+  for (int i = 0; i < kChunks; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + ((i + lane) % kChunks) * 16);
+    bad |= e4m3_nan_bits(v.x) | e4m3_nan_bits(v.y) | e4m3_nan_bits(v.z) | e4m3_nan_bits(v.w);
+  }
+  if (!__any_sync(0xffffffffu, there && bad != 0)) return false;
+#pragma unroll 1
+  for (int i = 0; i < kChunks * 4; ++i) {
+    uint32_t& w = reinterpret_cast<uint32_t*>(row)[i];
+    w &= ~(e4m3_nan_bits(w) >> 7);               // with a weight of 0 where the key is not seen
+  }
+  // plain writes to the ring's memory come before the next copies into it
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  return true;
+}
+// Where the rows that meet have values d .. d+3 of row r: 16-byte units of a row are permuted so
+// that a quarter warp's stores differ in bank.
+template <int D>
+__device__ __forceinline__ int merge_unit(int r, int d) {
+  const int u = d / 4, cc = (r & 7) >> 1;
+  return D == 64 ? u ^ ((cc & 1) | (cc >> 1) << 2) : u ^ (cc | ((u >> 4) & 1) << 2);
+}
+// NaN codes kept out of the products, from the pages: a lane per key of the warp's steps from key j0 on,
+// into those of the warp's rows that see it (all to the sequence's end: a row has the NaN of a key that
+// it sees in another CTA's piece anyway). A call of its own: it is hardly ever made, and in line its
+// registers cost the steps theirs (64 sequences: 79 us, 76.8 so).
+template <class S>
+__device__ __noinline__ void put_nan(const AttentionArgs& a, int n, int start, int len, int b, int head, int block,
+                                     int j0, float* rows) {
+  constexpr int D = S::D;
+  const int lane = threadIdx.x & 31, P = a.c.page_size, group = a.q_heads / a.c.kv_heads;
+  const int R = min(S::kRows, n * group - block * S::kRows);
+  for (int j = j0 + lane; lane < S::kStep && j < len; j += S::kWarps * S::kStep) {
+    const int page = a.b.page_table[(int64_t)b * a.b.table_stride + j / P];
+    if (page < 0 || page >= a.c.num_pages) continue;
+    each_nan<D>(a.c.v_codes + page * a.c.page_stride + (int64_t)(head * P + j % P) * D, [&](int d) {
+      for (int r = 0; r < R; ++r) {
+        const int place = start + (block * S::kRows + r) / group;
+        if (j <= place && (a.window == 0 || j > place - a.window)) rows[r * D + merge_unit<D>(r, d) * 4 + d % 4] = NAN;
+      }
+    });
+  }
+}
+
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -341,6 +395,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   __shared__ volatile int s_abort;
   __shared__ float s_rowf[S::kRows], s_m[kWarps][S::kRows], s_l[kWarps][S::kRows];
   __shared__ int s_last;
+  constexpr int kNone = 0x7fffffff;
+  __shared__ volatile int s_nan[kWarps];       // first key of the warp's first step with NaN codes kept out
   char* big = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   char* s_q = big + S::kBigB;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -528,6 +584,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       }
     };
     ask(0);
+    if (lane == 0) s_nan[warp] = kNone;
     for (int i = 0; i < min(count, S::kSlots); ++i) issue(i);
 #pragma unroll 1
     for (int i0 = 0; i0 < kMine; i0 += kAtOnce) {
@@ -613,9 +670,15 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         k.good[h] = k.inv[h] > 0.0f;
         masked |= !k.good[h];
       }
-      const char* st = ring + tslot * S::kStageB;
-      if (masked) take_step<S, true>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
-      else take_step<S, false>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+      char* st = ring + tslot * S::kStageB;
+      if (masked) {
+        const int tok = lane % S::kStep;
+        if (keep_nan_out<S>(st, lane, (lane < 16 || H == 1 ? k.good[0] : k.good[H - 1]) && j0 + tok < q.len) && lane == 0)
+          s_nan[warp] = min(s_nan[warp], j0);
+        take_step<S, true>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+      } else {
+        take_step<S, false>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+      }
       if (++tslot == S::kSlots) tslot = 0, tphase ^= 1;
       --in_flight;
       __syncwarp();
@@ -646,11 +709,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     __syncthreads();                           // also: every warp is done with the ring
     if (s_abort) break;                        // the same for the whole block
     float* merge = reinterpret_cast<float*>(big);
-    // 16-byte units of a row are permuted so that a quarter warp's stores differ in bank
-    auto unit_of = [](int r, int d) {
-      const int u = d / 4, cc = (r & 7) >> 1;
-      return D == 64 ? u ^ ((cc & 1) | (cc >> 1) << 2) : u ^ (cc | ((u >> 4) & 1) << 2);
-    };
+    auto unit_of = [](int r, int d) { return merge_unit<D>(r, d); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -668,6 +727,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
                           t.O[nt][n + 1][2 + y] * keep);
         }
       }
+    __syncwarp();
+    if (s_nan[warp] < kNone)
+      put_nan<S>(a, q.n, q.start, q.len, b, head, block, s_nan[warp], merge + (size_t)warp * S::kRows * D);
     __syncthreads();
     const bool opens = st0 == 0, closes = st1 == q.steps;
     const int slot = 2 * blockIdx.x + (opens ? 1 : 0);

@@ -12,7 +12,8 @@
 //                    a weight would pass 2^8, and O is rescaled (in tensor memory) only then
 //   warps 8-15       keys and values: 16-byte pieces from the pages, widened to f16 (exact) and
 //                    stored as 128-byte-swizzled tiles; slots past the end or in pages out of
-//                    range become 0
+//                    range become 0, and NaN codes of V in tiles that not every row sees whole
+//                    become finite (the softmax threads then put NaN into the rows that see them)
 //   warp 16          one thread issues the tensor-core products (kind::f16, f32 accumulation):
 //                    S = Q K^T (K-major tiles), O += P V (P from tensor memory, V as the tile's
 //                    rows, i.e. with the value dimension contiguous)
@@ -199,6 +200,12 @@ __device__ __forceinline__ int2 block_tiles(const Seq& q, int block, int group, 
   const int x = lo / kTile;
   return make_int2(x, max(x, (max(hi, 0) + kTile - 1) / kTile));
 }
+// Key tiles from `from` on and before `before` have keys that some row of the piece's block does not
+// see.
+struct Partly {
+  int from, before;
+};
+__device__ __forceinline__ bool partly(const Partly& p, int t) { return t >= p.from || t < p.before; }
 __device__ __forceinline__ int block_line(const Seq& q, int block, int group, int window) {
   const int2 t = block_tiles(q, block, group, window);
   return max(t.y - t.x, 1) + kSegmentCost;
@@ -301,6 +308,12 @@ __device__ __forceinline__ Piece walk_next(Walk* state, const AttentionArgs& a, 
   return p;
 }
 
+__device__ __forceinline__ Partly partly_seen(const Piece& p, int group, int window) {
+  const int lo = p.start + p.block * kBlock / group;       // the block's first and last rows' places
+  const int hi = p.start + (p.block * kBlock + p.R - 1) / group;
+  return {min(lo + 1, p.len) / kTile, window > 0 ? (hi - window + kTile) / kTile : 0};
+}
+
 template <int D>
 struct Smem {
   static constexpr int kQ = 128 * D * 2;       // one row tile of queries
@@ -324,6 +337,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   __shared__ Walk s_walk[16];
   __shared__ int2 s_issue;                     // the issuing thread's piece: key tiles (0: no more), row tiles
   __shared__ long long s_line[kThreads];
+  __shared__ volatile uint32_t s_nan[2][kConvert / 32];    // NaN codes that a widening warp kept out of V
+  __shared__ volatile int s_nan_from[kSoftmax / 32];       // a softmax warp's first key tile with such
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size;
@@ -507,6 +522,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         if (t < p.t1 && j < p.len) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
         return (int64_t)-1;
       };
+      const Partly part = partly_seen(p, group, a.window);
+      uint32_t nan = 0;
       int page_next = page_of(p.t0);           // of the tile after the one fetched from
       int64_t start = -1;
       auto fetch = [&](int t, int half, uint4 (&r)[kHalfN]) {   // half 0, 1: K's; 2, 3: V's
@@ -542,6 +559,22 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
           if ((h & 1) == 0 && ok)
             ok = wait_warp(h ? &s_vempty[kv & 1] : &s_kempty[kv & 1], ((kv >> 1) & 1) ^ 1, abort_flag, err);
           if (!ok) break;
+          if (h & 2 && partly(part, t)) {
+            if (h == 2) nan = 0;
+#pragma unroll
+            for (int i = 0; i < kHalfN; ++i)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t& w = x == 0 ? r[h][i].x : x == 1 ? r[h][i].y : x == 2 ? r[h][i].z : r[h][i].w;
+                const uint32_t m = e4m3_nan_bits(w);
+                w &= ~(m >> 7);                // a finite code, with a weight of 0 where it is not seen
+                nan |= m;
+              }
+            if (h == 3) {
+              nan = __reduce_or_sync(0xffffffffu, nan);
+              if (lane == 0) s_nan[kv & 1][warp - 8] = nan;
+            }
+          }
           char* dst = smem + (h & 2 ? S::kVAt : S::kKAt) + (kv & 1) * S::kKv + (piece >> 2) * S::kHalf;
 #pragma unroll
           for (int i = 0; i < kHalfN; ++i) {
@@ -573,7 +606,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
     const int log_p = 31 - __clz(P);
     uint32_t* counters = reinterpret_cast<uint32_t*>(ws + kCountersAt);
     float* stats = reinterpret_cast<float*>(ws + kStatsAt);
-    float4* part = reinterpret_cast<float4*>(ws + kRowsAt);
+    float4* part_rows = reinterpret_cast<float4*>(ws + kRowsAt);
     uint32_t sph = 0, jph = 0, kv = 0;         // phases; key tiles
     bool ok = true;
     // the softmax threads meet (bounded, like every wait here)
@@ -664,8 +697,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         };
         int page = page_of(p.t0), page_next = page_of(p.t0 + 1);
         Scales scales = scales_of(page);
-        const int place_lo = p.start + p.block * kBlock / group;             // the block's first and last rows
-        const int place_hi = p.start + (p.block * kBlock + p.R - 1) / group;
+        const Partly part = partly_seen(p, group, a.window);
+        if (lane == 0) s_nan_from[warp] = p.t1;
         for (int t = p.t0; t < p.t1; ++t) {
           const bool there = page >= 0 && page < a.c.num_pages;
           __syncwarp();
@@ -689,8 +722,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
           }
           if (warp_live) {
             const int j0 = t * kTile;
-            bool masked = gone || j0 + kTile > place_lo + 1 || j0 + kTile > p.len;
-            if (a.window > 0) masked |= j0 <= place_hi - a.window;
+            const bool masked = gone || partly(part, t);
             // keys j0 + x with x in [x0, x1) are the row's; groups without a page are nobody's
             const int x1 = min(place + 1, p.len) - j0;
             const int x0 = a.window > 0 ? place - a.window + 1 - j0 : -j0;
@@ -797,6 +829,11 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
             }
             tmem_wait_st();
           }
+          if (partly(part, t)) {
+            if (!(ok = wait_warp(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
+            const uint32_t bad = lane < kConvert / 32 ? s_nan[kv & 1][lane] : 0;
+            if (__any_sync(0xffffffffu, bad != 0) && lane == 0 && s_nan_from[warp] > t) s_nan_from[warp] = t;
+          }
           if (warp == 1 && !(ok = wait_warp(&s_vfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
           ++kv;
           if (warp == 2 && t + 1 < p.t1 && !(ok = wait_warp(&s_kfull[kv & 1], (kv >> 1) & 1, abort_flag, err))) break;
@@ -853,8 +890,23 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
           } else if (mine) {
 #pragma unroll
             for (int x = 0; x < 32; x += 4)
-              part[((size_t)slot * (D / 4) + i * 8 + x / 4) * kBlock + r] =
+              part_rows[((size_t)slot * (D / 4) + i * 8 + x / 4) * kBlock + r] =
                   make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          }
+        }
+        __syncwarp();
+        if (nt > 0 && s_nan_from[warp] < p.t1 && mine) {
+          // NaN codes kept out of the products, from the pages, into the row if it sees them
+          const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
+          const int j1 = min(min(place + 1, p.len), p.t1 * kTile);
+#pragma unroll 1
+          for (int j = max(s_nan_from[warp] * kTile, a.window > 0 ? place - a.window + 1 : 0); j < j1; ++j) {
+            const int page = table[j >> log_p];
+            if (page < 0 || page >= a.c.num_pages) continue;
+            each_nan<D>(a.c.v_codes + page * a.c.page_stride + ((int64_t)p.head * P + (j & (P - 1))) * D, [&](int d) {
+              if (whole) reinterpret_cast<uint16_t*>(column_at(r, d / 8))[d % 8] = 0x7fff;      // of either type
+              else reinterpret_cast<float*>(&part_rows[((size_t)slot * (D / 4) + d / 4) * kBlock + r])[d % 4] = NAN;
+            });
           }
         }
         if (whole) store_rows();
@@ -896,7 +948,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
               const float k = exp2_approx(__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top);
               float4 o[8];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] = __ldcg(part + (slot_of(i) * (D / 4) + d / 4 + x) * kBlock + r);
+              for (int x = 0; x < 8; ++x) o[x] = __ldcg(part_rows + (slot_of(i) * (D / 4) + d / 4 + x) * kBlock + r);
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 v[4 * x] = fmaf(o[x].x, k, v[4 * x]), v[4 * x + 1] = fmaf(o[x].y, k, v[4 * x + 1]);

@@ -105,6 +105,19 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Which of a word's four E4M3 codes are NaN (0x7f, 0xff): the top bit of each such byte.
+__device__ __forceinline__ uint32_t e4m3_nan_bits(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// Calls put(d) for every value d of a row of D codes that is NaN.
+template <int D, class F>
+__device__ __forceinline__ void each_nan(const uint8_t* codes, F&& put) {
+#pragma unroll 1
+  for (int d = 0; d < D; d += 4)
+    for (uint32_t m = e4m3_nan_bits(*reinterpret_cast<const uint32_t*>(codes + d)); m; m &= m - 1)
+      put(d + (__ffs(m) - 1) / 8);
+}
+
 // Loads that stay where they are written: the compiler may move an ordinary load behind a wait, next
 // to its use, and expose its latency there.
 __device__ __forceinline__ uint4 load_ahead(const void* at, bool there) {   // zeros if not there

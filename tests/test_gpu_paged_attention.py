@@ -320,3 +320,52 @@ def test_tiny_queries_and_zero_keys_hide_what_a_row_does_not_see(pairs, window):
         return tuple(p)
     check(rng, pairs, 64, 2, 2, 128, "bf16", window=window, amp=2.0 ** -72, planes=planes)
     check(rng, pairs, 64, 2, 2, 128, "bf16", window=window, amp=0.0, planes=planes)
+
+
+# ---- NaN values that only some rows see ----
+@pytest.mark.parametrize("D,page,heads,group,dtype,pairs,window", [
+    (128, 64, 2, 4, "bf16", [(100, 1), (63, 1), (500, 1)], 50),         # one token, before its window
+    (64, 16, 1, 1, "f16", [(100, 7), (0, 5)], 0),                       # one, two, three row tiles
+    (128, 32, 1, 3, "bf16", [(100, 5), (31, 4)], 0),
+    (64, 64, 2, 4, "bf16", [(200, 6), (63, 5)], 9),
+    (256, 32, 1, 2, "f16", [(70, 6), (0, 9)], 0),
+    (256, 16, 1, 1, "bf16", [(70, 3), (0, 9)], 20),
+    (128, 64, 1, 2, "bf16", [(300, 100), (0, 150), (64, 3)], 0),        # many rows, and few beside them
+    (64, 16, 1, 3, "f16", [(130, 90)], 0),
+    (64, 32, 2, 4, "bf16", [(400, 300), (10, 20)], 70),
+    (128, 128, 1, 1, "f16", [(1000, 300)], 129)])
+def test_nan_values_reach_only_the_rows_that_see_them(D, page, heads, group, dtype, pairs, window):
+    """V codes of NaN at places that some new tokens see and others do not (later ones, or before
+    the window): those who see the key have NaN in that value, all else is as if the code were 0."""
+    rng = np.random.default_rng(39)
+    batch = Batch(rng, pairs, page)
+    planes = cache_planes(rng, batch.num_pages, heads, page, D)
+    stale_nan(planes, batch)
+    nan = np.zeros((batch.T, heads * group, D), bool)
+    bad = planes[2].copy()
+    for b, (past, n) in enumerate(pairs):
+        end = past + n
+        places = {end - 1, past + n // 2, past}
+        if window:                               # just outside and inside some rows' windows
+            places |= {p for p in (past - window, past - window + 1, end - 1 - window) if p >= 0}
+        for at in places:
+            for d, h in ((int(rng.integers(D)), int(rng.integers(heads))), (D - 1, 0), (0, heads - 1)):
+                slot = batch.table[b, at // page], h, at % page, d
+                planes[2][slot], bad[slot] = 0, int(rng.choice([0x7F, 0xFF]))
+                for i in range(n):
+                    if at <= past + i and (window == 0 or at > past + i - window):
+                        nan[batch.offsets[b] + i, h * group:(h + 1) * group, d] = True
+    q = activations(rng, (batch.T, heads * group, D), dtype)
+    want, wl, eo, el = oracle.attention(q.double().numpy(), *planes, batch.offsets, batch.lens,
+                                        batch.table, D ** -0.5, window)
+    clean, cl, _ = run(q.cuda(), device_cache(planes), batch.device(), heads * group, D, D ** -0.5, window)
+    planes = planes[:2] + (bad,) + planes[3:]
+    out, lse, ws = run(q.cuda(), device_cache(planes), batch.device(), heads * group, D, D ** -0.5, window)
+    assert moe.get_device_error(ws) == 0
+    assert np.array_equal(torch.isnan(out).cpu().numpy(), nan)
+    keep = torch.from_numpy(~nan).cuda()
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse, cl)
+    got = clean.double().cpu().numpy()
+    rel, floor = ROUND[dtype]
+    assert np.all(np.abs(got - want) <= eo + rel * (np.abs(want) + eo) + floor)
+    assert np.all(np.abs(cl.double().cpu().numpy() - wl) <= el + 1e-6)
