@@ -897,10 +897,15 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         __syncwarp();
         if (nt > 0 && s_nan_from[warp] < p.t1 && mine) {
           // NaN codes kept out of the products, from the pages, into the row if it sees them
+          const Partly part = partly_seen(p, group, a.window);
           const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
           const int j1 = min(min(place + 1, p.len), p.t1 * kTile);
 #pragma unroll 1
           for (int j = max(s_nan_from[warp] * kTile, a.window > 0 ? place - a.window + 1 : 0); j < j1; ++j) {
+            if (!partly(part, j / kTile)) {                // every row sees this tile: its NaN are there
+              j = part.from * kTile - 1;
+              continue;
+            }
             const int page = table[j >> log_p];
             if (page < 0 || page >= a.c.num_pages) continue;
             each_nan<D>(a.c.v_codes + page * a.c.page_stride + ((int64_t)p.head * P + (j & (P - 1))) * D, [&](int d) {
