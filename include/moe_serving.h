@@ -44,7 +44,8 @@ enum { MOE_DEVERR_PAGE = 4, MOE_DEVERR_POSITION = 8, MOE_DEVERR_TOKEN = 16, MOE_
  *   codes   E4M3 [num_pages][kv_heads][page_size][head_dim]; page p of either plane starts
  *           page_stride bytes after page p-1 (a multiple of 16, at least
  *           kv_heads*page_size*head_dim, so both planes can share one allocation)
- *   scales  f32 [num_pages][kv_heads], contiguous, positive and finite
+ *   scales  f32 [num_pages][kv_heads], contiguous, positive and finite; V's within
+ *           [2^-100, 2^120] (an append writes [2^-64, 2^119])
  *   value(page, head, slot, d) = E4M3(code) * scale[page][head]
  * page_size is 16, 32, 64 or 128; head_dim 64, 128 or 256; code planes 16-byte aligned. */
 typedef struct moe_kv_cache {

@@ -21,7 +21,9 @@
 //                  of keys for one value come from two rows' bytes by byte permutes
 // With f = scale * k_scale * log2 e and v = log2 v_scale of a key's page, the weight that meets
 // V's codes is w = 2^(s f + v - M) and the softmax sum adds w / v_scale, so the value scale
-// costs nothing per element. M follows the running maximum of s f + v lazily: it moves only when
+// costs nothing per element. Where scales lie far apart a quiet page's w may be below the least float
+// while its share of the sum is not: from its first scale outside [2^-kFar, 2^kFar] on a warp takes
+// half the exponent, x = 2^((s f + v - M) / 2), and adds (x / v_scale) x. M follows the running maximum of s f + v lazily: it moves only when
 // a weight would pass 2^8, which leaves f16 weights their full precision and makes rescaling of
 // the accumulators rare. w is rounded to f16 (2^-11), sums and accumulators are f32.
 //
@@ -45,6 +47,9 @@ constexpr int kMaxGrid = 512;              // partial slots of the workspace
 constexpr int kMaxRows = 24;
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
+// With value scales within 2^(2 kFar) of one another a weight that is flushed to 0 (below 2^-126) has
+// less than 2^-46 of the sum.
+constexpr float kFar = 40.0f;
 // What a segment costs beside its steps (queries, first copies, the warps' rows meeting), in
 // steps: pieces of the line are equal with it counted.
 constexpr int kSegmentCost = 12;
@@ -166,7 +171,9 @@ __device__ long long block_scan(long long v, long long* s_sum, long long* before
 // A warp's keys: which page each half-step (16 tokens) lies in, its scales, for 32 of them at a
 // time (lane l holds half-step l of the batch).
 struct Keys {
-  float f, v, inv;              // (all 0 without a page) scale * k_scale * log2 e; log2 v_scale; 1 / v_scale
+  // (all 0 without a page) scale * k_scale * log2 e; log2 v_scale; 1 / v_scale, negative from the
+  // warp's first far scale on
+  float f, v, inv;
 };
 
 // A lane's share of a block of rows: query fragments, accumulators, and what the running softmax
@@ -191,7 +198,7 @@ struct StepKeys {
 };
 
 // One step of STEP keys for all rows; `masked` where a key of it is hidden from a row or is not
-// there.
+// there, or a value scale is or was far from the others.
 template <class S, bool masked>
 __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepKeys<S::kHalves>& k,
                                           const char* st, const char* s_q, int lane, int j0, int len,
@@ -267,9 +274,10 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
         for (int o = 4; o < 32; o <<= 1) top[nt][y] = fmaxf(top[nt][y], __shfl_xor_sync(0xffffffffu, top[nt][y], o));
         const bool unset = t.M[nt][y] == kNoMax;           // no key of the row so far
         const float up = unset ? (top[nt][y] > -INFINITY ? top[nt][y] : 0.0f) : fmaxf(top[nt][y], 0.0f);
-        const float keep = unset ? 0.0f : exp2_approx(-up);
+        // (the sum may be far from 1: its factor in two halves)
+        const float half = unset ? 0.0f : exp2_approx(-0.5f * up), keep = half * half;
         if (!unset || top[nt][y] > -INFINITY) t.M[nt][y] = (unset ? 0.0f : t.M[nt][y]) + up;
-        t.L[nt][y] *= keep;
+        t.L[nt][y] = t.L[nt][y] * half * half;
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) t.O[nt][n][y] *= keep, t.O[nt][n][2 + y] *= keep;
 #pragma unroll
@@ -284,9 +292,17 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sc[nt][h][x] = exp2_approx(sc[nt][h][x]);
+      for (int x = 0; x < 4; ++x) {
+        sc[nt][h][x] = exp2_approx(masked ? 0.5f * sc[nt][h][x] : sc[nt][h][x]);
+        if (masked) {
+          t.L[nt][x & 1] = fmaf(sc[nt][h][x] * fabsf(k.inv[h]), sc[nt][h][x], t.L[nt][x & 1]);
+          sc[nt][h][x] *= sc[nt][h][x];
+        }
+      }
+      if (!masked) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) t.L[nt][y] = fmaf(k.inv[h], sc[nt][h][y] + sc[nt][h][2 + y], t.L[nt][y]);
+        for (int y = 0; y < 2; ++y) t.L[nt][y] = fmaf(k.inv[h], sc[nt][h][y] + sc[nt][h][2 + y], t.L[nt][y]);
+      }
       pb[nt][h][0] = transpose8(pack_f16(sc[nt][h][0], sc[nt][h][1]));
       pb[nt][h][1] = transpose8(pack_f16(sc[nt][h][2], sc[nt][h][3]));
     }
@@ -395,6 +411,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   __shared__ volatile int s_abort;
   __shared__ float s_rowf[S::kRows], s_m[kWarps][S::kRows], s_l[kWarps][S::kRows];
   __shared__ int s_last;
+  __shared__ volatile char s_far[kWarps][32];  // whether the warp has met a far value scale: a lane's own
   constexpr int kNone = 0x7fffffff;
   __shared__ volatile int s_nan[kWarps];       // first key of the warp's first step with NaN codes kept out
   char* big = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -490,6 +507,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     // A batch's pages are read a batch ahead, its scales as its first copy is issued; they become
     // factors when its first step is taken.
     Keys cur = {0.f, 0.f, 0.f};
+    s_far[warp][lane] = 0;
     int page_of_lane = -1, page_ahead = -1;
     float k_scale = 0.0f, v_scale = 0.0f;
     auto key_of = [&](int batch) {             // the lane's first key of a batch, -1: none
@@ -520,6 +538,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         k.v = log2f(vs);
         k.inv = __fdividef(1.0f, vs);
       }
+      if (__any_sync(0xffffffffu, fabsf(k.v) > kFar)) s_far[warp][lane] = 1;
+      if (s_far[warp][lane]) k.inv = -k.inv;
       return k;
     };
     int have = 0;                              // key batches loaded
@@ -667,8 +687,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         k.f[h] = __shfl_sync(0xffffffffu, cur.f, src + h);
         k.v[h] = __shfl_sync(0xffffffffu, cur.v, src + h);
         k.inv[h] = __shfl_sync(0xffffffffu, cur.inv, src + h);
-        k.good[h] = k.inv[h] > 0.0f;
-        masked |= !k.good[h];
+        k.good[h] = k.inv[h] != 0.0f;
+        masked |= !(k.inv[h] > 0.0f);
       }
       char* st = ring + tslot * S::kStageB;
       if (masked) {
@@ -761,7 +781,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       for (int w = 0; w < kWarps; ++w) {
         const float4 o = *reinterpret_cast<const float4*>(merge + ((size_t)w * S::kRows + r) * D + unit * 4);
         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - top), sum);
+        const float half = exp2_approx(0.5f * (s_m[w][r] - top));
+        sum = fmaf(s_l[w][r] * half, half, sum);
       }
       if (opens && closes) {
         store_row(r, d, v, top, sum);
@@ -805,13 +826,13 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
           for (int p = lane + 32; p < np; p += 32) top = fmaxf(top, __ldcg(stat(p, r)));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float k0 = exp2_approx(m[n] - top);
-          sum = l[n] * k0;
-          if (lane < np) fac[lane * S::kRows + r] = k0;
+          const float k0 = exp2_approx(0.5f * (m[n] - top));
+          sum = l[n] * k0 * k0;
+          if (lane < np) fac[lane * S::kRows + r] = k0 * k0;
           for (int p = lane + 32; p < np; p += 32) {
-            const float k = exp2_approx(__ldcg(stat(p, r)) - top);
-            fac[p * S::kRows + r] = k;
-            sum = fmaf(__ldcg(stat(p, r) + kMaxRows), k, sum);
+            const float k = exp2_approx(0.5f * (__ldcg(stat(p, r)) - top));
+            fac[p * S::kRows + r] = k * k;
+            sum = fmaf(__ldcg(stat(p, r) + kMaxRows) * k, k, sum);
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

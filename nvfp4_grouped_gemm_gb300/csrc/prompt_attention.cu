@@ -51,6 +51,7 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsIssue <= 5 * kRegsLaunc
 static_assert(kRegsSoftmax >= kRegsLaunch && kRegsConvert <= kRegsLaunch && kRegsIssue <= kRegsLaunch, "");
 constexpr float kNoMax = -1e30f;
 constexpr float kLazy = 8.0f;
+constexpr float kFar = 40.0f;                  // of value scales, as in paged_attention.cu
 // A segment's fixed cost (queries, first tiles, storing rows) in key tiles.
 constexpr int kSegmentCost = 3;
 
@@ -115,6 +116,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -695,20 +701,20 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
           return Scales{__uint_as_float(load_ahead(a.c.k_scales + sc, there, 0u)),
                         __uint_as_float(load_ahead(a.c.v_scales + sc, there, 0u))};
         };
+        bool far = false;                        // a value scale so far was outside [2^-kFar, 2^kFar]
         int page = page_of(p.t0), page_next = page_of(p.t0 + 1);
         Scales scales = scales_of(page);
         const Partly part = partly_seen(p, group, a.window);
         if (lane == 0) s_nan_from[warp] = p.t1;
         for (int t = p.t0; t < p.t1; ++t) {
           const bool there = page >= 0 && page < a.c.num_pages;
+          const float vs = fminf(fmaxf(scales.v, 0x1p-100f), 0x1p120f), v = log2f(vs);
           __syncwarp();
-          if (lane < 8) {
-            const float vs = fminf(fmaxf(scales.v, 0x1p-100f), 0x1p120f);
-            s_coef[warp][lane] = there ? make_float4(a.scale * 1.4426950408889634f * scales.k, log2f(vs),
-                                                     __fdividef(1.0f, vs), 1.0f)
+          if (lane < 8)
+            s_coef[warp][lane] = there ? make_float4(a.scale * 1.4426950408889634f * scales.k, v, __fdividef(1.0f, vs), 1.0f)
                                        : make_float4(1.f, 0.f, 0.f, 0.f);   // no page: weights of -inf
-          }
           __syncwarp();
+          far |= __any_sync(0xffffffffu, there && fabsf(v) > kFar);
           const bool gone = !__all_sync(0xffffffffu, there);
           page = page_next;
           scales = scales_of(page);
@@ -727,8 +733,10 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
             const int x1 = min(place + 1, p.len) - j0;
             const int x0 = a.window > 0 ? place - a.window + 1 - j0 : -j0;
             // The weights are taken with the M that there is, from one reading of S, and stand if none
-            // passes 2^8. Tiles where that is not to be expected, or with hidden keys, take two.
-            bool twice = masked || t == p.t0 || __any_sync(0xffffffffu, fabsf(M) > 1e6f);
+            // passes 2^8. Tiles where that is not to be expected, with hidden keys, or with value scales
+            // far apart take two, and weights as squares: x = 2^((s f + v - M) / 2), x x of the values and
+            // (x / v_scale) x of the sum, which a quiet page's x x below the least float would lose.
+            bool twice = masked || far || t == p.t0 || __any_sync(0xffffffffu, fabsf(M) > 1e6f);
             if (!twice) {
               uint32_t w[64];
               float most = -INFINITY, sum = L;
@@ -777,9 +785,10 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 top = fmaxf(top, fmaf(max16(s + 16), c1.x * rowf, c1.y));
               }
               if (__any_sync(0xffffffffu, top > M + kLazy)) {
-                const float to = fmaxf(M, top), keep = exp2_approx(M - to);
+                // (the sum may be far from 1: its factor in two halves)
+                const float to = fmaxf(M, top), half = exp2_approx(0.5f * (M - to)), keep = half * half;
                 M = to;
-                L *= keep;
+                L = L * half * half;
                 if (t > p.t0) {
 #pragma unroll 1
                   for (int i = 0; i < D / 16; ++i) {
@@ -792,7 +801,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 }
               }
               // scores so large that their rounding alone could pass 2^8 end there
-              const float cap = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax) ? kLazy : INFINITY;
+              const float cap = __any_sync(0xffffffffu, fabsf(M) > 1e6f && M > kNoMax) ? 0.5f * kLazy : INFINITY;
               // weights; columns 16 ch .. of P lie over columns of S that are already read
 #pragma unroll 1
               for (int ch = 0; ch < 4; ++ch) {
@@ -802,7 +811,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const float f = (h ? c1.x : c0.x) * rowf, d = (h ? c1.y : c0.y) - M;
+                  const float f = 0.5f * (h ? c1.x : c0.x) * rowf, d = 0.5f * ((h ? c1.y : c0.y) - M);
                   const uint64_t ff = pair(f, f), dd = pair(d, d);
 #pragma unroll
                   for (int x = 16 * h; x < 16 * h + 16; x += 2) unpair(fma2(pair(s[x], s[x + 1]), ff, dd), s[x], s[x + 1]);
@@ -811,18 +820,21 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                  const float inv = h ? c1.z : c0.z;
+                  const uint64_t ii = pair(inv, inv);
                   uint64_t acc = 0;
 #pragma unroll
                   for (int x = 0; x < 16; x += 2) {
                     float e0 = s[16 * h + x], e1 = s[16 * h + x + 1];
                     e0 = e0 > cap ? cap : e0, e1 = e1 > cap ? cap : e1;
-                    e0 = exp2_approx(e0), e1 = exp2_approx(e1);
-                    acc = add2(acc, pair(e0, e1));
+                    const uint64_t xx = pair(exp2_approx(e0), exp2_approx(e1));
+                    acc = fma2(mul2(xx, ii), xx, acc);
+                    unpair(mul2(xx, xx), e0, e1);
                     w[h * 8 + x / 2] = pack_f16(e0, e1);
                   }
                   float l0, l1;
                   unpair(acc, l0, l1);
-                  L = fmaf(h ? c1.z : c0.z, l0 + l1, L);
+                  L += l0 + l1;
                 }
                 tc_st16(s_col + ch * 16, w);
               }
@@ -939,9 +951,10 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
 #pragma unroll 2
           for (int i = 0; i < p.np; ++i) top = fmaxf(top, __ldcg(stats + slot_of(i) * 2 * kBlock + r));
 #pragma unroll 2
-          for (int i = 0; i < p.np; ++i)
-            sum = fmaf(__ldcg(stats + (slot_of(i) * 2 + 1) * kBlock + r),
-                       exp2_approx(__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top), sum);
+          for (int i = 0; i < p.np; ++i) {
+            const float half = exp2_approx(0.5f * (__ldcg(stats + slot_of(i) * 2 * kBlock + r) - top));
+            sum = fmaf(__ldcg(stats + (slot_of(i) * 2 + 1) * kBlock + r) * half, half, sum);
+          }
           const float k1 = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll 1
           for (int d = 0; d < D; d += 32) {

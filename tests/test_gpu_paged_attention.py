@@ -369,3 +369,39 @@ def test_nan_values_reach_only_the_rows_that_see_them(D, page, heads, group, dty
     rel, floor = ROUND[dtype]
     assert np.all(np.abs(got - want) <= eo + rel * (np.abs(want) + eo) + floor)
     assert np.all(np.abs(cl.double().cpu().numpy() - wl) <= el + 1e-6)
+
+
+# ---- value scales further apart than float32's exponents ----
+@pytest.mark.parametrize("order", ["mixed", "rising", "falling", "by_fours"])
+@pytest.mark.parametrize("D,page,heads,group,pairs", [
+    (64, 16, 2, 4, [(700, 3), (80, 1)]), (128, 32, 1, 8, [(6000, 1), (300, 1)]),
+    (256, 16, 1, 2, [(500, 3), (90, 1)]), (64, 16, 1, 3, [(300, 100)]),
+    (128, 64, 1, 2, [(3000, 90), (400, 1)])])
+def test_quiet_values_keep_their_share_of_the_sum(D, page, heads, group, pairs, order):
+    """Pages of zeros (scale 2^-64) and quiet ones beside pages near the largest scale an append
+    writes: the softmax's sum is over all keys alike, whatever their values' scale."""
+    rng = np.random.default_rng(40)
+    batch = Batch(rng, pairs, page)
+    planes = list(cache_planes(rng, batch.num_pages, heads, page, D))
+    for row in batch.table:
+        for i, number in enumerate(row[row >= 0]):
+            loud = {"mixed": rng.random() < 0.4, "rising": i >= 3, "falling": i < 3,
+                    "by_fours": i % 4 < 2}[order]
+            planes[3][number] = np.float32(2.0 ** (rng.integers(95, 105) if loud else -64))
+            if not loud and rng.random() < 0.5:
+                planes[2][number] = 0
+    stale_nan(planes, batch)
+    for amp in (1.0, 8.0):
+        q = activations(rng, (batch.T, heads * group, D), "bf16", amp)
+        want, wl, eo, el = oracle.attention(q.double().numpy(), *planes, batch.offsets, batch.lens,
+                                            batch.table, D ** -0.5)
+        out, lse, ws = run(q.cuda(), device_cache(planes), batch.device(), heads * group, D, D ** -0.5)
+        assert moe.get_device_error(ws) == 0
+        got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        rel, floor = ROUND["bf16"]
+        # the exponents here reach 2^8, where float32 rounds by 2^-17: three times, in natural logarithms
+        # less than 2^-16 beside the bound for scores alone; the values' weights have it twice
+        eo = eo + 2.0 ** -15 * np.abs(want)
+        tol = eo + rel * (np.abs(want) + eo) + floor
+        assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+        assert np.all(np.abs(gl - wl) <= el + 1e-6 + 2.0 ** -16), float(np.max(np.abs(gl - wl)))
