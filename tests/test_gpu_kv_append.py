@@ -184,3 +184,11 @@ def test_nan_stays_in_its_own_code():
     got[0, 0, 2, 7] &= 0x7F
     assert np.array_equal(got, codes)
     assert np.array_equal(cache.v_scales.cpu().numpy(), scales)
+
+
+@pytest.mark.parametrize("D,qh,inter,dtype,pairs", [
+    (64, 13, False, "bf16", [(0, 5000), (17, 1203)]),                  # 2, 4 and 8 query heads per thread,
+    (128, 7, True, "f16", [(5, 9000), (0, 1), (100, 2203)]),           # the last group short
+    (256, 11, False, "bf16", [(0, 7101)])])
+def test_many_tokens_with_odd_numbers_of_query_heads(D, qh, inter, dtype, pairs):
+    assert check(np.random.default_rng(12), pairs, 128, 1, qh, D, D, inter, dtype) == 0

@@ -185,3 +185,11 @@ def test_the_layer_object_s_memory_follows_the_largest_call():
     for T in (96, 5, 64, 1):
         y = lin.forward(xs[:T])
         assert np.all(np.abs(y.double().cpu().numpy() - want[:T]) <= tol[:T])
+
+
+@pytest.mark.parametrize("T,N,K,xd", [(513, 40, 4096, "bf16"), (600, 33, 1024, "bf16"),
+                                      (515, 20, 8192, "f16"), (513, 17, 16384, "bf16"),
+                                      (514, 18, 32768, "bf16"), (513, 16, 65536, "bf16"),
+                                      (512, 21, 1056, "bf16"), (700, 50, 352, "f16")])
+def test_more_tokens_than_are_prepared_at_once(T, N, K, xd):
+    check(np.random.default_rng(T + N + K), T, N, K, xd, "f32")

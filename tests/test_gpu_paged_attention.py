@@ -405,3 +405,31 @@ def test_quiet_values_keep_their_share_of_the_sum(D, page, heads, group, pairs, 
         tol = eo + rel * (np.abs(want) + eo) + floor
         assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
         assert np.all(np.abs(gl - wl) <= el + 1e-6 + 2.0 ** -16), float(np.max(np.abs(gl - wl)))
+
+
+# ---- forms that large batches and long sequences run ----
+@pytest.mark.parametrize("D,page,heads,group,dtype", [
+    (128, 64, 8, 4, "bf16"), (64, 16, 4, 8, "f16"), (256, 32, 4, 2, "bf16"), (128, 16, 3, 1, "f16")])
+def test_one_token_of_many_sequences(D, page, heads, group, dtype):
+    """More segments (sequences times key heads) than there are SMs, one row tile each."""
+    rng = np.random.default_rng(41)
+    pairs = [(int(n), 1) for n in np.exp(rng.uniform(0, np.log(700), 64)).astype(int)] + [(0, 0), (3000, 1)]
+    check(rng, pairs, page, heads, group, D, dtype)
+    check(rng, pairs, page, heads, group, D, dtype, window=37)
+
+
+@pytest.mark.parametrize("D,n", [(128, 30011), (256, 14003), (64, 40000)])
+def test_one_sequence_in_more_pieces_than_a_warp_has_lanes(D, n):
+    check(np.random.default_rng(42), [(n, 1)], 64, 1, 2, D, "bf16")
+
+
+@pytest.mark.parametrize("D,page,window", [(128, 64, 50), (64, 16, 9), (256, 32, 70)])
+def test_nan_values_in_many_sequences(D, page, window):
+    pairs = [(int(n), 1) for n in np.linspace(0, 400, 60)]
+    test_nan_values_reach_only_the_rows_that_see_them(D, page, 4, 2, "bf16", pairs, window)
+
+
+@pytest.mark.parametrize("order", ["mixed", "rising", "falling"])
+def test_quiet_values_in_long_and_in_many_sequences(order):
+    test_quiet_values_keep_their_share_of_the_sum(128, 64, 1, 2, [(30011, 1)], order)
+    test_quiet_values_keep_their_share_of_the_sum(64, 16, 4, 2, [(int(n), 1) for n in np.linspace(0, 400, 60)], order)

@@ -130,3 +130,21 @@ def test_padded_rows():
                          torch.from_numpy(us).cuda(), out, cnt, zeros_ws(moe.verify_workspace_bytes(3, 333)),
                          draft_probs=dp.cuda()[..., :333])
     assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(cnt.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("B,V,dtype", [(64, 20011, "f32"), (130, 20011, "bf16"), (61, 41000, "f16"),
+                                       (130, 24576, "f32")])
+def test_rows_of_several_chunks_per_block(B, V, dtype):
+    """Batches large enough for the larger chunks, one and several of them per block."""
+    rng = np.random.default_rng(B + V)
+    ids, t, d, ua, us = draw(rng, B, 2, V, dtype)
+    check(ids, t, d, ua, us, n_draft=rng.integers(0, 3, B).astype(np.int32), calls=1)
+    check(ids, t, None, ua, us, calls=1)
+    # nothing left after the difference: every chunk of the target is summed again
+    check(ids, t, t[:, :2].clone(), np.ones_like(ua), us)
+
+
+def test_nothing_left_after_the_difference_in_a_long_row():
+    rng = np.random.default_rng(6)
+    ids, t, _, ua, us = draw(rng, 3, 2, 9001, "f32")
+    check(ids, t, t[:, :2].clone(), np.ones_like(ua), us)
