@@ -345,56 +345,47 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
     }
 }
 
-// Makes the NaN codes among a step's values finite (a lane per token, two at D = 256; `there`: the token
-// is). Whether there were any. A pass of its own over the stage, so that the products' registers stay theirs.
+// Makes the NaN codes among a masked step's values finite and sets the bits of those that the warp's rows
+// (at places[row]) see, bits[row][value]; *any: whether some were found (0: the bits are not valid yet).
+// `there`: the lane's key is (a lane per key, at D = 256 two). A pass and a call of its own, which leaves
+// nothing in registers (64 sequences of 100 to 16000 tokens 73.9 us; with the pages read again at the end
+// instead of bits 75.0).
 template <class S>
-__device__ __forceinline__ bool keep_nan_out(char* st, int lane, bool there) {
-  constexpr int kChunks = S::kPlaneB / 16 / 32;
-  char* row = st + S::kPlaneB + (S::D == 256 ? (lane >> 4) * (S::kStep * 128) + (lane & 15) * 128 : lane * S::kRowB);
+__device__ __noinline__ void keep_nan_out(char* st, int lane, bool there, int j0, int window, const int* places,
+                                          uint32_t* bits, volatile int* any) {
+  constexpr int D = S::D, kWords = D / 32, kChunks = S::kPlaneB / 16 / 32;
+  const int sub = D == 256 ? lane >> 4 : 0, tok = D == 256 ? lane & 15 : lane;
+  char* row = st + S::kPlaneB + sub * (S::kStep * 128) + tok * S::kRowB;
   uint32_t bad = 0;
 #pragma unroll 2
   for (int i = 0; i < kChunks; ++i) {
     const uint4 v = *reinterpret_cast<const uint4*>(row + ((i + lane) % kChunks) * 16);
     bad |= e4m3_nan_bits(v.x) | e4m3_nan_bits(v.y) | e4m3_nan_bits(v.z) | e4m3_nan_bits(v.w);
   }
-  if (!__any_sync(0xffffffffu, there && bad != 0)) return false;
+  if (!__any_sync(0xffffffffu, there && bad != 0)) return;
+  const bool first = *any == 0;
+  __syncwarp();
 #pragma unroll 1
-  for (int i = 0; i < kChunks * 4; ++i) {
+  for (int i = lane; first && i < S::kRows * kWords; i += 32) bits[i] = 0;
+  if (lane == 0) *any = 1;
+  __syncwarp();
+  const int swz = D == 64 ? (tok >> 1) & 3 : tok & 7;
+#pragma unroll 1
+  for (int i = 0; i < kChunks * 4; ++i) {        // words of the row as they lie
     uint32_t& w = reinterpret_cast<uint32_t*>(row)[i];
-    w &= ~(e4m3_nan_bits(w) >> 7);               // with a weight of 0 where the key is not seen
+    const uint32_t m = e4m3_nan_bits(w);
+    if (m == 0) continue;
+    w &= ~(m >> 7);                              // with a weight of 0 where the key is not seen
+    const uint32_t four = (m >> 7 & 1) | (m >> 14 & 2) | (m >> 21 & 4) | (m >> 28 & 8);
+    const int d = sub * 128 + ((i / 4) ^ swz) * 16 + (i % 4) * 4;
+#pragma unroll 1
+    for (int r = 0; there && r < S::kRows; ++r)
+      if (j0 + tok <= places[r] && (window == 0 || j0 + tok > places[r] - window))
+        atomicOr(bits + r * kWords + d / 32, four << (d % 32));
   }
   // plain writes to the ring's memory come before the next copies into it
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
-  return true;
-}
-// Where the rows that meet have values d .. d+3 of row r: 16-byte units of a row are permuted so
-// that a quarter warp's stores differ in bank.
-template <int D>
-__device__ __forceinline__ int merge_unit(int r, int d) {
-  const int u = d / 4, cc = (r & 7) >> 1;
-  return D == 64 ? u ^ ((cc & 1) | (cc >> 1) << 2) : u ^ (cc | ((u >> 4) & 1) << 2);
-}
-// NaN codes kept out of the products, from the pages: a lane per key of the warp's steps from key j0 on,
-// into those of the warp's rows that see it (all to the sequence's end: a row has the NaN of a key that
-// it sees in another CTA's piece anyway). A call of its own: it is hardly ever made, and in line its
-// registers cost the steps theirs (64 sequences: 79 us, 76.8 so).
-template <class S>
-__device__ __noinline__ void put_nan(const AttentionArgs& a, int n, int start, int len, int b, int head, int block,
-                                     int j0, float* rows) {
-  constexpr int D = S::D;
-  const int lane = threadIdx.x & 31, P = a.c.page_size, group = a.q_heads / a.c.kv_heads;
-  const int R = min(S::kRows, n * group - block * S::kRows);
-  for (int j = j0 + lane; lane < S::kStep && j < len; j += S::kWarps * S::kStep) {
-    const int page = a.b.page_table[(int64_t)b * a.b.table_stride + j / P];
-    if (page < 0 || page >= a.c.num_pages) continue;
-    each_nan<D>(a.c.v_codes + page * a.c.page_stride + (int64_t)(head * P + j % P) * D, [&](int d) {
-      for (int r = 0; r < R; ++r) {
-        const int place = start + (block * S::kRows + r) / group;
-        if (j <= place && (a.window == 0 || j > place - a.window)) rows[r * D + merge_unit<D>(r, d) * 4 + d % 4] = NAN;
-      }
-    });
-  }
 }
 
 template <class S>
@@ -409,11 +400,12 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   __shared__ int s_seq;
   __shared__ long long s_first;
   __shared__ volatile int s_abort;
+  __shared__ int s_place[S::kRows];
   __shared__ float s_rowf[S::kRows], s_m[kWarps][S::kRows], s_l[kWarps][S::kRows];
   __shared__ int s_last;
   __shared__ volatile char s_far[kWarps][32];  // whether the warp has met a far value scale: a lane's own
-  constexpr int kNone = 0x7fffffff;
-  __shared__ volatile int s_nan[kWarps];       // first key of the warp's first step with NaN codes kept out
+  __shared__ volatile int s_nan[kWarps];       // whether the warp kept NaN codes out, and which of its sums they belong in
+  __shared__ uint32_t s_nan_bits[kWarps][S::kRows * (D / 32)];
   char* big = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   char* s_q = big + S::kBigB;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -604,7 +596,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       }
     };
     ask(0);
-    if (lane == 0) s_nan[warp] = kNone;
+    if (lane == 0) s_nan[warp] = 0;
+    if (tid < S::kRows) s_place[tid] = q.start + (block * S::kRows + tid) / group;
     for (int i = 0; i < min(count, S::kSlots); ++i) issue(i);
 #pragma unroll 1
     for (int i0 = 0; i0 < kMine; i0 += kAtOnce) {
@@ -664,7 +657,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         const int r = 8 * nt + 2 * c + y;
         t.M[nt][y] = kNoMax, t.L[nt][y] = 0.0f;
         t.rowf[nt][y] = s_rowf[r];
-        t.place[nt][y] = q.start + (block * S::kRows + r) / group;
+        t.place[nt][y] = s_place[r];
       }
     }
 
@@ -692,9 +685,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       }
       char* st = ring + tslot * S::kStageB;
       if (masked) {
-        const int tok = lane % S::kStep;
-        if (keep_nan_out<S>(st, lane, (lane < 16 || H == 1 ? k.good[0] : k.good[H - 1]) && j0 + tok < q.len) && lane == 0)
-          s_nan[warp] = min(s_nan[warp], j0);
+        const bool there = (lane < 16 || H == 1 ? k.good[0] : k.good[H - 1]) && j0 + lane % S::kStep < q.len;
+        keep_nan_out<S>(st, lane, there, j0, a.window, s_place, s_nan_bits[warp], &s_nan[warp]);
         take_step<S, true>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
       } else {
         take_step<S, false>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
@@ -729,7 +721,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     __syncthreads();                           // also: every warp is done with the ring
     if (s_abort) break;                        // the same for the whole block
     float* merge = reinterpret_cast<float*>(big);
-    auto unit_of = [](int r, int d) { return merge_unit<D>(r, d); };
+    // 16-byte units of a row are permuted so that a quarter warp's stores differ in bank
+    auto unit_of = [](int r, int d) {
+      const int u = d / 4, cc = (r & 7) >> 1;
+      return D == 64 ? u ^ ((cc & 1) | (cc >> 1) << 2) : u ^ (cc | ((u >> 4) & 1) << 2);
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -748,8 +744,12 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
         }
       }
     __syncwarp();
-    if (s_nan[warp] < kNone)
-      put_nan<S>(a, q.n, q.start, q.len, b, head, block, s_nan[warp], merge + (size_t)warp * S::kRows * D);
+    if (s_nan[warp]) {
+#pragma unroll 1
+      for (int i = lane; i < S::kRows * D; i += 32)
+        if (s_nan_bits[warp][i / 32] >> (i % 32) & 1)
+          merge[((size_t)warp * S::kRows + i / D) * D + unit_of(i / D, i % D) * 4 + i % 4] = NAN;
+    }
     __syncthreads();
     const bool opens = st0 == 0, closes = st1 == q.steps;
     const int slot = 2 * blockIdx.x + (opens ? 1 : 0);
