@@ -116,8 +116,10 @@ size_t moe_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t 
  * apart (16-byte aligned as above); lse f32 [T][q_heads] or NULL. q_heads is a multiple of
  * kv_heads. Products and sums are held in f32 from f16 operands: q times a power of two
  * (exact for bf16 and f16 values within 2^-28 of the row's largest), E4M3 codes (exact), and
- * the weights exp(s_j - max) v_scale rounded to f16 beside the largest. Slots past a
- * sequence's end may hold anything, NaN codes included. */
+ * the weights exp(s_j - max) v_scale rounded to f16 beside the largest. scale times a page's
+ * k_scale times a row's largest |q| has to be finite in f32. Slots past a sequence's end may
+ * hold anything, NaN codes included; a NaN code of K or V in use reaches only the rows that
+ * see its token (of V: that value of them). */
 moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, int32_t q_heads,
                                     int32_t dtype, const moe_kv_cache* cache,
                                     const moe_seq_batch* batch, float scale, int32_t window,

@@ -16,7 +16,8 @@
 //
 // Bound by the rows' bytes (2 read and 2 written per query value, 2 read and 1 written per key or
 // value): six prompts of up to 2048 tokens, 32 query and 8 key heads of 128 (127 MB), take 30.5 us, 4.2
-// TB/s; what does not stream are a page's dependent steps (largest magnitude, then codes). One
+// TB/s: a third of the warps are active (80 registers) and a page's steps depend on one another (largest
+// magnitude, then codes), so too few loads are in flight. One
 // token of one sequence takes 3.3 us, a launch and a few dependent loads.
 #include "serving.cuh"
 

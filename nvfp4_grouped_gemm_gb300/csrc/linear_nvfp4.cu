@@ -19,8 +19,8 @@
 // a stage's sixteen k-steps run in accumulators of their own and are added to the row's sum with
 // rounding (K = 4096: error 2.0e-6 of the result's norm in one chain of 256 k-steps).
 //
-// Measured: 131101 x 4096 for 16 tokens 72.5 us, 4.3 TB/s: the conversions and products of a
-// stage, not the copies, fill the warps' time. 2560 x 5120 for one token 6.7 us, where the first
+// Measured: 131101 x 4096 for 16 tokens 72.5 us, 4.3 TB/s: a stage's conversions and products, which
+// depend on one another, and not the copies take the warps' time (issue 53%). 2560 x 5120 for one token 6.7 us, where the first
 // copies' latency, the meeting of the warps and the launch are most of it.
 #include "serving.cuh"
 #include "tma_sync.cuh"

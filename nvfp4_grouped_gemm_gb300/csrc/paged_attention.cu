@@ -2,7 +2,7 @@
 // for few rows; prompt_attention.cu has the one for many.
 //
 // A sequence's n new tokens and the G query heads that share a key head are n*G rows over the
-// same keys and values; a segment is (sequence, key head, block of 16*MT such rows). Its keys
+// same keys and values; a segment is (sequence, key head, block of 8*NT such rows). Its keys
 // are cut into steps of STEP tokens, and all segments' steps form one line that the grid cuts
 // into equal pieces, so a batch of very different lengths loads every SM alike. A CTA whose
 // piece covers a whole segment writes its rows; the CTAs of a segment that was cut leave
@@ -29,14 +29,14 @@
 //
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
 // weight 0. V's bytes that are nobody's are replaced by 0 (they may be NaN codes). NaN codes of
-// keys that some rows of the block see and others do not are kept out of the products, and NaN is
-// put into the sums of the rows that see them when the rows meet.
+// keys that some rows of the block see and others do not are kept out of the products and noted
+// for the rows that see them, whose sums get NaN when the rows meet.
 //
 // Bound by the cache's bytes: 64 sequences of 100 to 16000 tokens, 32 query and 8 key heads of 128,
-// one new token each: 73.7 us, 5.7 TB/s (0.84 of the copy rate). One sequence of 32767: 23.6 us, of
+// one new token each: 73.9 us, 5.7 TB/s (0.84 of the copy rate). One sequence of 32767: 24.2 us, of
 // which about 12 are fixed: the line's scan, the first keys and queries, the warps' rows meeting,
 // and the join of the segment's pieces. With more rows the products and the softmax's instructions
-// are the limit: 16 sequences, 8 tokens and 5 heads of 64 (40 rows): 46.6 us.
+// are the limit: 16 sequences, 8 tokens and 5 heads of 64 (40 rows): 47.8 us.
 #include "serving.cuh"
 #include "tma_sync.cuh"
 
@@ -57,8 +57,8 @@ constexpr int kSegmentCost = 12;
 // Rows of a sequence (new tokens times query heads per key head) from which on it goes to the
 // tensor-memory form of prompt_attention.cu. That form's time hardly depends on the rows up to 128,
 // this one's grows with every 24. Sequences of 500 to 9000 tokens, 8 key heads, this form and the
-// other, us: 16 sequences, D = 128: 64 rows 92 / 116, 96 rows 121 / 115; D = 64: 70 rows 63 / 67, 80
-// rows 74 / 67; 64 sequences of up to 4000, 80 rows: D = 128 258 / 229, D = 64 167 / 145.
+// other, us: 16 sequences, D = 128: 64 rows 95 / 109, 96 rows 124 / 110; D = 64: 70 rows 63 / 70, 80
+// rows 75 / 70; 64 sequences of up to 4000, 80 rows: D = 128 268 / 220, D = 64 172 / 149.
 constexpr int kPromptRows = 73;
 constexpr int kAllRows = 0x7fffffff;
 
@@ -168,8 +168,8 @@ __device__ long long block_scan(long long v, long long* s_sum, long long* before
   return all;
 }
 
-// A warp's keys: which page each half-step (16 tokens) lies in, its scales, for 32 of them at a
-// time (lane l holds half-step l of the batch).
+// The factors of a warp's half-steps (16 tokens, which lie in one page), 32 of them at a time: lane l
+// holds half-step l of the batch.
 struct Keys {
   // (all 0 without a page) scale * k_scale * log2 e; log2 v_scale; 1 / v_scale, negative from the
   // warp's first far scale on

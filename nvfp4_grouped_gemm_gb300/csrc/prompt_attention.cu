@@ -23,7 +23,7 @@
 //
 // Tensor memory is full at D = 128 (two S, two O of 128 columns), so a tile's weights lie over its
 // S and its chain (softmax, O += P V, the next S) is serial; two tiles in flight hide each other's
-// softmax. 2048 new tokens after 6144, 32 query and 8 key heads of 128, bf16: 275 us, 0.87 PFLOP/s
+// softmax. 2048 new tokens after 6144, 32 query and 8 key heads of 128, bf16: 278 us, 0.87 PFLOP/s
 // of unmasked products. A period of both tiles takes about 4400 clocks: 2 * 1400 of products (1024
 // without the widening warps' stores beside their operand reads in shared memory), and a softmax
 // of about 2000 with hand-offs of about 400. What its steps gave: the weights from one reading of

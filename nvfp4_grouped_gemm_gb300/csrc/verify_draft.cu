@@ -22,7 +22,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 // The row is cut into chunks whose sums the last block chooses from, and a block takes `per` of them
-// in turn: 1024 tokens and one each while that leaves at most 8 blocks per SM of a 152-SM GPU,
+// in turn: 1024 tokens and one each while that leaves at most 8 blocks per SM of a 152-SM GPU (a constant:
+// the workspace's size must not depend on the GPU that is asked),
 // else 2048 and as many as bring the grid down to that (the test of the drafts and the arrival
 // are then paid once for several chunks: 64 sequences of 151937 took 35.6 us with a block per
 // 4096 tokens, four waves of them).
