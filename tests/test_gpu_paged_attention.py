@@ -433,3 +433,38 @@ def test_nan_values_in_many_sequences(D, page, window):
 def test_quiet_values_in_long_and_in_many_sequences(order):
     test_quiet_values_keep_their_share_of_the_sum(128, 64, 1, 2, [(30011, 1)], order)
     test_quiet_values_keep_their_share_of_the_sum(64, 16, 4, 2, [(int(n), 1) for n in np.linspace(0, 400, 60)], order)
+
+
+@pytest.mark.parametrize("D,page,heads,group,dtype,pairs,window", [
+    (128, 64, 2, 4, "bf16", [(100, 1), (63, 1), (500, 3)], 50), (64, 16, 1, 3, "f16", [(100, 7), (0, 5)], 0),
+    (256, 32, 1, 2, "bf16", [(70, 6), (0, 9)], 20), (128, 64, 1, 2, "bf16", [(300, 100), (64, 3)], 0),
+    (64, 32, 2, 4, "f16", [(400, 300), (10, 20)], 70)])
+def test_nan_keys_reach_only_the_rows_that_see_them(D, page, heads, group, dtype, pairs, window):
+    """K codes of NaN at the last new token and before some rows' windows: rows that see the key are
+    NaN, the others within their bounds."""
+    rng = np.random.default_rng(43)
+    batch = Batch(rng, pairs, page)
+    planes = cache_planes(rng, batch.num_pages, heads, page, D)
+    stale_nan(planes, batch)
+    nan = np.zeros((batch.T, heads * group), bool)
+    for b, (past, n) in enumerate(pairs):
+        for at in {past + n - 1} | ({past + n - 1 - window, past - window} if window else set()):
+            if at < 0:
+                continue
+            h = int(rng.integers(heads))
+            planes[0][batch.table[b, at // page], h, at % page, int(rng.integers(D))] = 0x7F
+            for i in range(n):
+                if at <= past + i and (window == 0 or at > past + i - window):
+                    nan[batch.offsets[b] + i, h * group:(h + 1) * group] = True
+    q = activations(rng, (batch.T, heads * group, D), dtype)
+    want, wl, eo, el = oracle.attention(q.double().numpy(), *planes, batch.offsets, batch.lens,
+                                        batch.table, D ** -0.5, window)
+    out, lse, ws = run(q.cuda(), device_cache(planes), batch.device(), heads * group, D, D ** -0.5, window)
+    assert moe.get_device_error(ws) == 0
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.broadcast_to(nan[:, :, None], got.shape))
+    assert np.array_equal(np.isnan(gl), nan) and nan.any() and not nan.all()
+    rel, floor = ROUND[dtype]
+    tol = eo + rel * (np.abs(want) + eo) + floor
+    assert np.all(np.abs(got - want)[~nan] <= tol[~nan])
+    assert np.all(np.abs(gl - wl)[~nan] <= el[~nan] + 1e-6)
