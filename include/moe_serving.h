@@ -9,11 +9,16 @@
  *   moe_attention_paged_e4m3  causal attention of the new tokens over that cache
  *   moe_verify_draft          accepts or refuses drafted tokens against the target's
  *                             probabilities, with the random numbers given
+ *   moe_attention_tree_e4m3   the attention for trees of drafted tokens
+ *   moe_kv_keep_e4m3          what a tree's accepted path leaves in the cache
+ *   moe_kv_weights_e4m3       the attention weight that cached tokens have gathered
+ *   moe_kv_evict_e4m3         a cache cut to a budget by that weight
+ *   moe_residual_norm         norms, gate and residual around attention and the layer
  *
  * The conventions of moe.h hold: array pointers are DEVICE pointers owned by the caller;
  * calls are asynchronous on `stream`, allocate nothing and can be captured in a CUDA graph;
  * sizes are checked on the host before anything is launched; no call prints, aborts or
- * throws. Every call takes a workspace `ws` (256-byte aligned, zero-filled once after it is
+ * throws. Every call but moe_residual_norm takes a workspace `ws` (256-byte aligned, zero-filled once after it is
  * allocated, of the bytes its size function returns) whose first word is the device error
  * word of moe_get_device_error. A workspace serves any number of calls in one stream, of the
  * sizes it was made for and smaller ones (the attention's of its head_dim); calls that can
@@ -36,7 +41,8 @@ enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
  *                        than its row of the page table, or more new tokens than its length
  *                        (the tokens concerned are left out)
  *   MOE_DEVERR_POSITION  a position outside the cos/sin tables (clamped into them)
- *   MOE_DEVERR_TOKEN     a drafted id outside [0, V) (refused)
+ *   MOE_DEVERR_TOKEN     a drafted id outside [0, V) (refused), or a list of kept tokens that does
+ *                        not ascend within the new tokens (it ends there)
  *   MOE_DEVERR_PROBS     a target row without any mass (the token drawn from it is -1) */
 enum { MOE_DEVERR_PAGE = 4, MOE_DEVERR_POSITION = 8, MOE_DEVERR_TOKEN = 16, MOE_DEVERR_PROBS = 32 };
 
@@ -167,6 +173,113 @@ moe_status moe_verify_draft(const int32_t* draft_ids, const int32_t* n_draft, in
                             const void* draft_probs, int64_t draft_stride, int32_t dtype,
                             const float* u_accept, const float* u_sample, int32_t* out_ids,
                             int32_t* n_accepted, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- attention for trees of drafted tokens ---------------------------------------------- */
+
+/* moe_attention_paged_e4m3 for new tokens that form a tree (or several): new token i of a sequence
+ * sees the tokens before the new ones, and of the n new ones those c < 32*tree_words whose bit is set
+ * in its row of tree_mask (bit c % 32 of word c / 32): for a tree its ancestors and itself. The bits
+ * alone decide, in any order; bits from n on have no meaning, and a row may have none. With
+ * window > 0 a row sees the last `window` tokens of its chain, which is the tokens before the new
+ * ones followed by those of its bits.
+ *   tree_mask  u32 [T][tree_words], rows tree_stride words apart; 1 <= tree_words <= 8
+ * The rest is as above, and so is the workspace (moe_attention_workspace_bytes). Positions for the
+ * rotation are the caller's: moe_kv_append_rope_e4m3 takes them (a node's is the number of tokens
+ * before the new ones plus its depth). */
+moe_status moe_attention_tree_e4m3(const void* q, int64_t q_stride, int32_t T, int32_t q_heads,
+                                   int32_t dtype, const moe_kv_cache* cache,
+                                   const moe_seq_batch* batch, const uint32_t* tree_mask,
+                                   int32_t tree_words, int64_t tree_stride, float scale,
+                                   int32_t window, void* out, int64_t out_stride, float* lse,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* ---- keeping some of the new tokens -------------------------------------------------------- */
+
+size_t moe_kv_keep_workspace_bytes(void);
+
+/* Of each sequence's new tokens those in its list stay, in order: new token keep[b][i] moves to
+ * place start + i, start being the number of tokens before the new ones, for every key head, and
+ * new_lens[b] = start + (the list's length). The list is the first n_keep[b] entries (negative: 0,
+ * at most `width`) of row b, ascending within [0, n) for n new tokens; at an entry that is not it
+ * ends (MOE_DEVERR_TOKEN). A page into which a token moves keeps its scale, or takes the largest of
+ * those its new tokens came from if that is larger; codes under another scale than before are
+ * rescaled by old / new and rounded again to nearest even, in all slots of such a page. A token
+ * from or into a page out of range stays (MOE_DEVERR_PAGE). No two sequences may have a page in
+ * common that holds new tokens. A sequence without a valid start keeps its length.
+ *   keep i32 [B][width] (may be NULL if width is 0)  n_keep i32 [B]  new_lens i32 [B], not the
+ *   batch's own seq_lens */
+moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch,
+                            const int32_t* keep, const int32_t* n_keep, int32_t width,
+                            int32_t* new_lens, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- attention weights of cached tokens, and eviction by them ------------------------------- */
+
+size_t moe_kv_weights_workspace_bytes(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+
+/* What attention gave each cached token: for token j of a sequence with new tokens and key head h
+ *   w_out[j][h] = (j new ? 0 : decay * w[j][h]) + sum exp(s_rj - lse_r)
+ * over the rows r (new tokens, times the query heads of h) that see j as in
+ * moe_attention_paged_e4m3 (causal, window), whose lse is given here; a row with lse -inf adds
+ * nothing. decay 0 does not read w. Sequences without new tokens, and slots past a sequence's
+ * end, are left alone. A NaN key code makes the weights of its token NaN if a row sees it.
+ *   w, w_out  f32 [num_pages][kv_heads][page_size], the slots of the cache; may be the same
+ *   lse       f32 [T][q_heads]                       decay within [0, 1]
+ * Products are as in the attention (f16 operands, f32 sums); each token's sum is made in one order,
+ * so two calls give the same bits. Tokens in pages out of range are left out (MOE_DEVERR_PAGE). */
+moe_status moe_kv_weights_e4m3(const void* q, int64_t q_stride, int32_t T, int32_t q_heads,
+                               int32_t dtype, const float* lse, const moe_kv_cache* cache,
+                               const moe_seq_batch* batch, float scale, int32_t window, float decay,
+                               const float* w, float* w_out, void* ws, size_t ws_bytes,
+                               void* stream);
+
+size_t moe_kv_evict_workspace_bytes(int32_t B, int32_t kv_heads);
+
+/* Copies of each sequence's tokens those that a budget keeps into other pages of the same cache:
+ * k = min(length, budget, width) tokens of each key head, the last min(recent, k), of what is left
+ * of k the first `first`, and the largest weights among the others (ties: the lower place; NaN and
+ * tokens in pages out of range below all numbers, -0 as 0). They keep their order:
+ *   kept[b][h][0..k) their places, ascending, then -1 up to `width`
+ *   new_lens[b] = k
+ *   place i of the copy lies in page dst_table[b][i / page_size], slot i % page_size; codes, and the
+ *   tokens' weights (which the plane w has for all pages)
+ * A page of the copy gets the largest of the scales its tokens came from; codes under another scale
+ * than before are rescaled by old / new and rounded again to nearest even. Slots behind the last
+ * token are left as they were. budgets i32 [B], or NULL for `width` everywhere; a sequence with a
+ * negative budget is left alone (new_lens its length, kept -1). Old pages are only read, and may
+ * be in use by other sequences; the pages of dst_table in use must be in nobody else's.
+ *   w f32 [num_pages][kv_heads][page_size]   kept i32 [B][kv_heads][width]   new_lens i32 [B], not
+ *   the batch's own   dst_table i32 [B][dst_stride] with at least ceil(width / page_size) columns
+ * Tokens from or into pages out of range are not copied (MOE_DEVERR_PAGE). The batch's q_offsets are
+ * not read. */
+moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch, float* w,
+                             const int32_t* dst_table, int32_t dst_stride, const int32_t* budgets,
+                             int32_t width, int32_t first, int32_t recent, int32_t* kept,
+                             int32_t* new_lens, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- norms, gate and residual around a block ------------------------------------------------- */
+
+/* What lies between two blocks of a layer, for T rows of H values:
+ *   z = y * w_post / rms(y)     (y itself without post_weight)
+ *   r = residual + scale * g * z  -> out        (g = 1 without gate)
+ *   n = r * w_pre / rms(r)        -> normed     (w_pre = 1 without pre_weight)
+ * with rms(v) = sqrt(mean v^2 + eps) over the row and w = weight + weight_offset; with gate_sigmoid
+ * g = 1 / (1 + exp(-gate)). All in f32; out and normed are rounded once each, n from the r that is
+ * not rounded. y may be NULL (r = residual, then post_weight and gate are too); out or normed may be
+ * NULL, not both. out may be residual or y itself, normed y or residual, with the same type and stride.
+ *   y, residual, out, normed  rows of y_dtype, residual_dtype (out's too), normed_dtype (bf16, f16, f32)
+ *   weights                   weight_dtype [H]
+ *   gate                      gate_dtype, element (t, i) at t * gate_stride + i * gate_inner,
+ *                             gate_inner 0 or 1, gate_stride 0 for one row that all share
+ * H at most 32768; any alignment of the types (16-byte aligned rows and H a multiple of 8 are the
+ * fast form). Takes no workspace. */
+moe_status moe_residual_norm(const void* y, int64_t y_stride, int32_t y_dtype, const void* residual,
+                             int64_t residual_stride, void* out, int64_t out_stride,
+                             int32_t residual_dtype, void* normed, int64_t normed_stride,
+                             int32_t normed_dtype, int32_t T, int32_t H, const void* post_weight,
+                             const void* pre_weight, int32_t weight_dtype, const void* gate,
+                             int64_t gate_stride, int32_t gate_inner, int32_t gate_dtype,
+                             int32_t gate_sigmoid, float scale, float eps, float weight_offset,
+                             void* stream);
 
 #ifdef __cplusplus
 }

@@ -92,6 +92,23 @@ SIGNATURES = [
     ("moe_verify_draft", c_i32,
      [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp,
       c_vp, c_size, c_vp]),
+    ("moe_attention_tree_e4m3", c_i32,
+     [c_vp, c_i64, c_i32, c_i32, c_i32, ctypes.POINTER(KvCache), ctypes.POINTER(SeqBatch), c_vp,
+      c_i32, c_i64, c_f32, c_i32, c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
+    ("moe_kv_keep_workspace_bytes", c_size, []),
+    ("moe_kv_keep_e4m3", c_i32,
+     [ctypes.POINTER(KvCache), ctypes.POINTER(SeqBatch), c_vp, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
+    ("moe_kv_weights_workspace_bytes", c_size, [c_i32] * 4),
+    ("moe_kv_weights_e4m3", c_i32,
+     [c_vp, c_i64, c_i32, c_i32, c_i32, c_vp, ctypes.POINTER(KvCache), ctypes.POINTER(SeqBatch),
+      c_f32, c_i32, c_f32, c_vp, c_vp, c_vp, c_size, c_vp]),
+    ("moe_kv_evict_workspace_bytes", c_size, [c_i32] * 2),
+    ("moe_kv_evict_e4m3", c_i32,
+     [ctypes.POINTER(KvCache), ctypes.POINTER(SeqBatch), c_vp, c_vp, c_i32, c_vp, c_i32, c_i32,
+      c_i32, c_vp, c_vp, c_vp, c_size, c_vp]),
+    ("moe_residual_norm", c_i32,
+     [c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32, c_vp,
+      c_vp, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32, c_f32, c_f32, c_f32, c_vp]),
 ]
 
 _lib = None

@@ -27,6 +27,10 @@
 // a weight would pass 2^8, which leaves f16 weights their full precision and makes rescaling of
 // the accumulators rare. w is rounded to f16 (2^-11), sums and accumulators are f32.
 //
+// For trees of drafted tokens (moe_attention_tree_e4m3) the same kernel asks a row's bits instead of
+// its place in the steps that hold new tokens or a window's edge; the bits, cut to what the window
+// leaves, lie in shared memory.
+//
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
 // weight 0. V's bytes that are nobody's are replaced by 0 (they may be NaN codes). NaN codes of
 // keys that some rows of the block see and others do not are kept out of the products and noted
@@ -126,7 +130,7 @@ struct Seq {
   int row0, n, start, len;      // token rows, new tokens, place of the first, visible length
   int step0, steps, blocks;     // first step, steps, row blocks
 };
-template <class S>
+template <class S, bool TREE>
 __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group, uint32_t* err) {
   Seq q;
   q.row0 = min(max(a.b.q_offsets[b], 0), a.T);
@@ -138,7 +142,7 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
   const int cap = a.b.max_pages * a.c.page_size;
   if (q.n > 0 && (q.start < 0 || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
-  const int lo = a.window > 0 ? max(0, min(q.start - a.window + 1, q.len)) : 0;
+  const int lo = a.window > 0 ? max(0, min(q.start - a.window + (TREE ? 0 : 1), q.len)) : 0;
   q.step0 = lo / S::kStep;
   q.steps = max((q.len + S::kStep - 1) / S::kStep - q.step0, 1);
   q.blocks = (q.n * group + S::kRows - 1) / S::kRows;
@@ -197,12 +201,25 @@ struct StepKeys {
   bool good[H];
 };
 
+// What the rows of a block of trees see: of the tokens before the new ones those from lo[row] on, of the
+// new ones those of bits[row][..].
+struct TreeRows {
+  const uint32_t* bits;
+  const int* lo;
+  int start;                                   // place of the first new token
+};
+__device__ __forceinline__ bool tree_sees(const TreeRows& t, int row, int j) {
+  const int c = j - t.start;
+  if (c < 0) return j >= t.lo[row];
+  return c < 32 * kMaxTreeWords && (t.bits[row * kMaxTreeWords + (c >> 5)] >> (c & 31) & 1) != 0;
+}
+
 // One step of STEP keys for all rows; `masked` where a key of it is hidden from a row or is not
 // there, or a value scale is or was far from the others.
-template <class S, bool masked>
+template <class S, bool masked, bool TREE>
 __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepKeys<S::kHalves>& k,
                                           const char* st, const char* s_q, int lane, int j0, int len,
-                                          int window) {
+                                          int window, const TreeRows& tree) {
   constexpr int D = S::D, NT = S::NT, H = S::kHalves;
   float sc[NT][H][4];
 #pragma unroll
@@ -256,7 +273,9 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
         sc[nt][h][x] = fmaf(sc[nt][h][x], k.f[h] * t.rowf[nt][y], k.v[h] - base[y]);
         if (masked) {
           const int j = j0 + h * 16 + (x >> 1) * 8 + f.tau, pl = t.place[nt][y];
-          const bool see = k.good[h] && j <= pl && j < len && (window == 0 || j > pl - window);
+          const bool see = k.good[h] && j < len &&
+                           (TREE ? tree_sees(tree, 8 * nt + 2 * (lane & 3) + y, j)
+                                 : j <= pl && (window == 0 || j > pl - window));
           if (!see) sc[nt][h][x] = -INFINITY;
         }
         top[nt][y] = fmaxf(top[nt][y], sc[nt][h][x]);
@@ -350,9 +369,9 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
 // `there`: the lane's key is (a lane per key, at D = 256 two). A pass and a call of its own, which leaves
 // nothing in registers (64 sequences of 100 to 16000 tokens 73.9 us; with the pages read again at the end
 // instead of bits 75.0).
-template <class S>
+template <class S, bool TREE>
 __device__ __noinline__ void keep_nan_out(char* st, int lane, bool there, int j0, int window, const int* places,
-                                          uint32_t* bits, volatile int* any) {
+                                          uint32_t* bits, volatile int* any, TreeRows tree) {
   constexpr int D = S::D, kWords = D / 32, kChunks = S::kPlaneB / 16 / 32;
   const int sub = D == 256 ? lane >> 4 : 0, tok = D == 256 ? lane & 15 : lane;
   char* row = st + S::kPlaneB + sub * (S::kStep * 128) + tok * S::kRowB;
@@ -380,7 +399,8 @@ __device__ __noinline__ void keep_nan_out(char* st, int lane, bool there, int j0
     const int d = sub * 128 + ((i / 4) ^ swz) * 16 + (i % 4) * 4;
 #pragma unroll 1
     for (int r = 0; there && r < S::kRows; ++r)
-      if (j0 + tok <= places[r] && (window == 0 || j0 + tok > places[r] - window))
+      if (TREE ? tree_sees(tree, r, j0 + tok)
+               : j0 + tok <= places[r] && (window == 0 || j0 + tok > places[r] - window))
         atomicOr(bits + r * kWords + d / 32, four << (d % 32));
   }
   // plain writes to the ring's memory come before the next copies into it
@@ -388,7 +408,7 @@ __device__ __noinline__ void keep_nan_out(char* st, int lane, bool there, int j0
   __syncwarp();
 }
 
-template <class S>
+template <class S, bool TREE>
 __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
@@ -406,6 +426,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   __shared__ volatile char s_far[kWarps][32];  // whether the warp has met a far value scale: a lane's own
   __shared__ volatile int s_nan[kWarps];       // whether the warp kept NaN codes out, and which of its sums they belong in
   __shared__ uint32_t s_nan_bits[kWarps][S::kRows * (D / 32)];
+  __shared__ uint32_t s_bits[TREE ? S::kRows * kMaxTreeWords : 1];
+  __shared__ int s_lo[TREE ? S::kRows : 1];
   char* big = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   char* s_q = big + S::kBigB;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -426,7 +448,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   long long total = 0, mine = 0, at = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
     mine = 0;
-    if (b0 + tid < a.b.B) mine = line_of(read_seq<S>(a, b0 + tid, group, blockIdx.x == 0 ? err : nullptr));
+    if (b0 + tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, b0 + tid, group, blockIdx.x == 0 ? err : nullptr));
     total += block_scan<kWarps>(mine, s_sum, &at);
   }
   long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -442,7 +464,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     long long base = 0;
     for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
       mine = 0;
-      if (b0 + tid < a.b.B) mine = line_of(read_seq<S>(a, b0 + tid, group, nullptr));
+      if (b0 + tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, b0 + tid, group, nullptr));
       const long long sum = block_scan<kWarps>(mine, s_sum, &at);
       if (mine > 0 && base + at <= begin && begin < base + at + mine) s_seq = b0 + tid, s_first = base + at;
       base += sum;
@@ -451,7 +473,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   __syncthreads();
   int b = s_seq;
   long long first = s_first;                   // the line's place of sequence b's first step
-  Seq q = read_seq<S>(a, b, group, nullptr);
+  Seq q = read_seq<S, TREE>(a, b, group, nullptr);
 
   char* ring = big + warp * S::kSlots * S::kStageB;
   uint64_t* full = s_full + warp * S::kSlots;
@@ -474,7 +496,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   for (long long pos = begin; pos < end;) {
     while (pos >= first + line_of(q)) {
       first += line_of(q);
-      q = read_seq<S>(a, ++b, group, nullptr);
+      q = read_seq<S, TREE>(a, ++b, group, nullptr);
     }
     const int length = q.steps + kSegmentCost;
     const long long in_seq = pos - first;
@@ -490,7 +512,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     const int tok_first = block * S::kRows / group, tok_last = (block * S::kRows + R - 1) / group;
     const int place_lo = q.start + tok_first, place_hi = q.start + tok_last;
     // steps this block of rows can see at all
-    const int hi = min(q.len, place_hi + 1), lo = a.window > 0 ? max(0, place_lo - a.window + 1) : 0;
+    const int hi = TREE ? q.len : min(q.len, place_hi + 1);
+    const int lo = a.window > 0 ? max(0, TREE ? q.start - a.window : place_lo - a.window + 1) : 0;
     const int w0 = max(q.step0 + st0, lo / S::kStep);
     const int w1 = min(q.step0 + st1, (max(hi, 0) + S::kStep - 1) / S::kStep);
 
@@ -598,6 +621,12 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     ask(0);
     if (lane == 0) s_nan[warp] = 0;
     if (tid < S::kRows) s_place[tid] = q.start + (block * S::kRows + tid) / group;
+    if (TREE && tid < S::kRows) {
+      uint32_t w[kMaxTreeWords];
+      s_lo[tid] = tree_row(a, q.row0 + (block * S::kRows + tid) / group, tid < R, q.n, q.start, w);
+#pragma unroll
+      for (int i = 0; i < kMaxTreeWords; ++i) s_bits[tid * kMaxTreeWords + i] = w[i];
+    }
     for (int i = 0; i < min(count, S::kSlots); ++i) issue(i);
 #pragma unroll 1
     for (int i0 = 0; i0 < kMine; i0 += kAtOnce) {
@@ -661,6 +690,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       }
     }
 
+    const TreeRows tree = {s_bits, s_lo, q.start};
     bool ok = true;
     for (int i = 0; i < count; ++i) {
       // every lane looks at the barrier itself; the bounded wait is for copies not there yet
@@ -673,8 +703,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       static_assert(S::kSlots <= kPer, "");
       if (src == 0) cur = factors();
       StepKeys<H> k;
-      bool masked = j0 + S::kStep > place_lo + 1 || j0 + S::kStep > q.len;
-      if (a.window > 0) masked |= j0 <= place_hi - a.window;
+      bool masked = j0 + S::kStep > (TREE ? q.start : place_lo + 1) || j0 + S::kStep > q.len;
+      if (a.window > 0) masked |= j0 <= (TREE ? q.start + min(q.n, 32 * kMaxTreeWords) : place_hi) - a.window;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         k.f[h] = __shfl_sync(0xffffffffu, cur.f, src + h);
@@ -686,10 +716,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       char* st = ring + tslot * S::kStageB;
       if (masked) {
         const bool there = (lane < 16 || H == 1 ? k.good[0] : k.good[H - 1]) && j0 + lane % S::kStep < q.len;
-        keep_nan_out<S>(st, lane, there, j0, a.window, s_place, s_nan_bits[warp], &s_nan[warp]);
-        take_step<S, true>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+        keep_nan_out<S, TREE>(st, lane, there, j0, a.window, s_place, s_nan_bits[warp], &s_nan[warp], tree);
+        take_step<S, true, TREE>(t, frag, k, st, s_q, lane, j0, q.len, a.window, tree);
       } else {
-        take_step<S, false>(t, frag, k, st, s_q, lane, j0, q.len, a.window);
+        take_step<S, false, TREE>(t, frag, k, st, s_q, lane, j0, q.len, a.window, tree);
       }
       if (++tslot == S::kSlots) tslot = 0, tphase ^= 1;
       --in_flight;
@@ -873,7 +903,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   pdl_wait();
 }
 
-template <int D, int NT, int WARPS>
+template <int D, int NT, int WARPS, bool TREE>
 cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
   using S = Shape<D, NT, WARPS>;
   CUtensorMap map[2];
@@ -884,7 +914,7 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
   if (!make_map3(&map[0], a.c.k_codes, dims, strides, box, swz) ||
       !make_map3(&map[1], a.c.v_codes, dims, strides, box, swz))
     return cudaErrorInvalidValue;
-  auto kern = attention_kernel<S>;
+  auto kern = attention_kernel<S, TREE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   int grid = num_sms() * S::kCtas;
@@ -894,7 +924,7 @@ cudaError_t launch_shape(const AttentionArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
   // Row tiles of a block: as few as hold the sequences' rows on average in one pass over the keys,
   // or in equal passes beyond three: a fourth tile does not fit into the registers. 16 sequences of
@@ -905,12 +935,18 @@ cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
   const long long tiles = (rows + 7) / 8, passes = (tiles + kMost - 1) / kMost;
   const int nt = (int)((tiles + passes - 1) / passes);
   if constexpr (D <= 128) {
-    if (nt == 3) return launch_shape<D, 3, 4>(a, s);
+    if (nt == 3) return launch_shape<D, 3, 4, TREE>(a, s);
   }
-  if (nt == 2) return launch_shape<D, 2, 4>(a, s);
+  if (nt == 2) return launch_shape<D, 2, 4, TREE>(a, s);
   // Few segments: more warps per CTA, so that fewer partial rows have to be joined.
   const bool few = (long long)a.b.B * a.c.kv_heads <= num_sms();
-  return few ? launch_shape<D, 1, D == 256 ? 8 : 12>(a, s) : launch_shape<D, 1, 4>(a, s);
+  return few ? launch_shape<D, 1, D == 256 ? 8 : 12, TREE>(a, s) : launch_shape<D, 1, 4, TREE>(a, s);
+}
+
+template <bool TREE>
+cudaError_t launch_few(const AttentionArgs& a, cudaStream_t s) {
+  if (a.c.head_dim == 64) return launch_dim<64, TREE>(a, s);
+  return a.c.head_dim == 128 ? launch_dim<128, TREE>(a, s) : launch_dim<256, TREE>(a, s);
 }
 
 }  // namespace
@@ -935,8 +971,7 @@ cudaError_t launch_attention(const AttentionArgs& args, cudaStream_t s) {
     if (e != cudaSuccess || all) return e;
     a.max_rows = kPromptRows - 1;
   }
-  if (a.c.head_dim == 64) return launch_dim<64>(a, s);
-  return a.c.head_dim == 128 ? launch_dim<128>(a, s) : launch_dim<256>(a, s);
+  return a.tree ? launch_few<true>(a, s) : launch_few<false>(a, s);
 }
 
 }  // namespace moe

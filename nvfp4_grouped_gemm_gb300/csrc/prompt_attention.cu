@@ -21,6 +21,9 @@
 // covers every product issued before it, so a softmax that sees its S knows that the previous
 // O += P V is complete and may rescale O.
 //
+// For trees of drafted tokens (moe_attention_tree_e4m3) a row's bits, cut to what the window leaves, lie
+// in shared memory and stand in for its place in the tiles that hold new tokens or a window's edge.
+//
 // Tensor memory is full at D = 128 (two S, two O of 128 columns), so a tile's weights lie over its
 // S and its chain (softmax, O += P V, the next S) is serial; two tiles in flight hide each other's
 // softmax. 2048 new tokens after 6144, 32 query and 8 key heads of 128, bf16: 278 us, 0.87 PFLOP/s
@@ -141,6 +144,15 @@ __device__ __forceinline__ void hide(float (&s)[32], int x0, int x1, bool there0
     if (x < x0 || x >= x1 || !(x < 16 ? there0 : there1)) s[x] = -INFINITY;
 }
 
+// The same with the visible keys as bits.
+__device__ __forceinline__ void hide_bits(float (&s)[32], uint32_t seen, bool there0, bool there1) {
+  asm volatile("" ::: "memory");
+  seen &= (there0 ? 0x0000ffffu : 0u) | (there1 ? 0xffff0000u : 0u);
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(seen >> x & 1)) s[x] = -INFINITY;
+}
+
 // Instruction descriptor, kind::f16: f32 accumulator (bit 4), A and B f16, B's major bit 16 (1:
 // its N dimension contiguous), N >> 3 at 17, M >> 4 at 24.
 constexpr uint32_t f16_idesc(int M, int N, bool b_mn) {
@@ -199,10 +211,11 @@ struct Seq {
   long long per_head;                          // line length of one key head
 };
 // Key tiles [x, y) that block `block` of a sequence can see.
+template <bool TREE>
 __device__ __forceinline__ int2 block_tiles(const Seq& q, int block, int group, int window) {
   const int first = block * kBlock / group, last = (min((block + 1) * kBlock, q.n * group) - 1) / group;
-  const int hi = min(q.len, q.start + last + 1);
-  const int lo = window > 0 ? max(0, q.start + first - window + 1) : 0;
+  const int hi = TREE ? q.len : min(q.len, q.start + last + 1);
+  const int lo = window > 0 ? max(0, min(TREE ? q.start - window : q.start + first - window + 1, TREE ? q.len : 0x7fffffff)) : 0;
   const int x = lo / kTile;
   return make_int2(x, max(x, (max(hi, 0) + kTile - 1) / kTile));
 }
@@ -212,11 +225,13 @@ struct Partly {
   int from, before;
 };
 __device__ __forceinline__ bool partly(const Partly& p, int t) { return t >= p.from || t < p.before; }
+template <bool TREE>
 __device__ __forceinline__ int block_line(const Seq& q, int block, int group, int window) {
-  const int2 t = block_tiles(q, block, group, window);
+  const int2 t = block_tiles<TREE>(q, block, group, window);
   return max(t.y - t.x, 1) + kSegmentCost;
 }
 // By a warp: its lanes take the blocks in turn.
+template <bool TREE>
 __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group, int min_rows, uint32_t* err) {
   Seq q;
   q.row0 = min(max(a.b.q_offsets[b], 0), a.T);
@@ -231,7 +246,7 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
   if ((q.start < 0 || q.len > cap) && err && lane == 0) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
   q.blocks = (q.n * group + kBlock - 1) / kBlock;
-  for (int i = lane; i < q.blocks; i += 32) q.per_head += block_line(q, i, group, a.window);
+  for (int i = lane; i < q.blocks; i += 32) q.per_head += block_line<TREE>(q, i, group, a.window);
 #pragma unroll
   for (int o = 16; o; o >>= 1) q.per_head += __shfl_xor_sync(0xffffffffu, q.per_head, o);
   return q;
@@ -242,7 +257,7 @@ struct Piece {
   bool more;                                   // false: the CTA's line ended
   bool opens, closes;                          // holds the segment's first / last tile
   int b, head, block, R;                       // sequence, key head, block of rows, rows in it
-  int row0, start, len;                        // of the sequence
+  int row0, n, start, len;                     // of the sequence
   int t0, t1;                                  // key tiles to work on (none if t0 >= t1)
   int c0, np;                                  // the CTAs the segment is spread over
 };
@@ -253,12 +268,14 @@ struct Walk {
   long long at;                                // line position of (b, head, block)
   Seq q;
 };
+template <bool TREE>
 __device__ __forceinline__ void walk_enter(Walk& w, const AttentionArgs& a, int group, int min_rows) {  // from (b, first)
-  w.q = read_seq(a, w.b, group, min_rows, nullptr);
+  w.q = read_seq<TREE>(a, w.b, group, min_rows, nullptr);
   w.head = w.q.per_head ? (int)((w.pos - w.first) / w.q.per_head) : 0;
   w.block = 0;
   w.at = w.first + w.head * w.q.per_head;
 }
+template <bool TREE>
 __device__ __forceinline__ Piece walk_next(Walk* state, const AttentionArgs& a, int group, int min_rows) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
@@ -269,12 +286,12 @@ __device__ __forceinline__ Piece walk_next(Walk* state, const AttentionArgs& a, 
     while (w.pos >= w.first + w.q.per_head * a.c.kv_heads) {
       w.first += w.q.per_head * a.c.kv_heads;
       ++w.b;
-      walk_enter(w, a, group, min_rows);
+      walk_enter<TREE>(w, a, group, min_rows);
     }
     // the block that pos is in: 32 at a time, by a running sum of their lines
     int line = 0;
     while (true) {
-      const int mine = w.block + lane < w.q.blocks ? block_line(w.q, w.block + lane, group, a.window) : 0;
+      const int mine = w.block + lane < w.q.blocks ? block_line<TREE>(w.q, w.block + lane, group, a.window) : 0;
       int upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -294,14 +311,14 @@ __device__ __forceinline__ Piece walk_next(Walk* state, const AttentionArgs& a, 
       w.block += 32;
       if (w.block >= w.q.blocks) w.block = 0, ++w.head;
     }
-    const int2 t = block_tiles(w.q, w.block, group, a.window);
+    const int2 t = block_tiles<TREE>(w.q, w.block, group, a.window);
     const int st0 = max(0, (int)(w.pos - w.at) - kSegmentCost);
     const int st1 = (int)min((long long)line, w.end - w.at) - kSegmentCost;
     w.pos = w.at + st1 + kSegmentCost;
     if (st1 <= st0) continue;                  // only the segment's fixed cost fell to this CTA
     p.b = w.b, p.head = w.head, p.block = w.block;
     p.R = min(kBlock, w.q.n * group - w.block * kBlock);
-    p.row0 = w.q.row0, p.start = w.q.start, p.len = w.q.len;
+    p.row0 = w.q.row0, p.n = w.q.n, p.start = w.q.start, p.len = w.q.len;
     p.t0 = t.x + st0, p.t1 = min(t.x + st1, t.y);
     p.opens = st0 == 0, p.closes = st1 == line - kSegmentCost;
     p.c0 = (int)((w.at + kSegmentCost) / w.per);
@@ -314,7 +331,12 @@ __device__ __forceinline__ Piece walk_next(Walk* state, const AttentionArgs& a, 
   return p;
 }
 
+template <bool TREE>
 __device__ __forceinline__ Partly partly_seen(const Piece& p, int group, int window) {
+  if (TREE) {                                  // new tokens; where the rows' windows may begin
+    const int edge = p.start + min(p.n, 32 * kMaxTreeWords) - window;
+    return {max(min(p.start, p.len), 0) / kTile, window > 0 && edge > 0 ? (edge + kTile - 1) / kTile : 0};
+  }
   const int lo = p.start + p.block * kBlock / group;       // the block's first and last rows' places
   const int hi = p.start + (p.block * kBlock + p.R - 1) / group;
   return {min(lo + 1, p.len) / kTile, window > 0 ? (hi - window + kTile) / kTile : 0};
@@ -329,7 +351,7 @@ struct Smem {
   static constexpr int kBytes = kVAt + 2 * kKv;
 };
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   using S = Smem<D>;
@@ -344,6 +366,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   __shared__ int2 s_issue;                     // the issuing thread's piece: key tiles (0: no more), row tiles
   __shared__ long long s_line[kThreads];
   __shared__ volatile uint32_t s_nan[2][kConvert / 32];    // NaN codes that a widening warp kept out of V
+  __shared__ uint32_t s_bits[TREE ? kMaxTreeWords : 1][TREE ? kBlock : 1];     // a thread's own row
   __shared__ volatile int s_nan_from[kSoftmax / 32];       // a softmax warp's first key tile with such
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -377,7 +400,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   auto lines = [&](int b0, uint32_t* err) {
     __syncthreads();
     for (int b = b0 + warp; b < min(b0 + kThreads, a.b.B); b += kThreads / 32) {
-      const long long line = read_seq(a, b, group, min_rows, err).per_head * heads;
+      const long long line = read_seq<TREE>(a, b, group, min_rows, err).per_head * heads;
       if (lane == 0) s_line[b - b0] = line;
     }
     __syncthreads();
@@ -430,7 +453,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
   if (warp < 16) {
     Walk w;
     w.pos = begin, w.end = end, w.per = per, w.first = s_first, w.b = s_seq;
-    walk_enter(w, a, group, min_rows);
+    walk_enter<TREE>(w, a, group, min_rows);
     if (lane == 0) s_walk[warp] = w;
   }
 
@@ -513,7 +536,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
     uint32_t kv = 0;
     bool ok = true;
     while (ok) {
-      const Piece p = walk_next(&s_walk[warp], a, group, min_rows);
+      const Piece p = walk_next<TREE>(&s_walk[warp], a, group, min_rows);
       if (!p.more) break;
       const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
       // lane l holds where 16-key group l % 8 of a tile starts in either plane (-1: nowhere)
@@ -528,7 +551,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         if (t < p.t1 && j < p.len) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
         return (int64_t)-1;
       };
-      const Partly part = partly_seen(p, group, a.window);
+      const Partly part = partly_seen<TREE>(p, group, a.window);
       uint32_t nan = 0;
       int page_next = page_of(p.t0);           // of the tile after the one fetched from
       int64_t start = -1;
@@ -621,7 +644,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       return wait_warp(&s_join, jph++ & 1, abort_flag, err);
     };
     while (true) {
-      const Piece p = walk_next(&s_walk[warp], a, group, min_rows);
+      const Piece p = walk_next<TREE>(&s_walk[warp], a, group, min_rows);
       if (!p.more) break;
       const int nt = p.t1 - p.t0;
       const bool live = p.R > 128 * tile;                  // this row tile is worked on
@@ -631,6 +654,26 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
       const int64_t row = p.row0 + rr / group;
       const int hq = p.head * group + rr % group;
       float M = kNoMax, L = 0.0f, rowf = 1.0f;
+      int lo = 0;                              // first of the tokens before the new ones that the row sees
+      if (TREE) {
+        uint32_t w[kMaxTreeWords];
+        lo = tree_row(a, row, r < p.R, p.n, p.start, w);
+#pragma unroll
+        for (int i = 0; i < kMaxTreeWords; ++i) s_bits[TREE ? i : 0][TREE ? r : 0] = w[i];
+      }
+      // which of the keys j .. j + 31 the row sees, as bits
+      auto seen_from = [&](int j) {
+        const int c = j - p.start;             // as a new token
+        auto word = [&](int i) { return i >= 0 && i < kMaxTreeWords ? s_bits[TREE ? i : 0][TREE ? r : 0] : 0u; };
+        uint32_t v = __funnelshift_r(word(c >> 5), word((c >> 5) + 1), c & 31);
+        if (c < 0) {
+          const uint32_t before = c <= -32 ? 0xffffffffu : (1u << -c) - 1;
+          const int skip = lo - j;             // hidden by the window
+          v = (v & ~before) | (skip <= 0 ? before : skip >= 32 ? 0u : before & 0xffffffffu << skip);
+        }
+        const int there = p.len - j;
+        return there >= 32 ? v : there <= 0 ? 0u : v & ((1u << there) - 1);
+      };
       // The issuing thread's waits and commits are the block's bottleneck: what these warps can wait
       // for and signal in its place they do. The last row tile's products come last, so its S tells
       // that K and the V before it are read.
@@ -704,7 +747,7 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         bool far = false;                        // a value scale so far was outside [2^-kFar, 2^kFar]
         int page = page_of(p.t0), page_next = page_of(p.t0 + 1);
         Scales scales = scales_of(page);
-        const Partly part = partly_seen(p, group, a.window);
+        const Partly part = partly_seen<TREE>(p, group, a.window);
         if (lane == 0) s_nan_from[warp] = p.t1;
         for (int t = p.t0; t < p.t1; ++t) {
           const bool there = page >= 0 && page < a.c.num_pages;
@@ -780,7 +823,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                 float s[32];
                 tmem_ld32(s_col + ch * 32, s);
                 const float4 c0 = s_coef[warp][2 * ch], c1 = s_coef[warp][2 * ch + 1];
-                if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+                if (masked && TREE) hide_bits(s, seen_from(j0 + ch * 32), c0.w > 0.0f, c1.w > 0.0f);
+                if (masked && !TREE) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
                 top = fmaxf(top, fmaf(max16(s), c0.x * rowf, c0.y));
                 top = fmaxf(top, fmaf(max16(s + 16), c1.x * rowf, c1.y));
               }
@@ -817,7 +861,8 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
                   for (int x = 16 * h; x < 16 * h + 16; x += 2) unpair(fma2(pair(s[x], s[x + 1]), ff, dd), s[x], s[x + 1]);
                 }
                 // hidden as exponents: a factor that underflows to 0 would make NaN of a score of -inf
-                if (masked) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
+                if (masked && TREE) hide_bits(s, seen_from(j0 + ch * 32), c0.w > 0.0f, c1.w > 0.0f);
+                if (masked && !TREE) hide(s, x0 - ch * 32, x1 - ch * 32, c0.w > 0.0f, c1.w > 0.0f);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float inv = h ? c1.z : c0.z;
@@ -909,15 +954,17 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
         __syncwarp();
         if (nt > 0 && s_nan_from[warp] < p.t1 && mine) {
           // NaN codes kept out of the products, from the pages, into the row if it sees them
-          const Partly part = partly_seen(p, group, a.window);
+          const Partly part = partly_seen<TREE>(p, group, a.window);
           const int32_t* table = a.b.page_table + (int64_t)p.b * a.b.table_stride;
-          const int j1 = min(min(place + 1, p.len), p.t1 * kTile);
+          const int j1 = min(TREE ? p.len : min(place + 1, p.len), p.t1 * kTile);
+          const int from = TREE ? lo : a.window > 0 ? place - a.window + 1 : 0;
 #pragma unroll 1
-          for (int j = max(s_nan_from[warp] * kTile, a.window > 0 ? place - a.window + 1 : 0); j < j1; ++j) {
+          for (int j = max(s_nan_from[warp] * kTile, from); j < j1; ++j) {
             if (!partly(part, j / kTile)) {                // every row sees this tile: its NaN are there
               j = part.from * kTile - 1;
               continue;
             }
+            if (TREE && !(seen_from(j) & 1)) continue;
             const int page = table[j >> log_p];
             if (page < 0 || page >= a.c.num_pages) continue;
             each_nan<D>(a.c.v_codes + page * a.c.page_stride + ((int64_t)p.head * P + (j & (P - 1))) * D, [&](int d) {
@@ -992,13 +1039,13 @@ prompt_kernel(const __grid_constant__ AttentionArgs a, int min_rows, char* ws) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_prompt(const AttentionArgs& a, int min_rows, char* ws, cudaStream_t s) {
   constexpr int smem = 1024 + Smem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = num_sms() < kPromptMaxGrid ? num_sms() : kPromptMaxGrid;
-  prompt_kernel<D><<<grid, kThreads, smem, s>>>(a, min_rows, ws);
+  prompt_kernel<D, TREE><<<grid, kThreads, smem, s>>>(a, min_rows, ws);
   return cudaGetLastError();
 }
 
@@ -1010,7 +1057,9 @@ size_t prompt_attention_ws_bytes(int head_dim) {
 
 cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, size_t ws_at, cudaStream_t s) {
   char* ws = a.ws + ws_at;
-  return a.c.head_dim == 64 ? launch_prompt<64>(a, min_rows, ws, s) : launch_prompt<128>(a, min_rows, ws, s);
+  if (a.tree)
+    return a.c.head_dim == 64 ? launch_prompt<64, true>(a, min_rows, ws, s) : launch_prompt<128, true>(a, min_rows, ws, s);
+  return a.c.head_dim == 64 ? launch_prompt<64, false>(a, min_rows, ws, s) : launch_prompt<128, false>(a, min_rows, ws, s);
 }
 
 }  // namespace moe

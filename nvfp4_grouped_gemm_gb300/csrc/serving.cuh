@@ -32,7 +32,11 @@ struct AttentionArgs {
   int64_t q_stride, out_stride;
   float* lse;
   char* ws;
+  const uint32_t* tree;        // bits of the new tokens that a token sees (null: causal)
+  int64_t tree_stride;
+  int tree_words;
 };
+constexpr int kMaxTreeWords = 8;
 size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
 
@@ -65,6 +69,53 @@ struct VerifyArgs {
 };
 size_t verify_ws_bytes(int B, int V);
 cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
+
+struct KeepArgs {
+  moe_kv_cache c;
+  moe_seq_batch b;
+  const int32_t *keep, *n_keep;
+  int width;
+  int32_t* new_lens;
+  uint32_t* err;
+};
+cudaError_t launch_keep(const KeepArgs& a, cudaStream_t s);
+
+struct EvictArgs {
+  moe_kv_cache c;
+  moe_seq_batch b;
+  float* w;
+  const int32_t *dst_table, *budgets;
+  int dst_stride, width, first, recent;
+  int32_t *kept, *new_lens;
+  uint32_t* err;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
+struct WeightsArgs {
+  moe_kv_cache c;
+  moe_seq_batch b;
+  int T, q_heads, dtype, window;
+  float scale, decay;
+  const uint16_t* q;
+  int64_t q_stride;
+  const float* lse;
+  const float* w;
+  float* w_out;
+  char* ws;
+};
+size_t kv_weights_ws_bytes(int T, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_kv_weights(const WeightsArgs& a, cudaStream_t s);
+
+struct NormArgs {
+  const void *y, *residual;
+  void *out, *normed;
+  const void *post, *pre, *gate;
+  int64_t y_stride, residual_stride, out_stride, normed_stride, gate_stride;
+  int T, H, y_dtype, residual_dtype, normed_dtype, weight_dtype, gate_dtype;
+  int gate_inner, sigmoid;
+  float scale, eps, offset;
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
 
 // 16-bit activations as f32 and back (nearest even).
 template <int DT>
@@ -133,6 +184,27 @@ __device__ __forceinline__ uint32_t load_ahead(const void* at, bool there, uint3
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
                : "=r"(v) : "l"(at), "r"((int)there), "r"(other) : "memory");
   return v;
+}
+
+
+// What token row `token` (of a sequence with n new tokens, the first at place `start`) sees of its tree:
+// the bits of the new tokens, and as the value returned the first of the tokens before them. With a
+// window that is the end of the row's chain: tokens before the new ones, then those of its bits.
+__device__ __forceinline__ int tree_row(const AttentionArgs& a, int64_t token, bool there, int n, int start,
+                                        uint32_t (&w)[kMaxTreeWords]) {
+  int m = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxTreeWords; ++i) {
+    const int left = n - 32 * i;               // bits that are tokens
+    w[i] = there && i < a.tree_words && left > 0 ? a.tree[token * a.tree_stride + i] : 0u;
+    if (left < 32 && left > 0) w[i] &= (1u << left) - 1;
+    m += __popc(w[i]);
+  }
+  if (a.window <= 0) return 0;
+#pragma unroll
+  for (int i = 0; i < kMaxTreeWords; ++i)
+    for (; m > a.window && w[i]; --m) w[i] &= w[i] - 1;
+  return max(0, start + m - a.window);
 }
 
 }  // namespace moe

@@ -1,4 +1,6 @@
 // Host side of the serving operators' C ABI (moe_serving.h): argument validation.
+#include <cmath>
+
 #include "serving.cuh"
 
 namespace moe {
@@ -44,6 +46,39 @@ moe_status check_batch(const moe_seq_batch* b) {
 }
 
 bool act_dtype(int dt) { return dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_F16; }
+
+// What both forms of the attention call take.
+moe_status attention_args(AttentionArgs* a, const void* q, int64_t q_stride, int32_t T, int32_t q_heads, int32_t dtype,
+                          const moe_kv_cache* cache, const moe_seq_batch* batch, float scale, int32_t window, void* out,
+                          int64_t out_stride, float* lse, void* ws, size_t ws_bytes) {
+  moe_status st = check_cache(cache);
+  if (st != MOE_OK) return st;
+  if ((st = check_batch(batch)) != MOE_OK) return st;
+  if (T <= 0 || !act_dtype(dtype) || window < 0) return MOE_ERR_INVALID_ARG;
+  if (q_heads <= 0 || q_heads % cache->kv_heads != 0) return MOE_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || scale > 1e30f) return MOE_ERR_INVALID_ARG;
+  if ((st = check_rows(q, q_stride, (int64_t)q_heads * cache->head_dim)) != MOE_OK) return st;
+  if ((st = check_rows(out, out_stride, (int64_t)q_heads * cache->head_dim)) != MOE_OK) return st;
+  if (!aligned(lse, 4)) return MOE_ERR_INVALID_ARG;
+  if (T >= (1 << 24) || (int64_t)T * q_heads >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, attention_ws_bytes(q_heads, cache->kv_heads, cache->head_dim))) != MOE_OK)
+    return st;
+  a->c = *cache;
+  a->b = *batch;
+  a->T = T;
+  a->q_heads = q_heads;
+  a->dtype = dtype;
+  a->window = window;
+  a->scale = scale;
+  a->q = static_cast<const uint16_t*>(q);
+  a->out = static_cast<uint16_t*>(out);
+  a->q_stride = q_stride;
+  a->out_stride = out_stride;
+  a->lse = lse;
+  a->ws = static_cast<char*>(ws);
+  return MOE_OK;
+}
 
 }  // namespace
 }  // namespace moe
@@ -115,21 +150,81 @@ moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, 
                                     const moe_seq_batch* batch, float scale, int32_t window,
                                     void* out, int64_t out_stride, float* lse, void* ws,
                                     size_t ws_bytes, void* stream) {
+  AttentionArgs a = {};
+  moe_status st = attention_args(&a, q, q_stride, T, q_heads, dtype, cache, batch, scale, window, out, out_stride,
+                                 lse, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_attention_tree_e4m3(const void* q, int64_t q_stride, int32_t T, int32_t q_heads,
+                                   int32_t dtype, const moe_kv_cache* cache,
+                                   const moe_seq_batch* batch, const uint32_t* tree_mask,
+                                   int32_t tree_words, int64_t tree_stride, float scale,
+                                   int32_t window, void* out, int64_t out_stride, float* lse,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  if (!tree_mask || !aligned(tree_mask, 4) || tree_words <= 0 || tree_stride < tree_words)
+    return MOE_ERR_INVALID_ARG;
+  if (tree_words > kMaxTreeWords) return MOE_ERR_UNSUPPORTED;
+  AttentionArgs a = {};
+  moe_status st = attention_args(&a, q, q_stride, T, q_heads, dtype, cache, batch, scale, window, out, out_stride,
+                                 lse, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  a.tree = tree_mask;
+  a.tree_words = tree_words;
+  a.tree_stride = tree_stride;
+  return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_kv_keep_workspace_bytes(void) { return kAlign; }
+
+moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch,
+                            const int32_t* keep, const int32_t* n_keep, int32_t width,
+                            int32_t* new_lens, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_cache(cache);
+  if (st != MOE_OK) return st;
+  if ((st = check_batch(batch)) != MOE_OK) return st;
+  if (width < 0 || (width > 0 && !keep) || !n_keep || !new_lens) return MOE_ERR_INVALID_ARG;
+  if (!aligned(keep, 4) || !aligned(n_keep, 4) || !aligned(new_lens, 4)) return MOE_ERR_INVALID_ARG;
+  if (new_lens == batch->seq_lens) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, moe_kv_keep_workspace_bytes())) != MOE_OK) return st;
+  KeepArgs a = {};
+  a.c = *cache;
+  a.b = *batch;
+  a.keep = keep;
+  a.n_keep = n_keep;
+  a.width = width;
+  a.new_lens = new_lens;
+  a.err = static_cast<uint32_t*>(ws);
+  return from_cuda(launch_keep(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_kv_weights_workspace_bytes(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  if (T <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0) return 0;
+  if (T >= (1 << 24) || (int64_t)T * q_heads >= (1LL << 30)) return 0;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  return kv_weights_ws_bytes(T, q_heads, kv_heads, head_dim);
+}
+
+moe_status moe_kv_weights_e4m3(const void* q, int64_t q_stride, int32_t T, int32_t q_heads,
+                               int32_t dtype, const float* lse, const moe_kv_cache* cache,
+                               const moe_seq_batch* batch, float scale, int32_t window, float decay,
+                               const float* w, float* w_out, void* ws, size_t ws_bytes,
+                               void* stream) {
   moe_status st = check_cache(cache);
   if (st != MOE_OK) return st;
   if ((st = check_batch(batch)) != MOE_OK) return st;
   if (T <= 0 || !act_dtype(dtype) || window < 0) return MOE_ERR_INVALID_ARG;
   if (q_heads <= 0 || q_heads % cache->kv_heads != 0) return MOE_ERR_INVALID_ARG;
-  if (!(scale > 0.0f) || scale > 1e30f) return MOE_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || scale > 1e30f || !(decay >= 0.0f && decay <= 1.0f)) return MOE_ERR_INVALID_ARG;
   if ((st = check_rows(q, q_stride, (int64_t)q_heads * cache->head_dim)) != MOE_OK) return st;
-  if ((st = check_rows(out, out_stride, (int64_t)q_heads * cache->head_dim)) != MOE_OK) return st;
-  if (!aligned(lse, 4)) return MOE_ERR_INVALID_ARG;
-  if (T >= (1 << 24) || (int64_t)T * q_heads >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!lse || !w || !w_out || !aligned(lse, 4) || !aligned(w, 4) || !aligned(w_out, 4)) return MOE_ERR_INVALID_ARG;
+  if (T >= (1 << 24) || (int64_t)T * q_heads >= (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
-  if ((st = check_ws(ws, ws_bytes, attention_ws_bytes(q_heads, cache->kv_heads, cache->head_dim))) !=
-      MOE_OK)
+  if ((st = check_ws(ws, ws_bytes, kv_weights_ws_bytes(T, q_heads, cache->kv_heads, cache->head_dim))) != MOE_OK)
     return st;
-  AttentionArgs a = {};
+  WeightsArgs a = {};
   a.c = *cache;
   a.b = *batch;
   a.T = T;
@@ -137,13 +232,113 @@ moe_status moe_attention_paged_e4m3(const void* q, int64_t q_stride, int32_t T, 
   a.dtype = dtype;
   a.window = window;
   a.scale = scale;
+  a.decay = decay;
   a.q = static_cast<const uint16_t*>(q);
-  a.out = static_cast<uint16_t*>(out);
   a.q_stride = q_stride;
-  a.out_stride = out_stride;
   a.lse = lse;
+  a.w = w;
+  a.w_out = w_out;
   a.ws = static_cast<char*>(ws);
-  return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv_weights(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_kv_evict_workspace_bytes(int32_t B, int32_t kv_heads) {
+  if (B <= 0 || B > 65536 || kv_heads <= 0 || kv_heads > 1024) return 0;
+  return kAlign;
+}
+
+moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch, float* w,
+                             const int32_t* dst_table, int32_t dst_stride, const int32_t* budgets,
+                             int32_t width, int32_t first, int32_t recent, int32_t* kept,
+                             int32_t* new_lens, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_cache(cache);
+  if (st != MOE_OK) return st;
+  if ((st = check_batch(batch)) != MOE_OK) return st;
+  if (width <= 0 || first < 0 || recent < 0 || !w || !dst_table || !kept || !new_lens) return MOE_ERR_INVALID_ARG;
+  if (!aligned(w, 4) || !aligned(dst_table, 4) || !aligned(budgets, 4) || !aligned(kept, 4) || !aligned(new_lens, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (new_lens == batch->seq_lens) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30) || width > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  const int64_t pages = ((int64_t)width + cache->page_size - 1) / cache->page_size;
+  if (dst_stride < pages) return MOE_ERR_INVALID_ARG;
+  if (pages * batch->B * cache->kv_heads >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, moe_kv_evict_workspace_bytes(batch->B, cache->kv_heads))) != MOE_OK) return st;
+  EvictArgs a = {};
+  a.c = *cache;
+  a.b = *batch;
+  a.w = w;
+  a.dst_table = dst_table;
+  a.budgets = budgets;
+  a.dst_stride = dst_stride;
+  a.width = width;
+  a.first = first;
+  a.recent = recent;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.err = static_cast<uint32_t*>(ws);
+  return from_cuda(launch_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_residual_norm(const void* y, int64_t y_stride, int32_t y_dtype, const void* residual,
+                             int64_t residual_stride, void* out, int64_t out_stride,
+                             int32_t residual_dtype, void* normed, int64_t normed_stride,
+                             int32_t normed_dtype, int32_t T, int32_t H, const void* post_weight,
+                             const void* pre_weight, int32_t weight_dtype, const void* gate,
+                             int64_t gate_stride, int32_t gate_inner, int32_t gate_dtype,
+                             int32_t gate_sigmoid, float scale, float eps, float weight_offset,
+                             void* stream) {
+  auto known = [](int dt) { return act_dtype(dt) || dt == MOE_DTYPE_F32; };
+  auto size = [](int dt) { return dt == MOE_DTYPE_F32 ? 4 : 2; };
+  if (T <= 0 || H <= 0 || !residual || (!out && !normed)) return MOE_ERR_INVALID_ARG;
+  if (!y && (post_weight || gate)) return MOE_ERR_INVALID_ARG;
+  if (!known(residual_dtype) || (y && !known(y_dtype)) || (normed && !known(normed_dtype))) return MOE_ERR_INVALID_ARG;
+  if (((post_weight || pre_weight) && !known(weight_dtype)) || (gate && !known(gate_dtype))) return MOE_ERR_INVALID_ARG;
+  if (pre_weight && !normed) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f && eps < INFINITY) || !isfinite(scale) || !isfinite(weight_offset)) return MOE_ERR_INVALID_ARG;
+  if (gate && (gate_inner < 0 || gate_inner > 1 || gate_stride < 0)) return MOE_ERR_INVALID_ARG;
+  if (H > 32768) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(residual, size(residual_dtype)) || !aligned(out, size(residual_dtype)) ||
+      (y && !aligned(y, size(y_dtype))) || (normed && !aligned(normed, size(normed_dtype))) ||
+      !aligned(post_weight, size(weight_dtype)) || !aligned(pre_weight, size(weight_dtype)) ||
+      (gate && !aligned(gate, size(gate_dtype))))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 1 && (residual_stride < H || (out && out_stride < H) || (y && y_stride < H) || (normed && normed_stride < H)))
+    return MOE_ERR_INVALID_ARG;
+  // an output may lie on an input only row by row and value by value
+  auto on = [&](const void* p, int64_t ps, int pd, const void* in, int64_t is, int id) {
+    return !p || p != in || ((T == 1 || ps == is) && pd == id);
+  };
+  if (!on(out, out_stride, residual_dtype, residual, residual_stride, residual_dtype) ||
+      !on(out, out_stride, residual_dtype, y, y_stride, y_dtype) ||
+      !on(normed, normed_stride, normed_dtype, residual, residual_stride, residual_dtype) ||
+      !on(normed, normed_stride, normed_dtype, y, y_stride, y_dtype) || (out && out == normed))
+    return MOE_ERR_INVALID_ARG;
+  NormArgs a = {};
+  a.y = y;
+  a.residual = residual;
+  a.out = out;
+  a.normed = normed;
+  a.post = post_weight;
+  a.pre = pre_weight;
+  a.gate = gate;
+  a.y_stride = y_stride;
+  a.residual_stride = residual_stride;
+  a.out_stride = out_stride;
+  a.normed_stride = normed_stride;
+  a.gate_stride = gate_stride;
+  a.T = T;
+  a.H = H;
+  a.y_dtype = y ? y_dtype : residual_dtype;
+  a.residual_dtype = residual_dtype;
+  a.normed_dtype = normed_dtype;
+  a.weight_dtype = weight_dtype;
+  a.gate_dtype = gate_dtype;
+  a.gate_inner = gate ? gate_inner : 0;
+  a.sigmoid = gate_sigmoid != 0;
+  a.scale = scale;
+  a.eps = eps;
+  a.offset = weight_offset;
+  return from_cuda(launch_norm(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t K) {

@@ -1,7 +1,9 @@
 """Serving operators around the MoE layer: thin Python binding of include/moe_serving.h.
 
 NVFP4 matrix-vector products, the paged 8-bit key/value cache with the rotary rotation, causal
-attention over it, and the verification of drafted tokens.  Each ``moe_*`` function marshals its
+attention over it and attention for trees of drafted tokens, what a tree's accepted path or a
+budget leaves in the cache, the verification of drafted tokens, and the norms, gate and residual
+around a block.  Each ``moe_*`` function marshals its
 arguments and calls the C entry point of the same name; a non-OK status raises MoeError.
 ``NvFp4Linear`` keeps the buffers of one projection, as MoeLayer does for a layer.
 """
@@ -17,8 +19,10 @@ from ._native import MoeError, check as _check
 
 __all__ = ["PagedKvCache", "SeqBatch", "NvFp4Linear", "kv_append_workspace_bytes",
            "attention_workspace_bytes", "linear_workspace_bytes", "verify_workspace_bytes",
-           "moe_kv_append_rope_e4m3", "moe_attention_paged_e4m3", "moe_linear_nvfp4",
-           "moe_verify_draft"]
+           "kv_keep_workspace_bytes", "kv_weights_workspace_bytes", "kv_evict_workspace_bytes",
+           "moe_kv_append_rope_e4m3", "moe_attention_paged_e4m3", "moe_attention_tree_e4m3",
+           "moe_kv_keep_e4m3", "moe_kv_weights_e4m3", "moe_kv_evict_e4m3", "moe_linear_nvfp4",
+           "moe_verify_draft", "moe_residual_norm"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
@@ -164,6 +168,18 @@ def verify_workspace_bytes(B: int, V: int) -> int:
     return int(_native.load().moe_verify_workspace_bytes(B, V))
 
 
+def kv_keep_workspace_bytes() -> int:
+    return int(_native.load().moe_kv_keep_workspace_bytes())
+
+
+def kv_weights_workspace_bytes(T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_native.load().moe_kv_weights_workspace_bytes(T, q_heads, kv_heads, head_dim))
+
+
+def kv_evict_workspace_bytes(B: int, kv_heads: int) -> int:
+    return int(_native.load().moe_kv_evict_workspace_bytes(B, kv_heads))
+
+
 def moe_kv_append_rope_e4m3(cache: PagedKvCache, batch: SeqBatch, k: torch.Tensor, v: torch.Tensor,
                             cos: Optional[torch.Tensor], sin: Optional[torch.Tensor],
                             ws: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -220,6 +236,112 @@ def moe_attention_paged_e4m3(q: torch.Tensor, cache: PagedKvCache, batch: SeqBat
         q.data_ptr(), qs, T, qh, _dtype(q, "q"), cache._ref, batch._ref,
         d ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, lp, ws.data_ptr(),
         _workspace(dev, ws), _queue(dev, stream)), "moe_attention_paged_e4m3")
+
+
+def moe_attention_tree_e4m3(q: torch.Tensor, cache: PagedKvCache, batch: SeqBatch,
+                            tree_mask: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                            scale: Optional[float] = None, window: int = 0,
+                            lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_attention_paged_e4m3 for new tokens that form a tree: row t of tree_mask int32 [T, words]
+    has the bits of those new tokens of its sequence that token t sees (bit c % 32 of word c // 32:
+    its ancestors and itself); the tokens before the new ones it sees all."""
+    dev = _device()
+    if cache.dev != dev or batch.dev != dev:
+        raise _elsewhere("cache and batch")
+    d, shape, dt = cache.head_dim, q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"q must be [tokens, heads, {d}]")
+    T, qh, _ = shape
+    if tree_mask.get_device() != dev:
+        raise _elsewhere("tree_mask")
+    if tree_mask.dtype is not _I32 or tree_mask.dim() != 2:
+        raise TypeError("tree_mask must be int32 [tokens, words]")
+    words = tree_mask.shape[1]
+    if tree_mask.shape[0] != T or (words > 1 and tree_mask.stride(1) != 1):
+        raise ValueError("tree_mask must be [tokens, words] with contiguous rows")
+    qs, os_ = _rows(dev, q, dt, shape, "q"), _rows(dev, out, dt, shape, "out")
+    lp = None if lse is None else _need(dev, lse, _F32, (T, qh), "lse")
+    _check(_native.load().moe_attention_tree_e4m3(
+        q.data_ptr(), qs, T, qh, _dtype(q, "q"), cache._ref, batch._ref, tree_mask.data_ptr(), words,
+        tree_mask.stride(0) if T > 1 else words, d ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), os_, lp, ws.data_ptr(), _workspace(dev, ws), _queue(dev, stream)),
+        "moe_attention_tree_e4m3")
+
+
+def moe_kv_keep_e4m3(cache: PagedKvCache, batch: SeqBatch, keep: torch.Tensor, n_keep: torch.Tensor,
+                     new_lens: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Of each sequence's new tokens keep those numbered keep[b][:n_keep[b]] (int32 [B, width],
+    ascending), moved together behind the tokens before them; new_lens int32 [B] gets the lengths."""
+    dev = _device()
+    if cache.dev != dev or batch.dev != dev:
+        raise _elsewhere("cache and batch")
+    B = batch.B
+    if keep.dim() != 2 or keep.shape[0] != B:
+        raise ValueError(f"keep must be int32 [{B}, width]")
+    width = keep.shape[1]
+    kp = _need(dev, keep, _I32, (B, width), "keep")
+    _check(_native.load().moe_kv_keep_e4m3(
+        cache._ref, batch._ref, kp or None, _need(dev, n_keep, _I32, (B,), "n_keep"), width,
+        _need(dev, new_lens, _I32, (B,), "new_lens"), ws.data_ptr(), _workspace(dev, ws),
+        _queue(dev, stream)), "moe_kv_keep_e4m3")
+
+
+def _slots(cache: PagedKvCache) -> tuple:
+    return cache.num_pages, cache.kv_heads, cache.page_size
+
+
+def moe_kv_weights_e4m3(q: torch.Tensor, lse: torch.Tensor, cache: PagedKvCache, batch: SeqBatch,
+                        weights: torch.Tensor, ws: torch.Tensor, out: Optional[torch.Tensor] = None,
+                        scale: Optional[float] = None, window: int = 0, decay: float = 1.0,
+                        stream=None) -> None:
+    """weights float32 [num_pages, kv_heads, page_size] of the batch's tokens times decay (0 for new
+    tokens) plus what the rows q [T, q_heads, head_dim], whose lse [T, q_heads] the attention left,
+    give each of them; into out (weights itself when None). scale, window as in the attention."""
+    dev = _device()
+    if cache.dev != dev or batch.dev != dev:
+        raise _elsewhere("cache and batch")
+    d, shape, dt = cache.head_dim, q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"q must be [tokens, heads, {d}]")
+    T, qh, _ = shape
+    qs = _rows(dev, q, dt, shape, "q")
+    wp = _need(dev, weights, _F32, _slots(cache), "weights")
+    op = wp if out is None else _need(dev, out, _F32, _slots(cache), "out")
+    _check(_native.load().moe_kv_weights_e4m3(
+        q.data_ptr(), qs, T, qh, _dtype(q, "q"), _need(dev, lse, _F32, (T, qh), "lse"), cache._ref,
+        batch._ref, d ** -0.5 if scale is None else scale, window, decay, wp, op, ws.data_ptr(),
+        _workspace(dev, ws), _queue(dev, stream)), "moe_kv_weights_e4m3")
+
+
+def moe_kv_evict_e4m3(cache: PagedKvCache, batch: SeqBatch, weights: torch.Tensor,
+                      dst_table: torch.Tensor, kept: torch.Tensor, new_lens: torch.Tensor,
+                      ws: torch.Tensor, budgets: Optional[torch.Tensor] = None, first: int = 0,
+                      recent: int = 0, stream=None) -> None:
+    """Copy the tokens that a budget keeps (budgets int32 [B], at most kept's width; None: the width)
+    into the pages of dst_table int32 [B, pages]: the last `recent`, the first `first`, and the
+    largest weights [num_pages, kv_heads, page_size], for each key head. kept int32 [B, kv_heads,
+    width] gets their places, then -1, and new_lens int32 [B] their number."""
+    dev = _device()
+    if cache.dev != dev or batch.dev != dev:
+        raise _elsewhere("cache and batch")
+    B = batch.B
+    if dst_table.get_device() != dev:
+        raise _elsewhere("dst_table")
+    if dst_table.dtype is not _I32 or dst_table.dim() != 2 or \
+            (dst_table.shape[1] > 1 and dst_table.stride(1) != 1):
+        raise TypeError("dst_table must be int32 [B, pages] with contiguous rows")
+    if kept.dim() != 3:
+        raise ValueError(f"kept must be int32 [{B}, {cache.kv_heads}, width]")
+    width = kept.shape[2]
+    if dst_table.shape[0] != B or dst_table.shape[1] * cache.page_size < width:
+        raise ValueError("dst_table must have a row per sequence and pages for kept's width")
+    bp = None if budgets is None else _need(dev, budgets, _I32, (B,), "budgets")
+    _check(_native.load().moe_kv_evict_e4m3(
+        cache._ref, batch._ref, _need(dev, weights, _F32, _slots(cache), "weights"),
+        dst_table.data_ptr(), dst_table.stride(0) if B > 1 else dst_table.shape[1], bp, width, first,
+        recent, _need(dev, kept, _I32, (B, cache.kv_heads, width), "kept"),
+        _need(dev, new_lens, _I32, (B,), "new_lens"), ws.data_ptr(), _workspace(dev, ws),
+        _queue(dev, stream)), "moe_kv_evict_e4m3")
 
 
 def moe_linear_nvfp4(x: torch.Tensor, bank, y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
@@ -282,6 +404,66 @@ def _prob_rows(dev: int, t: torch.Tensor, dtype: torch.dtype, shape: tuple, what
     if B > 1 and rows > 0 and sb != rows * stride:
         raise ValueError(f"{what}: rows must be evenly spaced over sequences")
     return stride
+
+
+def _matrix(dev: int, t: torch.Tensor, T: int, H: int, what: str) -> tuple:
+    """Address, row stride and type of rows [T, H] whose values are neighbours."""
+    if t.get_device() != dev:
+        raise _elsewhere(what)
+    if t.shape != (T, H):
+        raise ValueError(f"{what} must be [{T}, {H}]")
+    s0, s1 = t.stride()
+    if s1 != 1 and H > 1:
+        raise ValueError(f"{what}: a row must be contiguous")
+    return t.data_ptr(), s0 if T > 1 else H, _dtype(t, what)
+
+
+def moe_residual_norm(y: Optional[torch.Tensor], residual: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None,
+                      post_weight: Optional[torch.Tensor] = None,
+                      pre_weight: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, gate_sigmoid: bool = False,
+                      scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0,
+                      stream=None) -> None:
+    """out = residual + scale * gate * norm(y, post_weight) and normed = norm(out, pre_weight), over
+    rows [T, H]; without post_weight y is not normed, without pre_weight normed has weights of 1, and
+    y None takes the residual alone. gate is [T, H], [T, 1] or [1, H] (or None), under a sigmoid with
+    gate_sigmoid; weights [H] are taken as weight + weight_offset."""
+    dev = _device()
+    if residual.dim() != 2:
+        raise ValueError("residual must be [tokens, hidden]")
+    T, H = residual.shape
+    rp, rs, rt = _matrix(dev, residual, T, H, "residual")
+    yp, ys, yt = (None, H, rt) if y is None else _matrix(dev, y, T, H, "y")
+    op, os_, ot = (None, H, rt) if out is None else _matrix(dev, out, T, H, "out")
+    np_, ns, nt = (None, H, rt) if normed is None else _matrix(dev, normed, T, H, "normed")
+    if ot != rt:
+        raise TypeError("out must have the residual's type")
+    wt, ptrs = 0, []
+    for w, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if w is None:
+            ptrs.append(None)
+            continue
+        code = _dtype(w, what)
+        if any(p is not None for p in ptrs) and code != wt:
+            raise TypeError("post_weight and pre_weight must have one type")
+        wt = code
+        ptrs.append(_need(dev, w, w.dtype, (H,), what))
+    gp, gs, gi, gt = None, 0, 0, 0
+    if gate is not None:
+        if gate.get_device() != dev:
+            raise _elsewhere("gate")
+        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
+            raise ValueError(f"gate must be [{T}, {H}], [{T}, 1] or [1, {H}]")
+        gp, gt = gate.data_ptr(), _dtype(gate, "gate")
+        gi = 1 if gate.shape[1] > 1 else 0
+        if gi and gate.stride(1) != 1:
+            raise ValueError("gate: a row must be contiguous")
+        gs = gate.stride(0) if gate.shape[0] > 1 else 0
+    _check(_native.load().moe_residual_norm(
+        yp, ys, yt, rp, rs, op, os_, rt, np_, ns, nt, T, H, ptrs[0], ptrs[1], wt, gp, gs, gi, gt,
+        1 if gate_sigmoid else 0, scale, eps, weight_offset, _queue(dev, stream)),
+        "moe_residual_norm")
 
 
 class NvFp4Linear:
