@@ -1,12 +1,21 @@
 // Norm of a block's output, gate, residual and the next block's norm in one pass (moe_residual_norm).
 //
-// Row statistics are sums of squares in f32: a CTA takes a row, each thread holds its values of y and
-// of the residual in registers (both are asked for before the first sum), and the two sums meet
-// through shuffles and shared memory. y, the residual and the gate are read once and the outputs
-// written once; weights come from L1 after a CTA's first row. CTAs take rows in turn.
+// Row statistics are sums of squares in f32: a CTA takes a row, each thread holds eight neighbouring
+// values of y and of the residual in registers, and the two sums meet through shuffles and shared
+// memory. y, the residual and the gate are read once and the outputs written once; the weights stay
+// in registers over all rows of a CTA. A CTA takes every grid-th row, and the next row's values are
+// asked for as soon as a row's are used up, before its sums meet and its stores.
 //
-// Threads and vectors per thread follow H alone: the fewest threads (up to 256) whose one vector of
-// eight values covers a row, beyond that two vectors, then more threads.
+// A CTA has as many threads as the row has vectors of eight (H = 2560: 320), up to 1024; rows beyond
+// 8192 values take two or four vectors per thread (without registers for weights and the next row),
+// and rows that are no whole 16-byte vectors are read
+// value by value.
+//
+// Bound by bytes for many rows. 4096 x 4096, y f32, residual and outputs bf16, a gate per row:
+// 31.7 us, 5.3 TB/s (0.78 of the copy rate); one row of 2560: 3.6 us in a graph, which is the launch
+// and one chain of loads and two sums. Measured against this at 4096 x 4096: rows ahead in shared
+// memory (cp.async) instead of in registers 36.6 us (one) and 36.7 us (two); rows and their gates read
+// only when they are taken 38.9; 40 registers per thread and half again as many threads 44.6.
 #include "serving.cuh"
 
 namespace moe {
@@ -24,15 +33,18 @@ __device__ __forceinline__ float scalar_of(uint32_t bits, int dtype) {
 
 // Where value x of a thread's vector v lies in the row: neighbouring values for whole vectors,
 // neighbouring threads otherwise.
-template <int THREADS, bool VEC>
+template <bool VEC>
 __device__ __forceinline__ int place_of(int v, int x) {
-  return VEC ? (v * THREADS + threadIdx.x) * 8 + x : (v * 8 + x) * THREADS + (int)threadIdx.x;
+  return VEC ? (int)(v * blockDim.x + threadIdx.x) * 8 + x : (int)((v * 8 + x) * blockDim.x + threadIdx.x);
 }
 
-template <int THREADS, bool VEC, bool F32>
+// Asks for a thread's eight values of a row; 0 past its end.
+template <bool VEC, bool F32>
 __device__ __forceinline__ void ask(Raw<F32>& r, const void* row, int v, int H) {
   if (VEC) {
-    const int at = place_of<THREADS, VEC>(v, 0);
+    const int at = place_of<VEC>(v, 0);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) r.w[i] = 0;
     if (at < H) {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)at * (F32 ? 4 : 2));
       const uint4 a = *p;
@@ -41,10 +53,7 @@ __device__ __forceinline__ void ask(Raw<F32>& r, const void* row, int v, int H) 
         const uint4 b = p[1];
         r.w[F32 ? 4 : 0] = b.x, r.w[F32 ? 5 : 0] = b.y, r.w[F32 ? 6 : 0] = b.z, r.w[F32 ? 7 : 0] = b.w;
       }
-      return;
     }
-#pragma unroll
-    for (int i = 0; i < (F32 ? 8 : 4); ++i) r.w[i] = 0;
     return;
   }
 #pragma unroll
@@ -52,7 +61,7 @@ __device__ __forceinline__ void ask(Raw<F32>& r, const void* row, int v, int H) 
     uint32_t b[2] = {0, 0};
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const int at = place_of<THREADS, VEC>(v, x + y);
+      const int at = place_of<VEC>(v, x + y);
       if (at < H) b[y] = F32 ? static_cast<const uint32_t*>(row)[at] : static_cast<const uint16_t*>(row)[at];
     }
     if (F32) {
@@ -75,24 +84,24 @@ __device__ __forceinline__ void values_of(const Raw<F32>& r, int dtype, float (&
   }
 }
 
-// Eight values of an operand that is the same for every row or small (weights, gates).
-template <int THREADS, bool VEC>
+// Eight values of a row of weights or gates.
+template <bool VEC>
 __device__ __forceinline__ void operand(const void* row, int dtype, int v, int H, float (&f)[8]) {
   if (dtype == MOE_DTYPE_F32) {
     Raw<true> r;
-    ask<THREADS, VEC, true>(r, row, v, H);
+    ask<VEC, true>(r, row, v, H);
     values_of<true>(r, dtype, f);
   } else {
     Raw<false> r;
-    ask<THREADS, VEC, false>(r, row, v, H);
+    ask<VEC, false>(r, row, v, H);
     values_of<false>(r, dtype, f);
   }
 }
 
-template <int THREADS, bool VEC>
+template <bool VEC>
 __device__ __forceinline__ void put(void* row, int dtype, int v, int H, const float (&f)[8]) {
   if (VEC) {
-    const int at = place_of<THREADS, VEC>(v, 0);
+    const int at = place_of<VEC>(v, 0);
     if (at >= H) return;
     if (dtype == MOE_DTYPE_F32) {
       float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
@@ -106,7 +115,7 @@ __device__ __forceinline__ void put(void* row, int dtype, int v, int H, const fl
   }
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
-    const int at = place_of<THREADS, VEC>(v, x);
+    const int at = place_of<VEC>(v, x);
     if (at >= H) continue;
     if (dtype == MOE_DTYPE_F32) {
       static_cast<float*>(row)[at] = f[x];
@@ -117,139 +126,216 @@ __device__ __forceinline__ void put(void* row, int dtype, int v, int H, const fl
   }
 }
 
-// Sum over the block, the same in every thread. `slot` is one of two, used in turn, so that one
-// barrier per sum is enough.
-template <int THREADS>
-__device__ __forceinline__ float block_sum(float v, float (*s)[THREADS / 32], int slot) {
+// Pairs of f32 in one 64-bit register, and eight values as four of them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+struct Eight {
+  uint64_t p[4];
+};
+__device__ __forceinline__ Eight pack(const float (&f)[8]) {
+  return {{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+}
+__device__ __forceinline__ void unpack(const Eight& e, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(e.p[i], f[2 * i], f[2 * i + 1]);
+}
+
+// Sum over the block of the pairs' sums, the same in every thread. `s` is one of two rows, used in turn,
+// so that one barrier per sum is enough; it is 0 past the block's warps.
+__device__ __forceinline__ float block_sum(uint64_t pairs, float* s) {
+  float v, u;
+  unpair(pairs, v, u);
+  v += u;
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (THREADS == 32) return v;
-  if ((threadIdx.x & 31) == 0) s[slot][threadIdx.x >> 5] = v;
+  if (blockDim.x == 32) return v;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
   float all = 0.0f;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) all += s[slot][w];
+  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(s + w);
+    all += (f.x + f.y) + (f.z + f.w);
+  }
   return all;
 }
 
-template <int THREADS, int V, bool VEC, bool Y32, bool R32>
-__global__ void __launch_bounds__(THREADS) norm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float s_sum[2][THREADS / 32];
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+template <int MOST, int V, bool VEC, bool Y32, bool R32>
+__global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ __align__(16) float s_sum[2][32];
+  constexpr int kY = Y32 ? 4 : 2, kR = R32 ? 4 : 2;
+  constexpr bool kHold = V == 1;
   const float each = 1.0f / (float)a.H;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const char* yr = static_cast<const char*>(a.y) + (int64_t)t * a.y_stride * (Y32 ? 4 : 2);
-    const char* rr = static_cast<const char*>(a.residual) + (int64_t)t * a.residual_stride * (R32 ? 4 : 2);
-    Raw<Y32> yw[V];
-    Raw<R32> rw[V];
+  const char* y = static_cast<const char*>(a.y) + (int64_t)blockIdx.x * a.y_stride * kY;
+  const char* res = static_cast<const char*>(a.residual) + (int64_t)blockIdx.x * a.residual_stride * kR;
+  const int64_t y_step = gridDim.x * a.y_stride * kY, res_step = gridDim.x * a.residual_stride * kR;
+  const int gate_size = a.gate_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const char* gate = static_cast<const char*>(a.gate) + (int64_t)blockIdx.x * a.gate_stride * gate_size;
+  const int64_t gate_step = gridDim.x * a.gate_stride * gate_size;
+  Raw<Y32> yw[V];
+  Raw<R32> rw[V];
+  uint32_t gate_bits = 0;                      // a gate that is one value per row
+  auto ask_rows = [&] {
     if (a.y) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) ask<THREADS, VEC, Y32>(yw[v], yr, v, a.H);
+      for (int v = 0; v < V; ++v) ask<VEC, Y32>(yw[v], y, v, a.H);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) ask<THREADS, VEC, R32>(rw[v], rr, v, a.H);
-    float r[V][8];
+    for (int v = 0; v < V; ++v) ask<VEC, R32>(rw[v], res, v, a.H);
+    if (a.gate && !a.gate_inner)
+      gate_bits = gate_size == 4 ? *reinterpret_cast<const uint32_t*>(gate) : *reinterpret_cast<const uint16_t*>(gate);
+    y += y_step, res += res_step;
+  };
+  if (kHold) ask_rows();
+  if (threadIdx.x < 32) s_sum[0][threadIdx.x] = s_sum[1][threadIdx.x] = 0.0f;
+  Eight held[2];
+  auto weights = [&](const void* w, int v) {
+    float f[8];
+    operand<VEC>(w, a.weight_dtype, v, a.H, f);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) f[x] += a.offset;
+    return pack(f);
+  };
+  if (kHold && a.post) held[0] = weights(a.post, 0);
+  if (kHold && a.pre) held[1] = weights(a.pre, 0);
+  if (blockDim.x > 32) __syncthreads();
+
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (!kHold) ask_rows();
+    Eight r[V];
+    float k = a.scale;
+    if (a.gate && !a.gate_inner) {
+      const float g = gate_size == 4 ? __uint_as_float(gate_bits) : scalar_of(gate_bits, a.gate_dtype);
+      k *= a.sigmoid ? sigmoid(g) : g;
+    }
+    Eight z[V];
+    uint64_t sum = 0;
     if (a.y) {
-      float k = a.scale;
-      if (a.post) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float f[8];
-          values_of<Y32>(yw[v], a.y_dtype, f);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) sum = fmaf(f[x], f[x], sum);
-        }
-        sum = block_sum<THREADS>(sum, s_sum, 0);
-        k = a.scale * rsqrtf(fmaf(sum, each, a.eps));
-      }
-      const int64_t g0 = (int64_t)t * a.gate_stride;
-      const char* gr = static_cast<const char*>(a.gate) + g0 * (a.gate_dtype == MOE_DTYPE_F32 ? 4 : 2);
-      if (a.gate && !a.gate_inner) {
-        const float g = a.gate_dtype == MOE_DTYPE_F32 ? *reinterpret_cast<const float*>(gr)
-                                                      : scalar_of(*reinterpret_cast<const uint16_t*>(gr), a.gate_dtype);
-        k *= a.sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
-      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float z[8];
-        values_of<Y32>(yw[v], a.y_dtype, z);
-        values_of<R32>(rw[v], a.residual_dtype, r[v]);
-        if (a.post) {
-          float w[8];
-          operand<THREADS, VEC>(a.post, a.weight_dtype, v, a.H, w);
+        float f[8];
+        values_of<Y32>(yw[v], a.y_dtype, f);
+        z[v] = pack(f);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) z[x] *= w[x] + a.offset;
+        for (int i = 0; i < 4; ++i) sum = fma2(z[v].p[i], z[v].p[i], sum);
+        if (a.post) {                          // what does not need the sum, before it
+          const Eight w = kHold ? held[0] : weights(a.post, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[v].p[i] = mul2(z[v].p[i], w.p[i]);
         }
         if (a.gate && a.gate_inner) {
-          float g[8];
-          operand<THREADS, VEC>(gr, a.gate_dtype, v, a.H, g);
+          operand<VEC>(gate, a.gate_dtype, v, a.H, f);
+          if (a.sigmoid) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) z[x] *= a.sigmoid ? 1.0f / (1.0f + expf(-g[x])) : g[x];
+            for (int x = 0; x < 8; ++x) f[x] = sigmoid(f[x]);
+          }
+          const Eight g = pack(f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[v].p[i] = mul2(z[v].p[i], g.p[i]);
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) r[v][x] = fmaf(z[x], k, r[v][x]);
       }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) values_of<R32>(rw[v], a.residual_dtype, r[v]);
     }
-    if (a.out) {
-      char* to = static_cast<char*>(a.out) + (int64_t)t * a.out_stride * (R32 ? 4 : 2);
 #pragma unroll
-      for (int v = 0; v < V; ++v) put<THREADS, VEC>(to, a.residual_dtype, v, a.H, r[v]);
+    for (int v = 0; v < V; ++v) {
+      float f[8];
+      values_of<R32>(rw[v], a.residual_dtype, f);
+      r[v] = pack(f);
     }
-    if (a.normed) {
-      float sum = 0.0f;
+    gate += gate_step;
+    if (kHold && a.T - t > (int)gridDim.x) ask_rows();  // the next row, into registers that this one is done with
+    if (a.y) {
+      if (a.post) k *= rsqrtf(fmaf(block_sum(sum, s_sum[0]), each, a.eps));
+      const uint64_t kk = pair(k, k);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (place_of<THREADS, VEC>(v, x) < a.H) sum = fmaf(r[v][x], r[v][x], sum);
-      sum = block_sum<THREADS>(sum, s_sum, 1);
-      const float k = rsqrtf(fmaf(sum, each, a.eps));
-      char* to = static_cast<char*>(a.normed) + (int64_t)t * a.normed_stride * (a.normed_dtype == MOE_DTYPE_F32 ? 4 : 2);
+        for (int i = 0; i < 4; ++i) r[v].p[i] = fma2(z[v].p[i], kk, r[v].p[i]);
+    }
+    if (a.normed) {
+      sum = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (a.pre) {
-          float w[8];
-          operand<THREADS, VEC>(a.pre, a.weight_dtype, v, a.H, w);
+        // values past the row count as 0 (a factor may have made NaN of them)
+        if (!VEC) {
+          float f[8];
+          unpack(r[v], f);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) r[v][x] *= k * (w[x] + a.offset);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) r[v][x] *= k;
+          for (int x = 0; x < 8; ++x) f[x] = place_of<VEC>(v, x) < a.H ? f[x] : 0.0f;
+          r[v] = pack(f);
         }
-        put<THREADS, VEC>(to, a.normed_dtype, v, a.H, r[v]);
+        if (!VEC || place_of<VEC>(v, 0) < a.H) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum = fma2(r[v].p[i], r[v].p[i], sum);
+        }
+      }
+      const float n = rsqrtf(fmaf(block_sum(sum, s_sum[1]), each, a.eps));
+      char* to = static_cast<char*>(a.normed) + (int64_t)t * a.normed_stride * (a.normed_dtype == MOE_DTYPE_F32 ? 4 : 2);
+      const uint64_t nn = pair(n, n);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        Eight e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e.p[i] = mul2(r[v].p[i], nn);
+        if (a.pre) {
+          const Eight w = kHold ? held[1] : weights(a.pre, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e.p[i] = mul2(e.p[i], w.p[i]);
+        }
+        float f[8];
+        unpack(e, f);
+        put<VEC>(to, a.normed_dtype, v, a.H, f);
       }
     }
-    // a sum's slot is written again only behind the other sum's barrier; where a row has one sum
+    if (a.out) {
+      char* to = static_cast<char*>(a.out) + (int64_t)t * a.out_stride * kR;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float f[8];
+        unpack(r[v], f);
+        put<VEC>(to, a.residual_dtype, v, a.H, f);
+      }
+    }
+    // a sum's slots are written again only behind the other sum's barrier; where a row has one sum
     // or none of the two this barrier stands in for it
-    if (THREADS > 32 && !(a.y && a.post && a.normed)) __syncthreads();
+    if (blockDim.x > 32 && !(a.y && a.post && a.normed)) __syncthreads();
   }
 }
 
-template <int THREADS, int V, bool VEC>
-cudaError_t launch_types(const NormArgs& a, cudaStream_t s) {
+template <int MOST, int V, bool VEC>
+cudaError_t launch_size(const NormArgs& a, cudaStream_t s) {
   const bool y32 = a.y_dtype == MOE_DTYPE_F32, r32 = a.residual_dtype == MOE_DTYPE_F32;
-  const int per_sm = 2048 / THREADS < 32 ? 2048 / THREADS : 32;
-  const long long most = (long long)num_sms() * per_sm;
-  const dim3 grid((unsigned)(a.T < most ? a.T : most));
-  if (y32 && r32) norm_kernel<THREADS, V, VEC, true, true><<<grid, THREADS, 0, s>>>(a);
-  else if (y32) norm_kernel<THREADS, V, VEC, true, false><<<grid, THREADS, 0, s>>>(a);
-  else if (r32) norm_kernel<THREADS, V, VEC, false, true><<<grid, THREADS, 0, s>>>(a);
-  else norm_kernel<THREADS, V, VEC, false, false><<<grid, THREADS, 0, s>>>(a);
+  const int threads = V > 1 ? MOST : (a.H + 255) / 256 * 32;
+  const long long most = (long long)num_sms() * (1024 / threads);
+  const unsigned grid = (unsigned)(a.T < most ? a.T : most);
+  if (y32 && r32) norm_kernel<MOST, V, VEC, true, true><<<grid, threads, 0, s>>>(a);
+  else if (y32) norm_kernel<MOST, V, VEC, true, false><<<grid, threads, 0, s>>>(a);
+  else if (r32) norm_kernel<MOST, V, VEC, false, true><<<grid, threads, 0, s>>>(a);
+  else norm_kernel<MOST, V, VEC, false, false><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <bool VEC>
-cudaError_t launch_size(const NormArgs& a, cudaStream_t s) {
-  if (a.H <= 256) return launch_types<32, 1, VEC>(a, s);
-  if (a.H <= 1024) return launch_types<128, 1, VEC>(a, s);
-  if (a.H <= 2048) return launch_types<256, 1, VEC>(a, s);
-  if (a.H <= 4096) return launch_types<256, 2, VEC>(a, s);
-  if (a.H <= 8192) return launch_types<512, 2, VEC>(a, s);
-  if (a.H <= 16384) return launch_types<1024, 2, VEC>(a, s);
-  return launch_types<1024, 4, VEC>(a, s);
+cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
+  if (a.H <= 4096) return launch_size<512, 1, VEC>(a, s);
+  if (a.H <= 8192) return launch_size<1024, 1, VEC>(a, s);
+  return a.H <= 16384 ? launch_size<1024, 2, VEC>(a, s) : launch_size<1024, 4, VEC>(a, s);
 }
 
 bool whole(const void* p, int64_t stride, int bytes) {   // rows that vectors of eight values may be read from
@@ -265,7 +351,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
                    whole(a.out, a.out_stride, size(a.residual_dtype)) &&
                    whole(a.normed, a.normed_stride, size(a.normed_dtype)) && whole(a.post, 0, 2) &&
                    whole(a.pre, 0, 2) && (!a.gate_inner || whole(a.gate, a.gate_stride, size(a.gate_dtype)));
-  return vec ? launch_size<true>(a, s) : launch_size<false>(a, s);
+  return vec ? launch_rows<true>(a, s) : launch_rows<false>(a, s);
 }
 
 }  // namespace moe
