@@ -221,8 +221,8 @@ size_t moe_kv_weights_workspace_bytes(int32_t T, int32_t q_heads, int32_t kv_hea
  * over the rows r (new tokens, times the query heads of h) that see j as in
  * moe_attention_paged_e4m3 (causal, window), whose lse is given here; a row with lse -inf adds
  * nothing. decay 0 does not read w. Sequences without new tokens, and slots past a sequence's
- * end, are left alone. A NaN key code makes the weights of its token NaN if a row sees it.
- *   w, w_out  f32 [num_pages][kv_heads][page_size], the slots of the cache; may be the same
+ * end, are left alone; two sequences with new tokens must not have a page in common. A NaN key code makes the weights of its token NaN if a row sees it.
+ *   w, w_out  f32 [num_pages][kv_heads][page_size], the slots of the cache, 16-byte aligned; may be the same
  *   lse       f32 [T][q_heads]                       decay within [0, 1]
  * Products are as in the attention (f16 operands, f32 sums); each token's sum is made in one order,
  * so two calls give the same bits. Tokens in pages out of range are left out (MOE_DEVERR_PAGE). */

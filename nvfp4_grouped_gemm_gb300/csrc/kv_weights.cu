@@ -1,130 +1,43 @@
 // Attention weights that cached tokens have gathered (moe_kv_weights_e4m3): for each key the sum of
-// exp(s - lse) over the rows that see it, the rows' lse being known.
-//
-// Nothing has to be joined: a key's sum belongs to one warp. All (sequence, key head) keys are cut into
-// steps of 32 tokens, which form one line; the grid cuts it into equal pieces and a CTA's warps take
-// its piece's steps in turn. Keys go from global memory straight into the fragments of mma.sync
-// m16n8k16 as the 16-row operand: lane 4g + c reads, of keys g and 8 + g of a half-step, 16
-// consecutive codes at 16c of every 64; the four codes of a word are its values of one k-step, and a
-// row's query values are taken with the same permutation of k, i.e. also 16 consecutive ones. A step's
-// codes are asked for while the step before is worked on, its page two steps ahead.
-//
-// The rows come in tiles of 8, the columns of the product. Up to 8 rows (a decode step) a warp keeps the
-// tile's fragments in registers and makes them itself from q. For more rows prepare_kernel lays all
-// rows out once as such fragments (f16 times a power of two, as the attention does), and the warps
-// read them through L1 for every step.
+// exp(s - lse) over the rows (new tokens times query heads per key head) that see it, the rows' lse
+// being known:
 //   w += 2^(s * scale * k_scale * rowf * log2 e - lse * log2 e)      (f32, ex2.approx)
-#include "serving.cuh"
+//
+// Nothing has to be joined: a key belongs to one thread. All (sequence, key head) keys are cut into
+// tiles of 128 tokens, which form one line; the grid cuts it into equal pieces. prepare_kernel lays the
+// rows out once, as f16 times a power of two (as the attention does) in the swizzled order of the
+// products' operand; the main kernel starts beside it. In a CTA one warp brings tiles of codes into a
+// ring (TMA, a box per page) and their tokens' old weights, pages and scales into another, one brings
+// blocks of rows and their factors, the next block ahead, and groups of four warps take the tiles in
+// turn, thread = key:
+//   the key's codes to f16 (exact) in tensor memory; S = K Q^T with the keys from there as the 128-row
+//   operand (tcgen05, f32; one thread issues); the key's row of S, weights, their sum, and the token's
+//   new weight
+// A tile is one chain of waits and dependent instructions of its group, most of it not arithmetic, so
+// what counts is how many groups an SM has. The widened keys go to tensor memory and not to shared
+// memory, whose bandwidth would be the limit: a code is written there and read once. Rows beyond a
+// block take the piece's tiles again and add to what the block before left.
+#include "tc_f16.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kStep = 32;
+constexpr int kTile = 128;                     // keys
+constexpr int kPrepWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
-}
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                    uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int m) {
-  return m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w;
-}
-
-// A lane's share of a tile of 8 rows: the values 64 j + 16 c .. + 15 of row g for every j, two uint4
-// each (words 0, 1 meet the keys' word 0, and so on).
-template <int D>
-struct Tile {
-  uint4 v[D / 32];
-};
-
-// The 8 rows from row0 on, of key head h, numbered over the call: row t * group + r is query head
-// h * group + r of token t. Rows from row_hi on become 0. *rowf: the power of two taken out of row g.
-template <int D>
-__device__ __forceinline__ void read_tile(Tile<D>& t, float* rowf, const WeightsArgs& a, int group, int h, int row0,
-                                          int row_hi, int lane) {
-  const int g = lane >> 2, c = lane & 3, row = row0 + g;
-  const bool there = row < row_hi;
-  const uint16_t* src = a.q + (int64_t)(row / group) * a.q_stride + (int64_t)(h * group + row % group) * D + 16 * c;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    t.v[i] = make_uint4(0, 0, 0, 0);
-    if (there) t.v[i] = *reinterpret_cast<const uint4*>(src + 64 * (i / 2) + 8 * (i & 1));
-  }
-  *rowf = 1.0f;
-  if (a.dtype != MOE_DTYPE_BF16) return;
-  // bf16 rows get the power of two that puts their largest magnitude below 2^15
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    float f[8];
-    unpack8<MOE_DTYPE_BF16>(t.v[i], f);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(f[x]));
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const int e = amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
-  const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
-  *rowf = pow2f(e);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    float f[8];
-    unpack8<MOE_DTYPE_BF16>(t.v[i], f);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) f[x] = f[x] * s1 * s2;
-    t.v[i] = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
-  }
-}
-// What is subtracted from a row's exponents; +inf (no weight) for rows that saw nothing.
-__device__ __forceinline__ float less_of(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
-
-// Workspace behind the error word: rows' factors float2 {rowf, less} [kv_heads][tiles][8], then the
-// tiles uint4 [kv_heads][tiles][D / 32][32].
-__host__ __device__ inline int tiles_of(long long T, int group) { return (int)((T * group + 7) / 8); }
-__host__ __device__ inline size_t laid_at(int heads, int tiles) {
-  return kAlign + ((size_t)heads * tiles * 64 + kAlign - 1) / kAlign * kAlign;
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant__ WeightsArgs a) {
-  const int lane = threadIdx.x & 31, heads = a.c.kv_heads, group = a.q_heads / heads;
-  const int tiles = tiles_of(a.T, group), rows = a.T * group;
-  float2* info = reinterpret_cast<float2*>(a.ws + kAlign);
-  uint4* out = reinterpret_cast<uint4*>(a.ws + laid_at(heads, tiles));
-  pdl_trigger();
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (w >= (long long)heads * tiles) return;
-  const int h = (int)(w / tiles), tile = (int)(w % tiles);
-  Tile<D> t;
-  float rowf;
-  read_tile<D>(t, &rowf, a, group, h, tile * 8, rows, lane);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) out[(w * (D / 32) + i) * 32 + lane] = t.v[i];
-  const int row = tile * 8 + (lane >> 2);
-  if ((lane & 3) == 0)
-    info[w * 8 + (lane >> 2)] = make_float2(
-        rowf, row < rows ? less_of(a.lse[(int64_t)(row / group) * a.q_heads + h * group + row % group]) : INFINITY);
-}
+// Rows are kept in groups of 8 that begin anew with every sequence: sequence b's first group is
+// q_offsets[b] * group / 8 + q_offsets[b], which leaves room for the last group of each that is not full.
+// Workspace behind the error word: factors [kv_heads][groups][4] of float4 {rowf, rowf, -less, -less} of
+// two rows each, new-token numbers int [groups][8], rows f16 [kv_heads][D / 64][groups][8][64], swizzled.
+__host__ __device__ inline long long groups_of(long long T, int group) { return T * group / 8 + T + 1; }
+__device__ __forceinline__ int first_group(int row0, int group) { return (int)((long long)row0 * group / 8 + row0); }
+__host__ __device__ inline size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+__host__ __device__ inline size_t tokens_at(int heads, long long groups) { return kAlign + round_up((size_t)heads * groups * 64); }
+__host__ __device__ inline size_t rows_at(int heads, long long groups) { return tokens_at(heads, groups) + round_up((size_t)groups * 32); }
 
 struct Seq {
-  int row0, n, start, len, steps;
+  int row0, n, start, len, tiles;
 };
 __device__ __forceinline__ Seq read_seq(const WeightsArgs& a, int b, uint32_t* err) {
   Seq q;
@@ -136,277 +49,527 @@ __device__ __forceinline__ Seq read_seq(const WeightsArgs& a, int b, uint32_t* e
   const int cap = a.b.max_pages * a.c.page_size;
   if (q.n > 0 && (q.start < 0 || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
-  q.steps = q.n > 0 ? (q.len + kStep - 1) / kStep : 0;
+  q.tiles = q.n > 0 ? (q.len + kTile - 1) / kTile : 0;
   return q;
 }
 
-__device__ long long block_scan(long long v, long long* s_sum, long long* before) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+// A warp per 8 rows of a key head; block (b, y) works for sequence b.
+template <int D>
+__global__ void __launch_bounds__(32 * kPrepWarps) prepare_kernel(const __grid_constant__ WeightsArgs a) {
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, heads = a.c.kv_heads, group = a.q_heads / heads;
+  const long long groups = groups_of(a.T, group);
+  const Seq q = read_seq(a, blockIdx.x, nullptr);
+  const int rows = q.n * group, mine = (rows + 7) / 8, at0 = first_group(q.row0, group);
+  float* info = reinterpret_cast<float*>(a.ws + kAlign);
+  int* tokens = reinterpret_cast<int*>(a.ws + tokens_at(heads, groups));
+  char* out = a.ws + rows_at(heads, groups);
+  for (long long it = (long long)blockIdx.y * kPrepWarps + (threadIdx.x >> 5); it < (long long)heads * mine;
+       it += (long long)gridDim.y * kPrepWarps) {
+    const int h = (int)(it / mine), tile = (int)(it % mine), row = tile * 8 + g;
+    const bool there = row < rows;
+    const int64_t token = q.row0 + (there ? row / group : 0), hq = h * group + row % group;
+    const uint16_t* src = a.q + token * a.q_stride + hq * D;
+    uint4 v[D / 32];                           // 16-byte pieces c, c + 4, ... of the row
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += up;
-  }
-  __syncthreads();
-  if (lane == 31) s_sum[warp] = x;
-  __syncthreads();
-  long long base = 0, all = 0;
+    for (int i = 0; i < D / 32; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (there) v[i] = *reinterpret_cast<const uint4*>(src + (c + 4 * i) * 8);
+    }
+    const float lse = there ? a.lse[token * a.q_heads + hq] : -INFINITY;
+    float rowf = 1.0f;
+    if (a.dtype == MOE_DTYPE_BF16) {
+      // bf16 rows get the power of two that puts their largest magnitude below 2^15
+      float amax = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += s_sum[w];
-    all += s_sum[w];
+      for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        unpack8<MOE_DTYPE_BF16>(v[i], f);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(f[x]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = amax < 3.4e38f ? f16_prescale_exp(amax) : 0;
+      const float s1 = pow2f(-e / 2), s2 = pow2f(-e - (-e / 2));
+      rowf = pow2f(e);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        unpack8<MOE_DTYPE_BF16>(v[i], f);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) f[x] = f[x] * s1 * s2;
+        v[i] = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int piece = c + 4 * i;
+      char* to = out + (((int64_t)h * (D / 64) + (piece >> 3)) * groups + at0 + tile) * 1024 + g * 128;
+      *reinterpret_cast<uint4*>(to + (((piece & 7) ^ g) * 16)) = v[i];
+    }
+    if (c == 0) {
+      float* f = info + (((int64_t)h * groups + at0 + tile) * 4 + g / 2) * 4;
+      f[g & 1] = rowf;
+      f[2 + (g & 1)] = lse == -INFINITY ? -INFINITY : -(lse * kLog2e);   // rows that saw nothing add nothing
+      if (h == 0) tokens[(int64_t)(at0 + tile) * 8 + g] = there ? row / group : -(1 << 30);
+    }
   }
-  *before = base + x - v;
-  return all;
 }
 
-// A step of the line: where its keys are.
-struct Place {
-  int b, h, j0;                                // sequence, key head, first token (j0 < 0: no step)
-  int row0, n, start, len;                     // of the sequence
+template <int D_, bool MANY>
+struct Shape {
+  static constexpr int D = D_;
+  static constexpr int kCtas = D == 256 ? 1 : 2;                       // per SM
+  static constexpr int kGroups = MANY ? 2 : 3, kThreads = 32 * (4 * kGroups + 2);
+  static constexpr int kRows = MANY ? 128 : D == 256 ? 32 : 16;        // of a block
+  static constexpr int kChunk = kRows < 64 ? kRows : 64;               // of a product
+  static constexpr int kSlots = D == 64 ? 6 : D == 256 ? 3 : MANY ? 2 : 6, kHeads = 6;
+  // every group has slots of its own, so that a wait never mistakes a phase
+  static constexpr int kOwn = kSlots / kGroups, kOwnHeads = kHeads / kGroups;
+  static_assert(kSlots % kGroups == 0 && kHeads % kGroups == 0, "");
+  static constexpr int kSubs = D == 256 ? 2 : 1, kRowB = D == 64 ? 64 : 128;
+  static constexpr int kTileB = kTile * D, kHalf = kRows * 128, kQB = kRows * D * 2;
+  static constexpr int kSAt = kGroups * D / 2, kCols = 512 / kCtas;    // tensor memory columns
+  static_assert(kSAt + kGroups * kChunk <= kCols, "");
+  static constexpr int kQAt = kSlots * kTileB, kInfoAt = kQAt + 2 * kQB, kTokenAt = kInfoAt + 2 * kRows * 8;
+  // of a tile: its tokens' old weights, and for each page where its weights are and its factor
+  static constexpr int kHeadB = kTile * 4 + 96, kHeadAt = kTokenAt + 2 * kRows * 4;
+  static constexpr int kSmem = 1024 + kHeadAt + kHeads * kHeadB;
+  static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "");
 };
 
-template <int D, bool MANY>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) weights_kernel(const __grid_constant__ WeightsArgs a) {
-  constexpr int kJ = D / 64;                   // 16-code pieces of a key per lane
-  __shared__ long long s_sum[kWarps];
-  __shared__ int s_seq;
-  __shared__ long long s_first;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size, log_p = 31 - __clz(P);
-  uint32_t* err = reinterpret_cast<uint32_t*>(a.ws);
-  const int tiles = tiles_of(a.T, group);
-  const float2* info = reinterpret_cast<const float2*>(a.ws + kAlign);
-  const uint4* laid = reinterpret_cast<const uint4*>(a.ws + laid_at(heads, tiles));
+// Neighbouring tiles of one sequence and key head for one block of rows.
+struct Run {
+  int b, h, block, t0, t1;                     // sequence, key head, block of rows, tiles
+  int first;                                   // first tile with a key that some row sees
+  int row0, n, start, len;                     // of the sequence
+};
+// A CTA's piece of the line; every role walks it for itself.
+struct Walk {
+  long long pos, end, first;                   // first: of (b, h)
+  int b, h, block, blocks, t0, t1;
+  Seq q;
+};
+__device__ __forceinline__ bool next_run(Walk& w, Run& r, const WeightsArgs& a, int group, int block_rows) {
+  if (++w.block >= w.blocks) {
+    if (w.pos >= w.end) return false;
+    while (w.pos >= w.first + w.q.tiles) {
+      w.first += w.q.tiles;
+      if (++w.h < a.c.kv_heads) continue;
+      w.h = 0;
+      do w.q = read_seq(a, ++w.b, nullptr);
+      while (w.q.tiles == 0);                  // (the line goes on, so there is one more)
+    }
+    w.t0 = (int)(w.pos - w.first);
+    w.t1 = (int)min((long long)w.q.tiles, w.end - w.first);
+    w.pos = w.first + w.t1;
+    w.block = 0, w.blocks = (w.q.n * group + block_rows - 1) / block_rows;
+  }
+  r.b = w.b, r.h = w.h, r.block = w.block, r.t0 = w.t0, r.t1 = w.t1;
+  r.row0 = w.q.row0, r.n = w.q.n, r.start = w.q.start, r.len = w.q.len;
+  r.first = a.window > 0 ? max(w.q.start - a.window + 1, 0) / kTile : 0;
+  return true;
+}
 
-  // this CTA's piece of the line
+__device__ __forceinline__ float load_plain(const float* at) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at) : "memory");
+  return v;
+}
+
+template <int D, bool MANY>
+__global__ void __launch_bounds__(Shape<D, MANY>::kThreads, Shape<D, MANY>::kCtas)
+weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CUtensorMap kmap) {
+  using S = Shape<D, MANY>;
+  constexpr int kThreads = S::kThreads, G = S::kGroups;
+  extern __shared__ char smem_raw[];
+  __shared__ uint64_t s_kfull[S::kSlots], s_kempty[S::kSlots], s_afull[G], s_sfull[G], s_sempty[G];
+  __shared__ uint64_t s_qfull[2], s_qempty[2], s_hfull[S::kHeads], s_hempty[S::kHeads];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ long long s_sum[kThreads / 32], s_first;
+  __shared__ int s_seq;
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = a.c.kv_heads, group = a.q_heads / heads, P = a.c.page_size, log_p = 31 - __clz(P);
+  const long long groups = groups_of(a.T, group);
+  uint32_t* err = reinterpret_cast<uint32_t*>(a.ws);
+  volatile int* abort_flag = &s_abort;
+
+  // ---- this CTA's piece of the line ----
+  auto scan = [&](long long v, long long* before) {
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += up;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    long long base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += s_sum[w];
+      all += s_sum[w];
+    }
+    *before = base + x - v;
+    return all;
+  };
+  auto line_of = [&](int b, uint32_t* e) { return b < a.b.B ? (long long)read_seq(a, b, e).tiles * heads : 0; };
   long long total = 0, mine = 0, at = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
-    mine = 0;
-    if (b0 + tid < a.b.B)
-      mine = (long long)read_seq(a, b0 + tid, blockIdx.x == 0 ? err : nullptr).steps * heads;
-    total += block_scan(mine, s_sum, &at);
+    mine = line_of(b0 + tid, blockIdx.x == 0 ? err : nullptr);
+    total += scan(mine, &at);
   }
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kWarps) per = kWarps;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
   const long long begin = per * blockIdx.x, end = min(begin + per, total);
-  if (begin >= end) return;
+  if (begin >= end) {
+    pdl_wait();                                // what follows in the stream waits for the kernel before too
+    return;
+  }
   long long base = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
     long long sum = total;
     if (a.b.B > kThreads) {
-      mine = b0 + tid < a.b.B ? (long long)read_seq(a, b0 + tid, nullptr).steps * heads : 0;
-      sum = block_scan(mine, s_sum, &at);
+      mine = line_of(b0 + tid, nullptr);
+      sum = scan(mine, &at);
     }
     if (mine > 0 && base + at <= begin && begin < base + at + mine) s_seq = b0 + tid, s_first = base + at;
     base += sum;
   }
-  __syncthreads();
-
-  // the warp's steps: begin + warp, + kWarps, ...
-  int wb = s_seq;
-  Seq wq = read_seq(a, wb, nullptr);
-  int wh = (int)((begin - s_first) / wq.steps);
-  long long pos = begin + warp, first = s_first + (long long)wh * wq.steps;      // first: of (wb, wh)
-  auto next_place = [&] {
-    Place p;
-    p.j0 = -1, p.b = p.h = p.row0 = p.n = p.start = p.len = 0;
-    if (pos >= end) return p;
-    while (pos >= first + wq.steps) {
-      first += wq.steps;
-      if (++wh < heads) continue;
-      wh = 0;
-      do wq = read_seq(a, ++wb, nullptr);
-      while (wq.steps == 0);                   // (the line goes on, so there is one more)
-    }
-    p.b = wb, p.h = wh, p.j0 = (int)(pos - first) * kStep;
-    p.row0 = wq.row0, p.n = wq.n, p.start = wq.start, p.len = wq.len;
-    pos += kWarps;
-    return p;
-  };
-  // first token that a row of the sequence sees
-  auto lowest = [&](const Place& p) { return a.window > 0 ? max(0, p.start - a.window + 1) : 0; };
-  auto read_pages = [&](const Place& p, int (&page)[2]) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int j = p.j0 + 16 * x;
-      page[x] = (int)load_ahead(a.b.page_table + (int64_t)p.b * a.b.table_stride + (j >> log_p),
-                                p.j0 >= 0 && j < p.len, 0xffffffffu);
-    }
-  };
-  // the codes of a step, its pages' scales, and what its tokens had
-  struct Keys {
-    uint4 k[2][2][kJ];                         // half, key g or 8 + g, piece
-    float scale[2], old;
-  };
-  auto read_keys = [&](const Place& p, int (&page)[2], Keys& s) {
-    const bool products = p.j0 >= 0 && p.j0 + kStep > lowest(p);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const bool in = p.j0 >= 0 && p.j0 + 16 * x < p.len;
-      bool good = in && page[x] >= 0 && page[x] < a.c.num_pages;
-      if (in && !good) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
-      if (!good) page[x] = -1;
-      const int slot = (p.j0 + 16 * x) & (P - 1);
-      const uint8_t* at_ = a.c.k_codes + (int64_t)page[x] * a.c.page_stride + ((int64_t)p.h * P + slot) * D + 16 * c;
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j)
-          s.k[x][r][j] = load_ahead(at_ + (g + 8 * r) * D + 64 * j, good && products);
-      s.scale[x] = __uint_as_float(load_ahead(a.c.k_scales + (int64_t)page[x] * heads + p.h, good, 0u));
-    }
-    // lane l: token j0 + l
-    const int j = p.j0 + lane;
-    const int pg = lane < 16 ? page[0] : page[1];
-    const bool had = p.j0 >= 0 && j < p.start && pg >= 0 && a.decay != 0.0f;
-    s.old = __uint_as_float(load_ahead(a.w + ((int64_t)pg * heads + p.h) * P + (j & (P - 1)), had, 0u));
-  };
-
-  // Two steps are in hand, one being worked on and one whose codes are on their way, in turn: a step's
-  // registers are never copied while loads into them are out. Pages are read another step ahead.
-  Place place[2];
-  int page[2][2];
-  Keys keys[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    place[i] = next_place();
-    read_pages(place[i], page[i]);
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) mbar_init(&s_kfull[i], 1), mbar_init(&s_kempty[i], 4);
+    for (int i = 0; i < G; ++i) mbar_init(&s_afull[i], 4), mbar_init(&s_sfull[i], 1), mbar_init(&s_sempty[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_qfull[i], 1), mbar_init(&s_qempty[i], 4 * G);
+    for (int i = 0; i < S::kHeads; ++i) mbar_init(&s_hfull[i], 1), mbar_init(&s_hempty[i], 4);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
   }
-  read_keys(place[0], page[0], keys[0]);
-  if (MANY) pdl_wait();                        // the rows, laid out by the kernel before
-  Tile<D> rows;
-  float less[2] = {0, 0}, rowf2[2] = {0, 0};
-  int have_b = -1, have_h = -1;
+  if (warp == 4 * G) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(&s_tmem)), "n"(S::kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  Walk w;
+  w.pos = begin, w.end = end, w.b = s_seq;
+  w.q = read_seq(a, w.b, nullptr);
+  w.h = (int)((begin - s_first) / w.q.tiles);
+  w.first = s_first + (long long)w.h * w.q.tiles;
+  w.block = w.blocks = w.t0 = w.t1 = 0;
+  Run run;
+  auto next = [&] { return next_run(w, run, a, group, S::kRows); };
+  auto rows_of = [&] { return min(S::kRows, run.n * group - run.block * S::kRows); };
+  bool ok = true;
 
-  auto take = [&](Place& here, int (&pg2)[2], Keys& k, Place& ahead, int (&pg2_ahead)[2], Keys& k_ahead) {
-    const Place later = next_place();
-    int page_later[2];
-    read_pages(later, page_later);
-    read_keys(ahead, pg2_ahead, k_ahead);
-
-    float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};        // of keys g and 8 + g of either half
-    const int j0 = here.j0, row_lo = here.row0 * group, row_hi = (here.row0 + here.n) * group;
-    const float f0 = a.scale * kLog2e;
-    // keys of the step that some row does not see
-    const bool masked = j0 + kStep > here.start + 1 || j0 + kStep > here.len ||
-                        (a.window > 0 && j0 <= here.start + here.n - 1 - a.window);
-    const float fs[2] = {f0 * k.scale[0], f0 * k.scale[1]};
-    // adds the weights of 8 rows; rf and ls of the lane's rows 2c and 2c + 1
-    auto add_tile = [&](const Tile<D>& t, int row0, const float (&rf)[2], const float (&ls)[2]) {
-      float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (warp < 4 * G) {
+    // ---------------- tiles: group `gr`'s, thread = key ----------------
+    const int gr = warp / 4, key = tid & 127, in_page = key & (P - 1);
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16, swz = D == 64 ? (key >> 1) & 3 : key & 7;
+    const uint32_t a_col = tmem + gr * (D / 2), s_col = tmem + S::kSAt + gr * S::kChunk;
+    const uint64_t q_desc = smem_desc(smem_u32(smem + S::kQAt), 16, 1024, 2);
+    const bool issues = (warp & 3) == 0 && lane == 0;
+    constexpr int kPer = S::kRowB / 16;        // 16-byte pieces of a sub-tile's row
+    uint32_t k = 0, sph = 0, eph = 0, blocks = 0;                      // tiles; phases; blocks of rows
+    while (ok && next()) {
+      const int rows = rows_of(), cols = (rows + 7) / 8 * 8, qb = blocks & 1;
+      // tiles that no row sees: the old weights fade
+      for (int t = run.t0 + gr; t < min(run.first, run.t1) && run.block == 0; t += G) {
+        const int j = t * kTile + key;
+        if (j >= run.len) continue;
+        const int page = a.b.page_table[(int64_t)run.b * a.b.table_stride + (j >> log_p)];
+        if (page < 0 || page >= a.c.num_pages) {
+          atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+          continue;
+        }
+        const int64_t at_ = ((int64_t)page * heads + run.h) * P + in_page;
+        a.w_out[at_] = a.decay == 0.0f ? 0.0f : load_plain(a.w + at_) * a.decay;
+      }
+      const int first = max(run.t0, run.first);
+      if (first >= run.t1) continue;           // the block's rows meet no tile
+      if (!(ok = wait_warp(&s_qfull[qb], blocks >> 1 & 1, abort_flag, err))) break;
+      const float4* info = reinterpret_cast<const float4*>(smem + S::kInfoAt + qb * S::kRows * 8);
+      const int* tokens = reinterpret_cast<const int*>(smem + S::kTokenAt + qb * S::kRows * 4);
+      auto products = [&](int c0) {            // S of the rows from c0 on
+        const uint32_t id = f16_idesc(128, min(S::kChunk, (rows - c0 + 15) / 16 * 16), false);
+        const uint64_t qd = q_desc + (uint32_t)((qb * S::kQB + c0 * 128) >> 4);
+        tc_fence_after();
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
+        for (int i = 0; i < D / 16; ++i)
+          mma_ts(s_col, a_col + i * 8, qd + (uint32_t)(((i >> 2) * S::kHalf + (i & 3) * 32) >> 4), id, i != 0);
+        tc_commit(&s_sfull[gr]);
+      };
+      // tiles from `part` on and before `edge` have keys that some row does not see
+      const int part = max(min(run.start + 1, run.len), 0) / kTile;
+      const int edge = a.window > 0 ? max(run.start + run.n - 1 - a.window + kTile, 0) / kTile : 0;
+      // a tile is the same group's for every block of rows: its threads add to what they left
+      for (int t = first + gr; t < run.t1; t += G, ++k) {
+        const int slot = gr + G * (k % S::kOwn), hb = gr + G * (k % S::kOwnHeads);
+        if (!(ok = wait_warp(&s_kfull[slot], k / S::kOwn & 1, abort_flag, err))) break;
+        const uint32_t row = smem_u32(smem + slot * S::kTileB) + (uint32_t)key * S::kRowB;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t b0 = word_of(t.v[2 * j + (m >> 1)], 2 * (m & 1)), b1 = word_of(t.v[2 * j + (m >> 1)], 2 * (m & 1) + 1);
+        for (int i = 0; i < D / 16; i += 2) {  // 32 codes at a time
+          uint32_t v[16];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            uint32_t a0, a1, a2, a3;
-            widen4(word_of(k.k[x][0][j], m), a0, a2);
-            widen4(word_of(k.k[x][1][j], m), a1, a3);
-            mma(s[x], a0, a1, a2, a3, b0, b1);
+            const int piece = i + x;
+            const uint4 c = lds128(row + (piece / kPer) * (kTile * 128) + (((piece % kPer) ^ swz) * 16));
+            widen4(c.x, v[8 * x], v[8 * x + 1]);
+            widen4(c.y, v[8 * x + 2], v[8 * x + 3]);
+            widen4(c.z, v[8 * x + 4], v[8 * x + 5]);
+            widen4(c.w, v[8 * x + 6], v[8 * x + 7]);
           }
+          tc_st16(a_col + quarter + i * 8, v);
         }
+        warp_arrive(&s_kempty[slot]);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&s_afull[gr]);
+        if (issues && wait_thread(&s_afull[gr], k & 1, abort_flag, err)) products(0);
+        __syncwarp();
+        // (meanwhile) the token's old weight, where its new one goes, and its page's factor
+        if (!(ok = wait_warp(&s_hfull[hb], k / S::kOwnHeads & 1, abort_flag, err))) break;
+        const char* head = smem + S::kHeadAt + hb * S::kHeadB;
+        const int j = t * kTile + key;
+        float old = reinterpret_cast<const float*>(head)[key];
+        const long long at_ = reinterpret_cast<const long long*>(head + kTile * 4)[key >> log_p];
+        const float f = reinterpret_cast<const float*>(head + kTile * 4 + 64)[key >> log_p];
+        warp_arrive(&s_hempty[hb]);
+        if (j >= run.start || run.block != 0 || a.decay == 0.0f) old = 0.0f;
+        float* to = a.w_out + at_ + in_page;
+        const bool mine = j < run.len && at_ >= 0;
+        const uint64_t ff = pair(f, f);
+        uint64_t acc[2] = {0, 0};
+        // the weights of eight rows
+        auto add8 = [&](const float* v, int r, auto hides) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int y = i & 1;
-          float w = exp2_approx(fmaf(s[x][i], fs[x] * rf[y], -ls[y]));
-          if (masked) {
-            const int row = row0 + 2 * c + y, j = j0 + 16 * x + 8 * (i >> 1) + g;
-            const int at_ = here.start + row / group - here.row0;
-            const bool see = row >= row_lo && row < row_hi && j <= at_ && j < here.len &&
-                             (a.window == 0 || j > at_ - a.window);
-            w = see ? w : 0.0f;
-          }
-          sum[x][i >> 1] += w;
-        }
-    };
-    if (j0 + kStep > lowest(here)) {
-      if (MANY) {
-        const long long base_ = (long long)here.h * tiles;
-        for (int tile = row_lo / 8; tile * 8 < row_hi; ++tile) {
-          Tile<D> t;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) t.v[i] = laid[((base_ + tile) * (D / 32) + i) * 32 + lane];
-          const float4 f = *reinterpret_cast<const float4*>(info + (base_ + tile) * 8 + 2 * c);
-          // rows of the tile that are another sequence's add nothing
-          const int r = tile * 8 + 2 * c;
-          const float rf[2] = {f.x, f.z};
-          const float ls[2] = {r >= row_lo && r < row_hi ? f.y : INFINITY,
-                               r + 1 >= row_lo && r + 1 < row_hi ? f.w : INFINITY};
-          add_tile(t, tile * 8, rf, ls);
-        }
-      } else {
-        for (int row0 = row_lo; row0 < row_hi; row0 += 8) {
-          if (have_b != here.b || have_h != here.h || row_hi - row_lo > 8) {
-            float rowf;
-            read_tile<D>(rows, &rowf, a, group, here.h, row0, row_hi, lane);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int row = row0 + 2 * c + y;
-              rowf2[y] = __shfl_sync(0xffffffffu, rowf, 4 * (2 * c + y));
-              less[y] = row < row_hi
-                            ? less_of(a.lse[(int64_t)(row / group) * a.q_heads + here.h * group + row % group])
-                            : INFINITY;
+          for (int x = 0; x < 8; x += 2) {
+            const float4 q = info[(r + x) / 2];
+            float e0, e1;
+            unpair(fma2(pair(v[x], v[x + 1]), mul2(pair(q.x, q.y), ff), pair(q.z, q.w)), e0, e1);
+            e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+            if (decltype(hides)::value) {
+              const int2 i = *reinterpret_cast<const int2*>(tokens + r + x);
+              // the tokens that see key j
+              const int from = max(j - run.start, 0), upto = a.window > 0 ? j - run.start + a.window : 0x7fffffff;
+              e0 = i.x >= from && i.x < upto ? e0 : 0.0f;
+              e1 = i.y >= from && i.y < upto ? e1 : 0.0f;
             }
-            have_b = here.b, have_h = here.h;
+            acc[x >> 1 & 1] = add2(acc[x >> 1 & 1], pair(e0, e1));
           }
-          add_tile(rows, row0, rowf2, less);
+        };
+        for (int c0 = 0; c0 < rows; c0 += S::kChunk) {
+          if (c0 > 0) {                        // the rows' next chunk over the one that all have read
+            tc_fence_before();
+            warp_arrive(&s_sempty[gr]);
+            if (issues && wait_thread(&s_sempty[gr], eph & 1, abort_flag, err)) products(c0);
+            ++eph;
+            __syncwarp();
+          }
+          if (!(ok = wait_warp(&s_sfull[gr], sph & 1, abort_flag, err))) break;
+          ++sph;
+          tc_fence_after();
+          const int n = min(S::kChunk, cols - c0);
+          auto add_all = [&](auto hides) {
+            int c = 0;
+            if (S::kChunk >= 32) {
+#pragma unroll 1
+              for (; c + 32 <= n; c += 32) {
+                float v[32];
+                tmem_ld32(s_col + quarter + c, v);
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) add8(v + x, c0 + c + x, hides);
+              }
+            }
+#pragma unroll 1
+            for (; c < n; c += 16) {
+              float v[16];
+              tmem_ld16(s_col + quarter + c, v);
+              add8(v, c0 + c, hides);
+              if (c + 8 < n) add8(v + 8, c0 + c + 8, hides);         // the last group of rows may stand alone
+            }
+          };
+          if (t >= part || t < edge) add_all(std::true_type{});
+          else add_all(std::false_type{});
         }
+        if (!ok) break;
+        tc_fence_before();
+        float x0, x1;
+        unpair(add2(acc[0], acc[1]), x0, x1);
+        if (mine) *to = run.block == 0 ? fmaf(old, a.decay, x0 + x1) : load_plain(to) + (x0 + x1);   // (its own of a block before)
+      }
+      if (!ok) break;
+      warp_arrive(&s_qempty[qb]);
+      ++blocks;
+    }
+    // gave up: a product that was issued is done before the tensor memory is given back (bounded)
+    if (!ok && issues) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try(&s_sfull[gr], sph & 1) && global_ns() - t0 < 100000000ull) {
       }
     }
-    // over the rows: columns 2c, 2c + 1 are added already; then lane l takes token j0 + l
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        sum[x][r] += __shfl_xor_sync(0xffffffffu, sum[x][r], 1);
-        sum[x][r] += __shfl_xor_sync(0xffffffffu, sum[x][r], 2);
+  } else if (warp == 4 * G) {
+    // ---------------- tiles of codes, and what goes with them ----------------
+    // Pages and scales come for as many tiles of a run at once as lanes allow, those of the next such
+    // batch (or run) asked for while this one is brought.
+    const int in_tile = kTile >> log_p, log_t = 7 - log_p, batch = 32 >> log_t, which = lane >> log_t;
+    const int slot_page = lane & (in_tile - 1);
+    Walk look = w;
+    Run lr = {};
+    int lt = 0;                                // next tile of lr
+    auto ask_pages = [&] {
+      while (lt >= lr.t1) {
+        if (!next_run(look, lr, a, group, S::kRows)) return -2;
+        lt = max(lr.t0, lr.first);
       }
-    const int from = 4 * (lane & 7);
-    const float w00 = __shfl_sync(0xffffffffu, sum[0][0], from), w01 = __shfl_sync(0xffffffffu, sum[0][1], from);
-    const float w10 = __shfl_sync(0xffffffffu, sum[1][0], from), w11 = __shfl_sync(0xffffffffu, sum[1][1], from);
-    const float w = lane & 16 ? (lane & 8 ? w11 : w10) : (lane & 8 ? w01 : w00);
-    const int j = j0 + lane, pg = lane < 16 ? pg2[0] : pg2[1];
-    if (j < here.len && pg >= 0)
-      a.w_out[((int64_t)pg * heads + here.h) * P + (j & (P - 1))] = fmaf(k.old, a.decay, w);
-    here = later;
-    pg2[0] = page_later[0], pg2[1] = page_later[1];
-  };
-  while (true) {
-    if (place[0].j0 < 0) break;
-    take(place[0], page[0], keys[0], place[1], page[1], keys[1]);
-    if (place[1].j0 < 0) break;
-    take(place[1], page[1], keys[1], place[0], page[0], keys[0]);
+      const int t = lt + which, j = t * kTile + slot_page * P;
+      const bool in = which < batch && t < lr.t1 && j < lr.len;
+      int page = (int)load_ahead(a.b.page_table + (int64_t)lr.b * a.b.table_stride + (j >> log_p), in, 0xffffffffu);
+      lt += batch;
+      return in ? page : -2;                   // (-2: no such page is asked for)
+    };
+    auto ask_scale = [&](int page, int h) {
+      const bool good = page >= 0 && page < a.c.num_pages;
+      return __uint_as_float(load_ahead(a.c.k_scales + (int64_t)page * heads + h, good, 0u));
+    };
+    int page = ask_pages(), h_next = lr.h;
+    float scale = ask_scale(page, h_next), scale_next = 0.0f;
+    int page_next = ask_pages();
+    h_next = lr.h;
+    uint32_t count[G] = {};                    // tiles of each group
+    bool begun = false;
+    while (ok && next()) {
+      const int first = max(run.t0, run.first);
+      for (int t = first, gr = 0; t < run.t1; ++t, gr = gr + 1 == G ? 0 : gr + 1) {
+        uint32_t k = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          if (i == gr) k = count[i]++;
+        const int in_batch = (t - first) & (batch - 1);
+        if (in_batch == 0 && begun) {
+          page = page_next, scale = scale_next;
+          page_next = ask_pages();
+          h_next = lr.h;
+        }
+        begun = true;
+        const bool mine = which == in_batch, good = mine && page >= 0 && page < a.c.num_pages;
+        if (mine && !good && page != -2) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+        const uint32_t there = __popc(__ballot_sync(0xffffffffu, good));
+        const int slot = gr + G * (k % S::kOwn), hb = gr + G * (k % S::kOwnHeads);
+        if (!(ok = wait_warp(&s_kempty[slot], (k / S::kOwn & 1) ^ 1, abort_flag, err))) break;
+        if (lane == 0) mbar_expect_tx(&s_kfull[slot], there * P * D);
+        __syncwarp();
+        if (good) {
+          char* to = smem + slot * S::kTileB + slot_page * P * S::kRowB;
+#pragma unroll
+          for (int i = 0; i < S::kSubs; ++i)
+            tma_load_3d(to + i * (kTile * 128), &kmap, i * 128, run.h * P, page, &s_kfull[slot]);
+        }
+        if (in_batch == min(1, min(batch, run.t1 - (t - in_batch)) - 1)) scale_next = ask_scale(page_next, h_next);
+        // old weights, where the new ones go, and the pages' factors
+        if (!(ok = wait_warp(&s_hempty[hb], (k / S::kOwnHeads & 1) ^ 1, abort_flag, err))) break;
+        char* head = smem + S::kHeadAt + hb * S::kHeadB;
+        const int64_t at_ = ((int64_t)page * heads + run.h) * P;
+        if (mine) {
+          reinterpret_cast<long long*>(head + kTile * 4)[slot_page] = good ? at_ : -1;
+          reinterpret_cast<float*>(head + kTile * 4 + 64)[slot_page] = good ? a.scale * kLog2e * scale : 0.0f;
+        }
+        const bool had = good && run.block == 0 && a.decay != 0.0f && t * kTile + slot_page * P < run.start;
+        const uint32_t olds = __popc(__ballot_sync(0xffffffffu, had));
+        if (lane == 0) mbar_expect_tx(&s_hfull[hb], olds * P * 4);
+        __syncwarp();
+        if (had) bulk_load(head + slot_page * P * 4, a.w + at_, P * 4, &s_hfull[hb]);
+      }
+    }
+    if (!ok) {                                 // gave up: let the copies in flight land (bounded)
+      const uint64_t t0 = global_ns();
+#pragma unroll
+      for (int g = 0; g < G; ++g) {            // (a wait for a phase that is no longer the slot's ends at once or with the limit)
+        for (uint32_t i = count[g] > S::kOwn ? count[g] - S::kOwn : 0; i < count[g]; ++i)
+          while (!mbar_try(&s_kfull[g + G * (i % S::kOwn)], i / S::kOwn & 1) && global_ns() - t0 < 100000000ull) {
+          }
+        for (uint32_t i = count[g] > S::kOwnHeads ? count[g] - S::kOwnHeads : 0; i < count[g]; ++i)
+          while (!mbar_try(&s_hfull[g + G * (i % S::kOwnHeads)], i / S::kOwnHeads & 1) && global_ns() - t0 < 100000000ull) {
+          }
+      }
+    }
+  } else {
+    // ---------------- blocks of rows ----------------
+    if (lane == 0) {
+      pdl_wait();                              // laid out by the kernel before
+      uint32_t k = 0;
+      const char* q = a.ws + rows_at(heads, groups);
+      while (ok && next()) {
+        if (run.first >= run.t1) continue;
+        const int qb = k & 1, n8 = (rows_of() + 7) / 8;
+        const int64_t g0 = first_group(run.row0, group) + run.block * (S::kRows / 8);
+        if (!(ok = wait_thread(&s_qempty[qb], (k >> 1 & 1) ^ 1, abort_flag, err))) break;
+        mbar_expect_tx(&s_qfull[qb], (uint32_t)n8 * (64 + 32 + 16 * D));
+        bulk_load(smem + S::kInfoAt + qb * S::kRows * 8, a.ws + kAlign + ((int64_t)run.h * groups + g0) * 64, n8 * 64, &s_qfull[qb]);
+        bulk_load(smem + S::kTokenAt + qb * S::kRows * 4, a.ws + tokens_at(heads, groups) + g0 * 32, n8 * 32, &s_qfull[qb]);
+        for (int i = 0; i < D / 64; ++i)
+          bulk_load(smem + S::kQAt + qb * S::kQB + i * S::kHalf, q + (((int64_t)run.h * (D / 64) + i) * groups + g0) * 1024,
+                    n8 * 1024, &s_qfull[qb]);
+        ++k;
+      }
+      if (!ok) {
+        const uint64_t t0 = global_ns();
+        for (uint32_t i = k > 2 ? k - 2 : 0; i < k; ++i)
+          while (!mbar_try(&s_qfull[i & 1], i >> 1 & 1) && global_ns() - t0 < 100000000ull) {
+          }
+      }
+    }
   }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4 * G)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kCols));
+}
+
+template <int D, bool MANY>
+cudaError_t launch_main(const WeightsArgs& a, cudaStream_t s) {
+  using S = Shape<D, MANY>;
+  CUtensorMap map;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.c.kv_heads * a.c.page_size, (uint64_t)a.c.num_pages};
+  const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.c.page_stride};
+  const uint32_t box[3] = {(uint32_t)S::kRowB, (uint32_t)a.c.page_size, 1};
+  if (!make_map3(&map, a.c.k_codes, dims, strides, box, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto kern = weights_kernel<D, MANY>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(S::kCtas * num_sms()), dim3(S::kThreads), S::kSmem, s, a, map);
 }
 
 template <int D>
 cudaError_t launch_dim(const WeightsArgs& a, cudaStream_t s) {
   const int heads = a.c.kv_heads, group = a.q_heads / heads;
-  const int grid = num_sms() * (D == 64 ? 2 : 1);
-  // Sequences of one row tile each, as far as the sizes tell (a longer one among them is read with its
-  // tiles made again for every step)
-  if (a.T <= a.b.B && group <= 8) {
-    weights_kernel<D, false><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
-  }
-  const long long warps = (long long)heads * tiles_of(a.T, group);
-  prepare_kernel<D><<<(unsigned)((warps + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
+  // prepare: blocks per sequence, as if all had the same number of rows
+  const long long warps = (long long)heads * ((((long long)a.T * group + a.b.B - 1) / a.b.B + 7) / 8);
+  const long long y = (warps + kPrepWarps - 1) / kPrepWarps, most = (4 * num_sms() + a.b.B - 1) / a.b.B;
+  prepare_kernel<D><<<dim3((unsigned)a.b.B, (unsigned)(y < most ? y : most)), 32 * kPrepWarps, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(weights_kernel<D, true>, dim3(grid), dim3(kThreads), 0, s, a);
+  // Few rows per sequence, as far as the sizes tell: a deeper ring instead of room for rows.
+  if constexpr (D <= 128) {
+    if ((long long)a.T * group > 16LL * a.b.B) return launch_main<D, true>(a, s);
+  }
+  return launch_main<D, false>(a, s);
 }
 
 }  // namespace
 
 size_t kv_weights_ws_bytes(int T, int q_heads, int kv_heads, int head_dim) {
-  const int tiles = tiles_of(T, q_heads / kv_heads);
-  return align_up(laid_at(kv_heads, tiles) + (size_t)kv_heads * tiles * head_dim * 16);
+  const long long groups = groups_of(T, q_heads / kv_heads);
+  return align_up(rows_at(kv_heads, groups) + (size_t)kv_heads * groups * head_dim * 16);
 }
 
 cudaError_t launch_kv_weights(const WeightsArgs& a, cudaStream_t s) {

@@ -219,7 +219,7 @@ moe_status moe_kv_weights_e4m3(const void* q, int64_t q_stride, int32_t T, int32
   if (q_heads <= 0 || q_heads % cache->kv_heads != 0) return MOE_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || scale > 1e30f || !(decay >= 0.0f && decay <= 1.0f)) return MOE_ERR_INVALID_ARG;
   if ((st = check_rows(q, q_stride, (int64_t)q_heads * cache->head_dim)) != MOE_OK) return st;
-  if (!lse || !w || !w_out || !aligned(lse, 4) || !aligned(w, 4) || !aligned(w_out, 4)) return MOE_ERR_INVALID_ARG;
+  if (!lse || !w || !w_out || !aligned(lse, 4) || !aligned(w, 16) || !aligned(w_out, 16)) return MOE_ERR_INVALID_ARG;
   if (T >= (1 << 24) || (int64_t)T * q_heads >= (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, kv_weights_ws_bytes(T, q_heads, cache->kv_heads, cache->head_dim))) != MOE_OK)

@@ -171,7 +171,7 @@ def test_keep_refusals(lib, kw, status):
     (dict(T=0), 1), (dict(dt=2), 1), (dict(q=None), 1), (dict(q=264), 1), (dict(qs=1020), 1), (dict(qh=7), 1),
     (dict(lse=None), 1), (dict(lse=258), 1), (dict(scale=-1.0), 1), (dict(scale=math.inf), 1), (dict(window=-1), 1),
     (dict(decay=-0.1), 1), (dict(decay=1.5), 1), (dict(decay=math.nan), 1), (dict(w=None), 1), (dict(out=None), 1),
-    (dict(w=258), 1), (dict(T=1 << 24), 2), (dict(ws=None), 3), (dict(nb=0), 3)])
+    (dict(w=264), 1), (dict(out=260), 1), (dict(T=1 << 24), 2), (dict(ws=None), 3), (dict(nb=0), 3)])
 def test_weights_refusals(lib, kw, status):
     assert _weights(lib, **kw) == status
 
