@@ -7,9 +7,8 @@
 // tiles of 128 tokens, which form one line; the grid cuts it into equal pieces. prepare_kernel lays the
 // rows out once, as f16 times a power of two (as the attention does) in the swizzled order of the
 // products' operand; the main kernel starts beside it. In a CTA one warp brings tiles of codes into a
-// ring (TMA, a box per page) and their tokens' old weights, pages and scales into another, one brings
-// blocks of rows and their factors, the next block ahead, and groups of four warps take the tiles in
-// turn, thread = key:
+// ring (TMA, a box per page), one brings their tokens' old weights and factors into another, and blocks
+// of rows before the tiles that need them, and groups of four warps take the tiles in turn, thread = key:
 //   the key's codes to f16 (exact) in tensor memory; S = K Q^T with the keys from there as the 128-row
 //   operand (tcgen05, f32; one thread issues); the key's row of S, weights, their sum, and the token's
 //   new weight
@@ -24,6 +23,9 @@ namespace {
 
 constexpr int kTile = 128;                     // keys
 constexpr int kPrepWarps = 8;
+// What a (sequence, key head) costs beside its tiles (its rows, the chain of its first tile), in tiles:
+// pieces of the line are equal with it counted.
+constexpr int kSegmentCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Rows are kept in groups of 8 that begin anew with every sequence: sequence b's first group is
@@ -142,30 +144,37 @@ struct Shape {
 // Neighbouring tiles of one sequence and key head for one block of rows.
 struct Run {
   int b, h, block, t0, t1;                     // sequence, key head, block of rows, tiles
+  int turn;                                    // the group that takes the first of them
   int first;                                   // first tile with a key that some row sees
   int row0, n, start, len;                     // of the sequence
 };
 // A CTA's piece of the line; every role walks it for itself.
 struct Walk {
   long long pos, end, first;                   // first: of (b, h)
-  int b, h, block, blocks, t0, t1;
+  int b, h, block, blocks, t0, t1, turn;
   Seq q;
 };
-__device__ __forceinline__ bool next_run(Walk& w, Run& r, const WeightsArgs& a, int group, int block_rows) {
+__device__ __forceinline__ long long length_of(const Seq& q) { return q.tiles ? q.tiles + kSegmentCost : 0; }
+__device__ __forceinline__ bool next_run(Walk& w, Run& r, const WeightsArgs& a, int group, int block_rows, int groups) {
   if (++w.block >= w.blocks) {
-    if (w.pos >= w.end) return false;
-    while (w.pos >= w.first + w.q.tiles) {
-      w.first += w.q.tiles;
-      if (++w.h < a.c.kv_heads) continue;
-      w.h = 0;
-      do w.q = read_seq(a, ++w.b, nullptr);
-      while (w.q.tiles == 0);                  // (the line goes on, so there is one more)
-    }
-    w.t0 = (int)(w.pos - w.first);
-    w.t1 = (int)min((long long)w.q.tiles, w.end - w.first);
-    w.pos = w.first + w.t1;
+    w.turn = (w.turn + max(w.t1 - w.t0, 0)) % groups;      // the groups go on taking tiles in turn
+    do {
+      if (w.pos >= w.end) return false;
+      while (w.pos >= w.first + length_of(w.q)) {
+        w.first += length_of(w.q);
+        if (++w.h < a.c.kv_heads) continue;
+        w.h = 0;
+        do w.q = read_seq(a, ++w.b, nullptr);
+        while (w.q.tiles == 0);                // (the line goes on, so there is one more)
+      }
+      const long long upto = min(length_of(w.q), w.end - w.first);
+      w.t0 = max((int)(w.pos - w.first) - kSegmentCost, 0);
+      w.t1 = (int)upto - kSegmentCost;
+      w.pos = w.first + upto;
+    } while (w.t1 <= w.t0);                    // (only the fixed cost fell to this CTA)
     w.block = 0, w.blocks = (w.q.n * group + block_rows - 1) / block_rows;
   }
+  r.turn = w.turn;
   r.b = w.b, r.h = w.h, r.block = w.block, r.t0 = w.t0, r.t1 = w.t1;
   r.row0 = w.q.row0, r.n = w.q.n, r.start = w.q.start, r.len = w.q.len;
   r.first = a.window > 0 ? max(w.q.start - a.window + 1, 0) / kTile : 0;
@@ -217,7 +226,7 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
     *before = base + x - v;
     return all;
   };
-  auto line_of = [&](int b, uint32_t* e) { return b < a.b.B ? (long long)read_seq(a, b, e).tiles * heads : 0; };
+  auto line_of = [&](int b, uint32_t* e) { return b < a.b.B ? length_of(read_seq(a, b, e)) * heads : 0; };
   long long total = 0, mine = 0, at = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
     mine = line_of(b0 + tid, blockIdx.x == 0 ? err : nullptr);
@@ -260,11 +269,11 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
   Walk w;
   w.pos = begin, w.end = end, w.b = s_seq;
   w.q = read_seq(a, w.b, nullptr);
-  w.h = (int)((begin - s_first) / w.q.tiles);
-  w.first = s_first + (long long)w.h * w.q.tiles;
-  w.block = w.blocks = w.t0 = w.t1 = 0;
+  w.h = (int)((begin - s_first) / length_of(w.q));
+  w.first = s_first + w.h * length_of(w.q);
+  w.block = w.blocks = w.t0 = w.t1 = w.turn = 0;
   Run run;
-  auto next = [&] { return next_run(w, run, a, group, S::kRows); };
+  auto next = [&] { return next_run(w, run, a, group, S::kRows, G); };
   auto rows_of = [&] { return min(S::kRows, run.n * group - run.block * S::kRows); };
   bool ok = true;
 
@@ -309,7 +318,7 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
       const int part = max(min(run.start + 1, run.len), 0) / kTile;
       const int edge = a.window > 0 ? max(run.start + run.n - 1 - a.window + kTile, 0) / kTile : 0;
       // a tile is the same group's for every block of rows: its threads add to what they left
-      for (int t = first + gr; t < run.t1; t += G, ++k) {
+      for (int t = first + (gr + G - run.turn) % G; t < run.t1; t += G, ++k) {
         const int slot = gr + G * (k % S::kOwn), hb = gr + G * (k % S::kOwnHeads);
         if (!(ok = wait_warp(&s_kfull[slot], k / S::kOwn & 1, abort_flag, err))) break;
         const uint32_t row = smem_u32(smem + slot * S::kTileB) + (uint32_t)key * S::kRowB;
@@ -414,10 +423,9 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
       while (!mbar_try(&s_sfull[gr], sph & 1) && global_ns() - t0 < 100000000ull) {
       }
     }
-  } else if (warp == 4 * G) {
-    // ---------------- tiles of codes, and what goes with them ----------------
-    // Pages and scales come for as many tiles of a run at once as lanes allow, those of the next such
-    // batch (or run) asked for while this one is brought.
+  } else {
+    // Pages come for as many tiles of a run at once as lanes allow, those of the next such batch (or run)
+    // asked for while this one's tiles are brought.
     const int in_tile = kTile >> log_p, log_t = 7 - log_p, batch = 32 >> log_t, which = lane >> log_t;
     const int slot_page = lane & (in_tile - 1);
     Walk look = w;
@@ -425,103 +433,120 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
     int lt = 0;                                // next tile of lr
     auto ask_pages = [&] {
       while (lt >= lr.t1) {
-        if (!next_run(look, lr, a, group, S::kRows)) return -2;
+        if (!next_run(look, lr, a, group, S::kRows, G)) return -2;
         lt = max(lr.t0, lr.first);
       }
       const int t = lt + which, j = t * kTile + slot_page * P;
       const bool in = which < batch && t < lr.t1 && j < lr.len;
-      int page = (int)load_ahead(a.b.page_table + (int64_t)lr.b * a.b.table_stride + (j >> log_p), in, 0xffffffffu);
+      const int page = (int)load_ahead(a.b.page_table + (int64_t)lr.b * a.b.table_stride + (j >> log_p), in, 0xffffffffu);
       lt += batch;
       return in ? page : -2;                   // (-2: no such page is asked for)
     };
-    auto ask_scale = [&](int page, int h) {
-      const bool good = page >= 0 && page < a.c.num_pages;
-      return __uint_as_float(load_ahead(a.c.k_scales + (int64_t)page * heads + h, good, 0u));
-    };
-    int page = ask_pages(), h_next = lr.h;
-    float scale = ask_scale(page, h_next), scale_next = 0.0f;
-    int page_next = ask_pages();
-    h_next = lr.h;
+    auto known = [&](int page) { return page >= 0 && page < a.c.num_pages; };
     uint32_t count[G] = {};                    // tiles of each group
-    bool begun = false;
-    while (ok && next()) {
-      const int first = max(run.t0, run.first);
-      for (int t = first, gr = 0; t < run.t1; ++t, gr = gr + 1 == G ? 0 : gr + 1) {
-        uint32_t k = 0;
-#pragma unroll
-        for (int i = 0; i < G; ++i)
-          if (i == gr) k = count[i]++;
-        const int in_batch = (t - first) & (batch - 1);
-        if (in_batch == 0 && begun) {
-          page = page_next, scale = scale_next;
-          page_next = ask_pages();
-          h_next = lr.h;
-        }
-        begun = true;
-        const bool mine = which == in_batch, good = mine && page >= 0 && page < a.c.num_pages;
-        if (mine && !good && page != -2) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
-        const uint32_t there = __popc(__ballot_sync(0xffffffffu, good));
-        const int slot = gr + G * (k % S::kOwn), hb = gr + G * (k % S::kOwnHeads);
-        if (!(ok = wait_warp(&s_kempty[slot], (k / S::kOwn & 1) ^ 1, abort_flag, err))) break;
-        if (lane == 0) mbar_expect_tx(&s_kfull[slot], there * P * D);
-        __syncwarp();
-        if (good) {
-          char* to = smem + slot * S::kTileB + slot_page * P * S::kRowB;
-#pragma unroll
-          for (int i = 0; i < S::kSubs; ++i)
-            tma_load_3d(to + i * (kTile * 128), &kmap, i * 128, run.h * P, page, &s_kfull[slot]);
-        }
-        if (in_batch == min(1, min(batch, run.t1 - (t - in_batch)) - 1)) scale_next = ask_scale(page_next, h_next);
-        // old weights, where the new ones go, and the pages' factors
-        if (!(ok = wait_warp(&s_hempty[hb], (k / S::kOwnHeads & 1) ^ 1, abort_flag, err))) break;
-        char* head = smem + S::kHeadAt + hb * S::kHeadB;
-        const int64_t at_ = ((int64_t)page * heads + run.h) * P;
-        if (mine) {
-          reinterpret_cast<long long*>(head + kTile * 4)[slot_page] = good ? at_ : -1;
-          reinterpret_cast<float*>(head + kTile * 4 + 64)[slot_page] = good ? a.scale * kLog2e * scale : 0.0f;
-        }
-        const bool had = good && run.block == 0 && a.decay != 0.0f && t * kTile + slot_page * P < run.start;
-        const uint32_t olds = __popc(__ballot_sync(0xffffffffu, had));
-        if (lane == 0) mbar_expect_tx(&s_hfull[hb], olds * P * 4);
-        __syncwarp();
-        if (had) bulk_load(head + slot_page * P * 4, a.w + at_, P * 4, &s_hfull[hb]);
-      }
-    }
-    if (!ok) {                                 // gave up: let the copies in flight land (bounded)
-      const uint64_t t0 = global_ns();
-#pragma unroll
-      for (int g = 0; g < G; ++g) {            // (a wait for a phase that is no longer the slot's ends at once or with the limit)
-        for (uint32_t i = count[g] > S::kOwn ? count[g] - S::kOwn : 0; i < count[g]; ++i)
-          while (!mbar_try(&s_kfull[g + G * (i % S::kOwn)], i / S::kOwn & 1) && global_ns() - t0 < 100000000ull) {
-          }
-        for (uint32_t i = count[g] > S::kOwnHeads ? count[g] - S::kOwnHeads : 0; i < count[g]; ++i)
-          while (!mbar_try(&s_hfull[g + G * (i % S::kOwnHeads)], i / S::kOwnHeads & 1) && global_ns() - t0 < 100000000ull) {
-          }
-      }
-    }
-  } else {
-    // ---------------- blocks of rows ----------------
-    if (lane == 0) {
-      pdl_wait();                              // laid out by the kernel before
+    auto next_of = [&](int gr) {
       uint32_t k = 0;
-      const char* q = a.ws + rows_at(heads, groups);
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        if (i == gr) k = count[i]++;
+      return k;
+    };
+    int page = ask_pages();
+    bool begun = false;
+    const uint64_t limit = 100000000ull;
+    if (warp == 4 * G) {
+      // ---------------- tiles of codes ----------------
+      int page_next = ask_pages();
       while (ok && next()) {
-        if (run.first >= run.t1) continue;
-        const int qb = k & 1, n8 = (rows_of() + 7) / 8;
+        const int first = max(run.t0, run.first);
+        for (int t = first, gr = run.turn; t < run.t1; ++t, gr = gr + 1 == G ? 0 : gr + 1) {
+          const uint32_t k = next_of(gr);
+          const int in_batch = (t - first) & (batch - 1), slot = gr + G * (k % S::kOwn);
+          if (in_batch == 0 && begun) page = page_next, page_next = ask_pages();
+          begun = true;
+          const bool good = which == in_batch && known(page);
+          const uint32_t there = __ballot_sync(0xffffffffu, good);
+          if (!(ok = wait_warp(&s_kempty[slot], (k / S::kOwn & 1) ^ 1, abort_flag, err))) break;
+          if (lane == 0) mbar_expect_tx(&s_kfull[slot], __popc(there) * P * D);
+          __syncwarp();
+          if (good) {
+            char* to = smem + slot * S::kTileB + slot_page * P * S::kRowB;
+#pragma unroll
+            for (int i = 0; i < S::kSubs; ++i)
+              tma_load_3d(to + i * (kTile * 128), &kmap, i * 128, run.h * P, page, &s_kfull[slot]);
+          }
+        }
+      }
+      if (!ok) {                               // gave up: let the copies in flight land (bounded)
+        const uint64_t t0 = global_ns();
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          for (uint32_t i = count[g] > S::kOwn ? count[g] - S::kOwn : 0; i < count[g]; ++i)
+            while (!mbar_try(&s_kfull[g + G * (i % S::kOwn)], i / S::kOwn & 1) && global_ns() - t0 < limit) {
+            }
+      }
+    } else {
+      // ---------------- blocks of rows; tiles' old weights, places of the new ones, factors ----------------
+      auto ask_scale = [&](int pg, int h) {
+        return __uint_as_float(load_ahead(a.c.k_scales + (int64_t)pg * heads + h, known(pg), 0u));
+      };
+      float scale = ask_scale(page, lr.h), scale_next = 0.0f;
+      int page_next = ask_pages(), h_next = lr.h;
+      uint32_t blocks = 0;
+      const char* q = a.ws + rows_at(heads, groups);
+      pdl_wait();                              // the rows are laid out by the kernel before
+      while (ok && next()) {
+        const int first = max(run.t0, run.first);
+        if (first >= run.t1) continue;
+        const int qb = blocks & 1, n8 = (rows_of() + 7) / 8;
         const int64_t g0 = first_group(run.row0, group) + run.block * (S::kRows / 8);
-        if (!(ok = wait_thread(&s_qempty[qb], (k >> 1 & 1) ^ 1, abort_flag, err))) break;
-        mbar_expect_tx(&s_qfull[qb], (uint32_t)n8 * (64 + 32 + 16 * D));
-        bulk_load(smem + S::kInfoAt + qb * S::kRows * 8, a.ws + kAlign + ((int64_t)run.h * groups + g0) * 64, n8 * 64, &s_qfull[qb]);
-        bulk_load(smem + S::kTokenAt + qb * S::kRows * 4, a.ws + tokens_at(heads, groups) + g0 * 32, n8 * 32, &s_qfull[qb]);
-        for (int i = 0; i < D / 64; ++i)
-          bulk_load(smem + S::kQAt + qb * S::kQB + i * S::kHalf, q + (((int64_t)run.h * (D / 64) + i) * groups + g0) * 1024,
-                    n8 * 1024, &s_qfull[qb]);
-        ++k;
+        if (!(ok = wait_warp(&s_qempty[qb], (blocks >> 1 & 1) ^ 1, abort_flag, err))) break;
+        if (lane == 0) {
+          mbar_expect_tx(&s_qfull[qb], (uint32_t)n8 * (64 + 32 + 16 * D));
+          bulk_load(smem + S::kInfoAt + qb * S::kRows * 8, a.ws + kAlign + ((int64_t)run.h * groups + g0) * 64, n8 * 64, &s_qfull[qb]);
+          bulk_load(smem + S::kTokenAt + qb * S::kRows * 4, a.ws + tokens_at(heads, groups) + g0 * 32, n8 * 32, &s_qfull[qb]);
+          for (int i = 0; i < D / 64; ++i)
+            bulk_load(smem + S::kQAt + qb * S::kQB + i * S::kHalf, q + (((int64_t)run.h * (D / 64) + i) * groups + g0) * 1024,
+                      n8 * 1024, &s_qfull[qb]);
+        }
+        __syncwarp();
+        ++blocks;
+        for (int t = first, gr = run.turn; t < run.t1; ++t, gr = gr + 1 == G ? 0 : gr + 1) {
+          const uint32_t k = next_of(gr);
+          const int in_batch = (t - first) & (batch - 1), hb = gr + G * (k % S::kOwnHeads);
+          if (in_batch == 0 && begun) {
+            page = page_next, scale = scale_next;
+            page_next = ask_pages();
+            h_next = lr.h;
+          }
+          begun = true;
+          if (in_batch == min(1, min(batch, run.t1 - (t - in_batch)) - 1)) scale_next = ask_scale(page_next, h_next);
+          const bool mine = which == in_batch, good = mine && known(page);
+          if (mine && !good && page != -2) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+          const bool had = good && run.block == 0 && a.decay != 0.0f && t * kTile + slot_page * P < run.start;
+          const uint32_t olds = __popc(__ballot_sync(0xffffffffu, had));
+          if (!(ok = wait_warp(&s_hempty[hb], (k / S::kOwnHeads & 1) ^ 1, abort_flag, err))) break;
+          char* head = smem + S::kHeadAt + hb * S::kHeadB;
+          const int64_t at_ = ((int64_t)page * heads + run.h) * P;
+          if (mine) {
+            reinterpret_cast<long long*>(head + kTile * 4)[slot_page] = good ? at_ : -1;
+            reinterpret_cast<float*>(head + kTile * 4 + 64)[slot_page] = good ? a.scale * kLog2e * scale : 0.0f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(&s_hfull[hb], olds * P * 4);
+          __syncwarp();
+          if (had) bulk_load(head + slot_page * P * 4, a.w + at_, P * 4, &s_hfull[hb]);
+        }
       }
       if (!ok) {
         const uint64_t t0 = global_ns();
-        for (uint32_t i = k > 2 ? k - 2 : 0; i < k; ++i)
-          while (!mbar_try(&s_qfull[i & 1], i >> 1 & 1) && global_ns() - t0 < 100000000ull) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          for (uint32_t i = count[g] > S::kOwnHeads ? count[g] - S::kOwnHeads : 0; i < count[g]; ++i)
+            while (!mbar_try(&s_hfull[g + G * (i % S::kOwnHeads)], i / S::kOwnHeads & 1) && global_ns() - t0 < limit) {
+            }
+        for (uint32_t i = blocks > 2 ? blocks - 2 : 0; i < blocks; ++i)
+          while (!mbar_try(&s_qfull[i & 1], i >> 1 & 1) && global_ns() - t0 < limit) {
           }
       }
     }
