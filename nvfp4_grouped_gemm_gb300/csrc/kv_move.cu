@@ -4,22 +4,20 @@
 // A page has one scale per head, so a page into which tokens move takes the largest of their old pages'
 // scales and its codes become RN(code * old / new); where old = new the bits are copied.
 //
-// keep: a CTA per (sequence, key head, plane) walks the pages that change in order. Places ascend, so
+// keep: a CTA per (sequence, key head) walks the pages that change in order. Places ascend, so
 // a page's tokens come from itself or later pages; a page is read whole before it is written, and no
 // later page needs what an earlier one overwrote.
 //
 // evict: select_kernel finds, per (sequence, key head), the weights' threshold by a radix descent over
-// order-preserving keys (11, 11 and 10 bits, histograms in shared memory), then lists the kept places
-// by ballots in order: ties at the threshold go to the lower places. copy_kernel has a CTA per page
-// of the copy; all reads are from pages that nobody writes, so pages are independent of one another.
+// order-preserving keys (11, 11 and 10 bits, histograms in shared memory, of up to 8 CTAs' a cluster
+// over distributed shared memory), then lists the kept places by ballots in order: ties at the threshold go to the lower places. copy_kernel has a CTA per 256
+// places of the copy; all reads are from pages that nobody writes, so pages are independent of one another.
 #include "serving.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kMoveThreads = 256;
-// 16-byte pieces of a page per thread and plane: 128 slots of 256 values.
-constexpr int kMostPieces = 128 * 256 / 16 / kMoveThreads;
 
 // Four codes under another scale.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
@@ -34,27 +32,27 @@ __device__ __forceinline__ uint4 rescale16(const uint4& v, float ratio) {
 // ---------------------------------------------------------------------------
 // keep
 // ---------------------------------------------------------------------------
+// PIECES: a thread's 16-byte pieces of both planes of a page.
+template <int PIECES>
 __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constant__ KeepArgs a) {
   __shared__ int s_first_bad, s_first_move;
   __shared__ int s_from[128];                  // a slot's source page (-1: stays as it is)
   __shared__ int s_slot[128];
-  __shared__ float s_ratio[128];
-  __shared__ float s_new;
-  const int tid = threadIdx.x, plane = blockIdx.x & 1;
-  const int h = (blockIdx.x >> 1) % a.c.kv_heads, b = (blockIdx.x >> 1) / a.c.kv_heads;
-  const int P = a.c.page_size, D = a.c.head_dim, heads = a.c.kv_heads;
-  const bool speaks = plane == 0 && h == 0;    // reports and writes the new length
+  __shared__ float s_ratio[2][128];
+  __shared__ float s_new[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % a.c.kv_heads, b = blockIdx.x / a.c.kv_heads;
+  const int P = a.c.page_size, log_p = 31 - __clz(P), D = a.c.head_dim, heads = a.c.kv_heads;
   const int n = max(a.b.q_offsets[b + 1] - a.b.q_offsets[b], 0), len = a.b.seq_lens[b];
-  const int start = len - n;
+  const int start = len - n, asked = min(max(a.n_keep[b], 0), a.width);
   if (start < 0 || len > (int64_t)a.b.max_pages * P) {
-    if (speaks && tid == 0) {
+    if (h == 0 && tid == 0) {
       atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
       a.new_lens[b] = len;
     }
     return;
   }
   const int32_t* list = a.keep + (int64_t)b * a.width;
-  const int asked = min(max(a.n_keep[b], 0), a.width);
   if (tid == 0) s_first_bad = asked, s_first_move = asked;
   __syncthreads();
   for (int i = tid; i < asked; i += kMoveThreads) {
@@ -64,76 +62,82 @@ __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constan
   }
   __syncthreads();
   const int count = s_first_bad, move0 = min(s_first_move, count);
-  if (speaks && tid == 0) {
+  if (h == 0 && tid == 0) {
     if (count < asked) atomicOr(a.err, (uint32_t)MOE_DEVERR_TOKEN);
     a.new_lens[b] = start + count;
   }
-  uint8_t* codes = plane ? a.c.v_codes : a.c.k_codes;
-  float* scales = plane ? a.c.v_scales : a.c.k_scales;
+  if (move0 == count) return;
   const int32_t* table = a.b.page_table + (int64_t)b * a.b.table_stride;
-  const int pieces = D / 16, all = P * pieces;
-  for (int pi = (start + move0) / P; pi * P < start + count; ++pi) {
-    if (move0 == count) break;
+  const int log_d = 31 - __clz(D / 16), plane_pieces = P << log_d;
+  auto known = [&](int page) { return page >= 0 && page < a.c.num_pages; };
+  for (int pi = (start + move0) >> log_p; pi * P < start + count; ++pi) {
     const int page = table[pi];
-    const bool good = page >= 0 && page < a.c.num_pages;
+    const bool good = known(page);
     __syncthreads();                           // the page before is done with the shared arrays
-    if (tid < 32) {                            // a lane per slot, the largest scale over all
+    if (warp < 2) {                            // a warp per plane, a lane per slot; the largest scale over all
+      const float* scales = warp ? a.c.v_scales : a.c.k_scales;
       const float own = good ? scales[(int64_t)page * heads + h] : 0.0f;
       float top = own;
-      for (int s = tid; s < P; s += 32) {
+      for (int s = lane; s < P; s += 32) {
         const int i = pi * P + s - start;      // the kept token that lands here
         int from = -1, slot = 0;
         float scale = own;
         if (i >= move0 && i < count && list[i] != i) {
-          const int src = start + list[i];
-          const int p = table[src / P];
-          if (good && p >= 0 && p < a.c.num_pages) {
-            from = p, slot = src % P;
+          const int src = start + list[i], p = table[src >> log_p];
+          if (good && known(p)) {
+            from = p, slot = src & (P - 1);
             scale = scales[(int64_t)p * heads + h];
           } else {
             atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
           }
         }
-        s_from[s] = from, s_slot[s] = slot, s_ratio[s] = scale;
+        if (warp == 0) s_from[s] = from, s_slot[s] = slot;
+        s_ratio[warp][s] = scale;
         top = fmaxf(top, scale);
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      for (int s = tid; s < P; s += 32) s_ratio[s] = s_ratio[s] == top ? 1.0f : s_ratio[s] / top;
-      if (tid == 0) s_new = top > own ? top : 0.0f;        // 0: the scale stays
+      for (int s = lane; s < P; s += 32) s_ratio[warp][s] = s_ratio[warp][s] == top ? 1.0f : s_ratio[warp][s] / top;
+      if (lane == 0) s_new[warp] = top > own ? top : 0.0f;       // 0: the scale stays
     }
     __syncthreads();
     if (!good) continue;
-    const bool grew = s_new > 0.0f;
-    uint4 v[kMostPieces];
+    uint4 v[PIECES];
+    auto place = [&](int k, int& s, int& plane) {          // of the thread's piece k; whether it is written
+      const int u = tid + k * kMoveThreads;
+      plane = u >= plane_pieces;
+      s = (u - plane * plane_pieces) >> log_d;
+      return u < 2 * plane_pieces && (s_from[s] >= 0 || s_new[plane] > 0.0f);
+    };
+    const int in = (tid & (D / 16 - 1)) * 16;  // (the threads of a block are whole rows)
 #pragma unroll
-    for (int k = 0; k < kMostPieces; ++k) {
-      const int u = tid + k * kMoveThreads, s = u / pieces;
+    for (int k = 0; k < PIECES; ++k) {
+      int s, plane;
       v[k] = make_uint4(0, 0, 0, 0);
-      if (u < all && (grew || s_from[s] >= 0)) {
-        const int p = s_from[s] >= 0 ? s_from[s] : page, sl = s_from[s] >= 0 ? s_slot[s] : s;
-        v[k] = *reinterpret_cast<const uint4*>(codes + (int64_t)p * a.c.page_stride +
-                                               ((int64_t)h * P + sl) * D + (u % pieces) * 16);
-      }
+      if (!place(k, s, plane)) continue;
+      const int p = s_from[s] >= 0 ? s_from[s] : page, sl = s_from[s] >= 0 ? s_slot[s] : s;
+      v[k] = *reinterpret_cast<const uint4*>((plane ? a.c.v_codes : a.c.k_codes) + (int64_t)p * a.c.page_stride +
+                                             ((int64_t)h * P + sl) * D + in);
     }
     __syncthreads();                           // the page is read whole before it is written
 #pragma unroll
-    for (int k = 0; k < kMostPieces; ++k) {
-      const int u = tid + k * kMoveThreads, s = u / pieces;
-      if (u < all && (grew || s_from[s] >= 0))
-        *reinterpret_cast<uint4*>(codes + (int64_t)page * a.c.page_stride + ((int64_t)h * P + s) * D +
-                                  (u % pieces) * 16) = rescale16(v[k], s_ratio[s]);
+    for (int k = 0; k < PIECES; ++k) {
+      int s, plane;
+      if (place(k, s, plane))
+        *reinterpret_cast<uint4*>((plane ? a.c.v_codes : a.c.k_codes) + (int64_t)page * a.c.page_stride +
+                                  ((int64_t)h * P + s) * D + in) = rescale16(v[k], s_ratio[plane][s]);
     }
-    if (grew && tid == 0) scales[(int64_t)page * heads + h] = s_new;
+    if (tid < 2 && s_new[tid] > 0.0f) (tid ? a.c.v_scales : a.c.k_scales)[(int64_t)page * heads + h] = s_new[tid];
   }
 }
 
 // ---------------------------------------------------------------------------
 // evict
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kHeldKeys = 24 * 1024;           // keys that stay in shared memory
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048, kMine = kBins / kSelThreads;
+constexpr int kHeldKeys = 9 * 1024;            // keys that a CTA keeps in shared memory
+constexpr int kMostCluster = 8;
 
 // Unsigned order of weights: NaN 0, below every number; -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -159,45 +163,99 @@ __device__ __forceinline__ Share share_of(const EvictArgs& a, int b) {
   return s;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictArgs a) {
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word of shared memory at the same place in the cluster's CTA `rank`.
+__device__ __forceinline__ int of_rank(const int* p, int rank) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  int v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.s32 %0, [a];\n\t}"
+               : "=r"(v) : "r"(at), "r"(rank) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int4 four_of_rank(const int* p, int rank) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  int4 v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [a];\n\t}"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "r"(rank) : "memory");
+  return v;
+}
+
+// A cluster of `size` CTAs per (sequence, key head), each with a run of the candidates.
+__global__ void __launch_bounds__(kSelThreads, 4) select_kernel(const __grid_constant__ EvictArgs a, int size) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ int s_hist[kBins];
-  __shared__ int s_warp[kSelWarps], s_warp2[kSelWarps];
+  __shared__ __align__(16) int s_hist[2][kBins];             // in turn, so that others may still read the one before
+  __shared__ int s_warp[kSelWarps], s_warp2[kSelWarps], s_all[2];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x % a.c.kv_heads, b = blockIdx.x / a.c.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % size;
+  const int h = blockIdx.x / size % a.c.kv_heads, b = blockIdx.x / size / a.c.kv_heads;
   const int P = a.c.page_size, log_p = 31 - __clz(P), heads = a.c.kv_heads;
+  const int t0 = rank * kSelThreads + tid, step = size * kSelThreads;
   const Share sh = share_of(a, b);
-  if (h == 0 && tid == 0) {
+  if (h == 0 && t0 == 0) {
     a.new_lens[b] = sh.alone ? a.b.seq_lens[b] : sh.keep;
     if (!sh.alone && a.b.seq_lens[b] > sh.len) atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
   }
   int32_t* kept = a.kept + ((int64_t)b * heads + h) * a.width;
   const int shown = sh.alone ? 0 : sh.keep;
-  for (int i = shown + tid; i < a.width; i += kSelThreads) kept[i] = -1;
+  for (int i = shown + t0; i < a.width; i += step) kept[i] = -1;
   if (shown == 0) return;
   if (sh.keep == sh.len) {
-    for (int i = tid; i < sh.keep; i += kSelThreads) kept[i] = i;
+    for (int i = t0; i < sh.keep; i += step) kept[i] = i;
     return;
   }
-  for (int i = tid; i < sh.first; i += kSelThreads) kept[i] = i;
-  for (int i = tid; i < sh.recent; i += kSelThreads) kept[sh.keep - 1 - i] = sh.len - 1 - i;
+  for (int i = t0; i < sh.first; i += step) kept[i] = i;
+  for (int i = t0; i < sh.recent; i += step) kept[sh.keep - 1 - i] = sh.len - 1 - i;
   const int choose = sh.keep - sh.recent - sh.first;
   if (choose == 0) return;
-  const int lo = sh.first, N = sh.len - sh.recent - lo;     // candidates, more than `choose`
+  const int all = sh.len - sh.recent - sh.first;           // candidates, more than `choose`
+  const int share = (all + size * 32 - 1) / (size * 32) * 32;
+  const int before_me = min(rank * share, all), lo = sh.first + before_me, N = min(share, all - before_me);
   const int32_t* table = a.b.page_table + (int64_t)b * a.b.table_stride;
-  auto load_key = [&](int i) {
-    const int j = lo + i, page = table[j >> log_p];
-    if (page < 0 || page >= a.c.num_pages) {
-      atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
-      return 0u;
+  auto known = [&](int page) { return page >= 0 && page < a.c.num_pages; };
+  // keys of candidates i .. of this thread, their pages and then their weights on their way together
+  constexpr int kBatch = 8;
+  bool bad = false;
+  auto load_keys = [&](int i, uint32_t (&k)[kBatch]) {
+    int page[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+      page[x] = (int)load_ahead(table + ((lo + i + x * kSelThreads) >> log_p), i + x * kSelThreads < N, 0u);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int j = lo + i + x * kSelThreads;
+      bad |= !known(page[x]);
+      k[x] = load_ahead(a.w + ((int64_t)page[x] * heads + h) * P + (j & (P - 1)),
+                        i + x * kSelThreads < N && known(page[x]), 0x7fc00000u);
     }
-    return weight_key(a.w[((int64_t)page * heads + h) * P + (j & (P - 1))]);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) k[x] = weight_key(__uint_as_float(k[x]));
   };
-  const int held = min(N, kHeldKeys);
-  for (int i = tid; i < held; i += kSelThreads) s_keys[i] = load_key(i);
-  auto key = [&](int i) { return i < held ? s_keys[i] : load_key(i); };
+  const int held = min(N, kHeldKeys);          // the others are read again in every pass
+  for (int i = tid; i < held; i += kSelThreads * kBatch) {
+    uint32_t k[kBatch];
+    load_keys(i, k);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+      if (i + x * kSelThreads < held) s_keys[i + x * kSelThreads] = k[x];
+  }
+  for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0;
+  __syncthreads();
+  auto each_key = [&](auto&& take) {           // take(key, there) by whole warps
+    for (int i0 = 0; i0 < held; i0 += kSelThreads) take(i0 + tid < held ? s_keys[i0 + tid] : 0u, i0 + tid < held);
+    for (int i0 = held / (kSelThreads * kBatch) * (kSelThreads * kBatch); held < N && i0 < N; i0 += kSelThreads * kBatch) {
+      uint32_t k[kBatch];
+      load_keys(i0 + tid, k);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int i = i0 + tid + x * kSelThreads;
+        take(k[x], i >= held && i < N);
+      }
+    }
+  };
 
   // the threshold: the key of rank `choose`, bits from the top
   uint32_t prefix = 0;
@@ -205,23 +263,38 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass < 2 ? 11 : 10;
+    int* hist = s_hist[pass & 1];
     shift -= bits;
-    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-    __syncthreads();                           // (and, the first time, the keys)
-    for (int i0 = 0; i0 < N; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const uint32_t k = i < N ? key(i) : 0;
-      const bool mine = i < N && (pass == 0 || (k >> (shift + bits)) == prefix);
+    each_key([&](uint32_t k, bool there) {
+      const bool mine = there && (pass == 0 || (k >> (shift + bits)) == prefix);
+      const uint32_t any = __ballot_sync(0xffffffffu, mine);
+      if (any == 0) return;
       const uint32_t bin = mine ? (k >> shift) & ((1u << bits) - 1) : 0xffffffffu;
-      // one addition per distinct bin of the warp: weights crowd into few bins
-      const uint32_t same = __match_any_sync(0xffffffffu, bin);
-      if (mine && lane == __ffs(same) - 1) atomicAdd(&s_hist[bin], __popc(same));
+      // the lanes that share the first one's bin add together: weights that are all alike (0) would
+      // otherwise meet at one address
+      const int lead = __ffs(any) - 1;
+      const uint32_t led = __shfl_sync(0xffffffffu, bin, lead);
+      const uint32_t same = __ballot_sync(0xffffffffu, mine && bin == led);
+      if (lane == lead) atomicAdd(&hist[bin], __popc(same));
+      else if (mine && !(same >> lane & 1)) atomicAdd(&hist[bin], 1);
+    });
+    if (size > 1) cluster_sync();
+    else __syncthreads();
+    // (from here on nobody reads the other histogram any more)
+    if (pass < 2)
+      for (int i = tid; i < kBins; i += kSelThreads) s_hist[~pass & 1][i] = 0;
+    // bins from the top, kMine per thread: the bin in which the count passes `need`
+    const int top = kBins - 1 - kMine * tid;
+    static_assert(kMine == 4, "");
+    int c[kMine] = {};
+    for (int r = 0; r < size; ++r) {
+      const int4 v = size > 1 ? four_of_rank(&hist[top - 3], r) : *reinterpret_cast<const int4*>(&hist[top - 3]);
+      c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
     }
-    __syncthreads();
-    // bins from the top, two per thread: the bin in which the count passes `need`
-    const int top = kBins - 1 - 2 * tid;
-    const int c0 = s_hist[top], c1 = s_hist[top - 1];
-    int upto = c0 + c1;
+    int mine = 0;
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) mine += c[x];
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, upto, o);
@@ -229,11 +302,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     }
     if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += s_warp[w];
-    const int before = base + upto - c0 - c1;
-    if (before < need && need <= before + c0) s_prefix = top, s_need = need - before;
-    else if (before + c0 < need && need <= before + c0 + c1) s_prefix = top - 1, s_need = need - before - c0;
+    int before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      if (before < need && need <= before + c[x]) s_prefix = top - x, s_need = need - before;
+      before += c[x];
+    }
     __syncthreads();
     prefix = prefix << bits | s_prefix;
     need = s_need;
@@ -242,19 +317,36 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   // of places; counts first, then places.
   const int run = (N + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
   const int r0 = min(warp * run, N), r1 = min(r0 + run, N);
+  auto key = [&](int i) {
+    if (i < held) return s_keys[i];
+    const int j = lo + i, page = table[j >> log_p];
+    return known(page) ? weight_key(a.w[((int64_t)page * heads + h) * P + (j & (P - 1))]) : 0u;
+  };
   int above = 0, equal = 0;
   for (int i0 = r0; i0 < r1; i0 += 32) {
-    const uint32_t k = i0 + lane < r1 ? key(i0 + lane) : 0;
     const bool in = i0 + lane < r1;
+    const uint32_t k = in ? key(i0 + lane) : 0;
     above += __popc(__ballot_sync(0xffffffffu, in && k > prefix));
     equal += __popc(__ballot_sync(0xffffffffu, in && k == prefix));
   }
   if (lane == 0) s_warp[warp] = above, s_warp2[warp] = equal;
   __syncthreads();
   int at = 0, eq = 0;                          // kept, equal before this warp's run
+  if (size > 1) {
+    if (tid == 0) {
+      int x = 0, y = 0;
+      for (int w = 0; w < kSelWarps; ++w) x += s_warp[w], y += s_warp2[w];
+      s_all[0] = x, s_all[1] = y;
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      const int x = of_rank(&s_all[0], r), y = of_rank(&s_all[1], r);
+      at += x + min(max(need - eq, 0), y);
+      eq += y;
+    }
+  }
   for (int w = 0; w < warp; ++w) {
-    const int take = min(max(need - eq, 0), s_warp2[w]);
-    at += s_warp[w] + take;
+    at += s_warp[w] + min(max(need - eq, 0), s_warp2[w]);
     eq += s_warp2[w];
   }
   const uint32_t below = (1u << lane) - 1;
@@ -268,70 +360,82 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     at += __popc(t);
     eq += __popc(e);
   }
+  if (bad) atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
+  if (size > 1) cluster_sync();                // nobody reads this CTA's shared memory any more
 }
 
-// One page of the copy, both planes.
+// kMoveThreads places of the copy (whole pages, of one key head), both planes: thread = place until the
+// pages' scales are known, then the places' 16-byte pieces in turn, kInFlight of a thread on their way
+// together and asked for before the scales are.
 __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ int s_page[128], s_slot[128];     // where a slot's token comes from (-1: nowhere)
-  __shared__ float s_ratio[2][128];
+  constexpr int kMostPages = kMoveThreads / 16, kInFlight = 8;
+  __shared__ int64_t s_from[kMoveThreads], s_to[kMoveThreads];   // bytes into a plane (-1: nowhere)
+  __shared__ float s_ratio[2][kMoveThreads];
+  __shared__ uint32_t s_top[2][kMostPages];
   const int tid = threadIdx.x;
   const int P = a.c.page_size, log_p = 31 - __clz(P), D = a.c.head_dim, heads = a.c.kv_heads;
-  const int pages = (a.width + P - 1) / P, pi = blockIdx.x % pages;
-  const int h = blockIdx.x / pages % heads, b = blockIdx.x / pages / heads;
+  const int blocks = (a.width + kMoveThreads - 1) / kMoveThreads;
+  const int h = blockIdx.x / blocks % heads, b = blockIdx.x / blocks / heads;
   const Share sh = share_of(a, b);
-  const int p0 = pi * P;
+  const int i0 = blockIdx.x % blocks * kMoveThreads, i = i0 + tid;
+  const int page = i < sh.keep ? a.dst_table[(int64_t)b * a.dst_stride + (i >> log_p)] : -1;
+  if (tid < kMostPages) s_top[0][tid] = s_top[1][tid] = 0;
   pdl_wait();
-  if (sh.alone || p0 >= sh.keep) return;
-  const int count = min(P, sh.keep - p0);
-  const int page = a.dst_table[(int64_t)b * a.dst_stride + pi];
-  if (page < 0 || page >= a.c.num_pages) {
-    if (tid == 0) atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
-    return;
+  if (sh.alone || i0 >= sh.keep) return;
+  const int count = min(kMoveThreads, sh.keep - i0);
+  int from = -1, slot = 0;
+  bool good = false;
+  if (tid < count) {
+    const int src = a.kept[((int64_t)b * heads + h) * a.width + i];
+    from = a.b.page_table[(int64_t)b * a.b.table_stride + (src >> log_p)];
+    slot = src & (P - 1);
+    good = from >= 0 && from < a.c.num_pages && page >= 0 && page < a.c.num_pages;
+    if (!good) atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
   }
-  const int32_t* table = a.b.page_table + (int64_t)b * a.b.table_stride;
-  if (tid < 128) {
-    int from = -1, slot = 0;
-    float sk = 0.0f, sv = 0.0f;
-    if (tid < count) {
-      const int src = a.kept[((int64_t)b * heads + h) * a.width + p0 + tid];
-      from = table[src >> log_p];
-      slot = src & (P - 1);
-      if (from < 0 || from >= a.c.num_pages) {
-        atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
-        from = -1;
-      } else {
-        sk = a.c.k_scales[(int64_t)from * heads + h];
-        sv = a.c.v_scales[(int64_t)from * heads + h];
-        a.w[((int64_t)page * heads + h) * P + tid] = a.w[((int64_t)from * heads + h) * P + slot];
-      }
-    }
-    s_page[tid] = from, s_slot[tid] = slot;
-    s_ratio[0][tid] = sk, s_ratio[1][tid] = sv;
-  }
+  s_from[tid] = good ? (int64_t)from * a.c.page_stride + ((int64_t)h * P + slot) * D : -1;
+  s_to[tid] = (int64_t)page * a.c.page_stride + ((int64_t)h * P + (i & (P - 1))) * D;
+  const float sk = __uint_as_float(load_ahead(a.c.k_scales + (int64_t)from * heads + h, good, 0u));
+  const float sv = __uint_as_float(load_ahead(a.c.v_scales + (int64_t)from * heads + h, good, 0u));
+  const float w = __uint_as_float(load_ahead(a.w + ((int64_t)from * heads + h) * P + slot, good, 0u));
   __syncthreads();
-  if (tid < 64) {                              // a warp per plane
-    const int plane = tid >> 5, lane = tid & 31;
-    float top = 0.0f;
-    for (int s = lane; s < count; s += 32) top = fmaxf(top, s_ratio[plane][s]);
+  const int log_d = 31 - __clz(D / 16), all = count << log_d;
+  uint4 v[kInFlight];
+  auto ask = [&](const uint8_t* codes, int u0) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int s = lane; s < count; s += 32) {
-      const float was = s_ratio[plane][s];
-      s_ratio[plane][s] = was == top ? 1.0f : was / top;
+    for (int k = 0; k < kInFlight; ++k) {
+      const int u = u0 + k * kMoveThreads;
+      const int64_t at = u < all ? s_from[u >> log_d] : -1;
+      v[k] = load_ahead(codes + at + (u & (D / 16 - 1)) * 16, at >= 0);
     }
-    if (lane == 0 && top > 0.0f) (plane ? a.c.v_scales : a.c.k_scales)[(int64_t)page * heads + h] = top;
+  };
+  ask(a.c.k_codes, tid);
+  // a page's scale: the largest of its tokens' (their bits order as they do)
+  if (good) {
+    atomicMax(&s_top[0][tid >> log_p], __float_as_uint(sk));
+    atomicMax(&s_top[1][tid >> log_p], __float_as_uint(sv));
+    a.w[((int64_t)page * heads + h) * P + (i & (P - 1))] = w;
   }
   __syncthreads();
-  const int pieces = D / 16, all = count * pieces;
+  const float tk = __uint_as_float(s_top[0][tid >> log_p]), tv = __uint_as_float(s_top[1][tid >> log_p]);
+  s_ratio[0][tid] = sk == tk ? 1.0f : sk / tk;
+  s_ratio[1][tid] = sv == tv ? 1.0f : sv / tv;
+  if (tid < count && (tid & (P - 1)) == 0 && page >= 0 && page < a.c.num_pages) {
+    if (tk > 0.0f) a.c.k_scales[(int64_t)page * heads + h] = tk;
+    if (tv > 0.0f) a.c.v_scales[(int64_t)page * heads + h] = tv;
+  }
+  __syncthreads();
+#pragma unroll 1
   for (int plane = 0; plane < 2; ++plane) {
     uint8_t* codes = plane ? a.c.v_codes : a.c.k_codes;
-    for (int u = tid; u < all; u += kMoveThreads) {
-      const int s = u / pieces;
-      if (s_page[s] < 0) continue;
-      const uint4 v = *reinterpret_cast<const uint4*>(codes + (int64_t)s_page[s] * a.c.page_stride +
-                                                      ((int64_t)h * P + s_slot[s]) * D + (u % pieces) * 16);
-      *reinterpret_cast<uint4*>(codes + (int64_t)page * a.c.page_stride + ((int64_t)h * P + s) * D +
-                                (u % pieces) * 16) = rescale16(v, s_ratio[plane][s]);
+#pragma unroll 1
+    for (int u0 = tid; u0 < all; u0 += kInFlight * kMoveThreads) {
+      if (plane || u0 != tid) ask(codes, u0);
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        const int u = u0 + k * kMoveThreads, s = u >> log_d;
+        if (u < all && s_from[s] >= 0)
+          *reinterpret_cast<uint4*>(codes + s_to[s] + (u & (D / 16 - 1)) * 16) = rescale16(v[k], s_ratio[plane][s]);
+      }
     }
   }
 }
@@ -339,7 +443,13 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_keep(const KeepArgs& a, cudaStream_t s) {
-  keep_kernel<<<(unsigned)(2 * a.b.B * a.c.kv_heads), kMoveThreads, 0, s>>>(a);
+  const unsigned grid = (unsigned)(a.b.B * a.c.kv_heads);
+  const int pieces = a.c.page_size * (a.c.head_dim / 16) * 2 / kMoveThreads;     // 0 (half of them idle) to 16
+  if (pieces <= 1) keep_kernel<1><<<grid, kMoveThreads, 0, s>>>(a);
+  else if (pieces == 2) keep_kernel<2><<<grid, kMoveThreads, 0, s>>>(a);
+  else if (pieces == 4) keep_kernel<4><<<grid, kMoveThreads, 0, s>>>(a);
+  else if (pieces == 8) keep_kernel<8><<<grid, kMoveThreads, 0, s>>>(a);
+  else keep_kernel<16><<<grid, kMoveThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -348,10 +458,26 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const unsigned heads = (unsigned)(a.b.B * a.c.kv_heads);
-  select_kernel<<<heads, kSelThreads, smem, s>>>(a);
+  // CTAs per (sequence, key head): while there is room for them (four per SM) and 2048 places for each,
+  // as far as the page table's width tells.
+  const long long places = (long long)a.b.max_pages * a.c.page_size;
+  int size = 1;
+  while (size < kMostCluster && 2LL * size * heads <= 4LL * num_sms() && places >= 4096LL * size) size *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(heads * size);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, select_kernel, a, size)) != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess || a.width == 0) return e;
-  const unsigned pages = (unsigned)((a.width + a.c.page_size - 1) / a.c.page_size);
-  return launch_pdl(copy_kernel, dim3(pages * heads), dim3(kMoveThreads), 0, s, a);
+  const unsigned blocks = (unsigned)((a.width + kMoveThreads - 1) / kMoveThreads);
+  return launch_pdl(copy_kernel, dim3(blocks * heads), dim3(kMoveThreads), 0, s, a);
 }
 
 }  // namespace moe

@@ -225,6 +225,19 @@ def test_weights_of_every_kind():
 def test_keys_that_do_not_fit_into_shared_memory():
     rng = np.random.default_rng(25)
     evict(rng, [60001], [4096], 128, 1, 64, first=4, recent=100)
+    evict(rng, [100003, 9], [5000, 7], 128, 1, 64, first=4, recent=100)
+
+
+@pytest.mark.parametrize("lens", [[4100], [8300, 5], [17000, 8193, 100], [33000, 40], [5000, 4000, 3000, 2000]])
+def test_candidates_over_several_blocks(lens):
+    """Long sequences' candidates are shared out: ties that cross the shares, and shares without any."""
+    rng = np.random.default_rng(len(lens))
+
+    def few(w, batch):
+        w[:] = rng.choice(np.array([0.0, 1.0, 1.0 + 2.0 ** -23, 3.0], np.float32), w.shape, p=[0.6, 0.2, 0.1, 0.1])
+    for edit_w in (None, few):
+        evict(rng, lens, [max(1, n // 3) for n in lens], 64, 2, 64, first=1, recent=40, edit_w=edit_w)
+    evict(rng, lens, [n - 1 for n in lens], 64, 1, 64, edit_w=few)
 
 
 def test_pages_out_of_range():
