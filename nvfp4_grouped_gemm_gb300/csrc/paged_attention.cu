@@ -65,11 +65,6 @@ constexpr int kSegmentCost = 12;
 // rows 75 / 70; 64 sequences of up to 4000, 80 rows: D = 128 268 / 220, D = 64 172 / 149.
 constexpr int kPromptRows = 73;
 constexpr int kAllRows = 0x7fffffff;
-// The same for trees, whose form for fewer rows is tree_attention.cu's (head_dim 256: this one).
-#ifndef TREER
-#define TREER 129
-#endif
-constexpr int kTreeRows = TREER;
 
 // Workspace: error word; arrival counters [kMaxGrid]; partial maxima and sums
 // [2 * kMaxGrid][2][kMaxRows]; partial rows f32 [2 * kMaxGrid][kMaxRows][D].
@@ -948,18 +943,17 @@ cudaError_t launch_dim(const AttentionArgs& a, cudaStream_t s) {
   return few ? launch_shape<D, 1, D == 256 ? 8 : 12, TREE>(a, s) : launch_shape<D, 1, 4, TREE>(a, s);
 }
 
+template <bool TREE>
 cudaError_t launch_few(const AttentionArgs& a, cudaStream_t s) {
-  if (a.c.head_dim == 64) return launch_dim<64, false>(a, s);
-  if (a.c.head_dim == 128) return launch_dim<128, false>(a, s);
-  return a.tree ? launch_dim<256, true>(a, s) : launch_dim<256, false>(a, s);
+  if (a.c.head_dim == 64) return launch_dim<64, TREE>(a, s);
+  return a.c.head_dim == 128 ? launch_dim<128, TREE>(a, s) : launch_dim<256, TREE>(a, s);
 }
 
 }  // namespace
 
 namespace {
 size_t few_rows_ws_bytes(int head_dim) {
-  const size_t own = align_up(kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4);
-  return head_dim <= 128 && tree_attention_ws_bytes(head_dim) > own ? tree_attention_ws_bytes(head_dim) : own;
+  return align_up(kRowsAt + (size_t)2 * kMaxGrid * kMaxRows * head_dim * 4);
 }
 }  // namespace
 
@@ -970,19 +964,14 @@ size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim) {
 cudaError_t launch_attention(const AttentionArgs& args, cudaStream_t s) {
   AttentionArgs a = args;
   a.max_rows = kAllRows;
-  const long long rows = (long long)a.T * (a.q_heads / a.c.kv_heads);
-  const int least = a.tree ? kTreeRows : kPromptRows;
-  bool beside = false;
-  if (a.c.head_dim <= 128 && (a.tree || a.T > a.b.B) && rows >= least) {
+  if (a.c.head_dim <= 128 && a.T > a.b.B && (long long)a.T * (a.q_heads / a.c.kv_heads) >= kPromptRows) {
     // some sequence may have that many rows; which ones have is settled on the GPU
     const bool all = a.b.B == 1;
-    const cudaError_t e = launch_prompt_attention(a, all ? 1 : least, few_rows_ws_bytes(a.c.head_dim), s);
+    const cudaError_t e = launch_prompt_attention(a, all ? 1 : kPromptRows, few_rows_ws_bytes(a.c.head_dim), s);
     if (e != cudaSuccess || all) return e;
-    a.max_rows = least - 1;
-    beside = true;
+    a.max_rows = kPromptRows - 1;
   }
-  if (a.tree && a.c.head_dim <= 128) return launch_tree_attention(a, beside, s);
-  return launch_few(a, s);
+  return a.tree ? launch_few<true>(a, s) : launch_few<false>(a, s);
 }
 
 }  // namespace moe

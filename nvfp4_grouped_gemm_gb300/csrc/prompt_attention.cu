@@ -62,6 +62,11 @@ constexpr size_t kCountersAt = 0;
 constexpr size_t kStatsAt = kCountersAt + kPromptMaxGrid * 4;
 constexpr size_t kRowsAt = kStatsAt + (size_t)2 * kPromptMaxGrid * 2 * kBlock * 4;
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max16(const float* s) {
   const float a = max3(s[0], s[1], s[2]), b = max3(s[3], s[4], s[5]), c = max3(s[6], s[7], s[8]);
   const float d = max3(s[9], s[10], s[11]), e = max3(s[12], s[13], s[14]);

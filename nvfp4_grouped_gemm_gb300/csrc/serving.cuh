@@ -46,11 +46,6 @@ constexpr int kPromptMaxGrid = 160;
 size_t prompt_attention_ws_bytes(int head_dim);
 cudaError_t launch_prompt_attention(const AttentionArgs& a, int min_rows, size_t ws_at, cudaStream_t s);
 
-// The form for trees of few rows (head_dim 64 or 128), in the few-row form's workspace; `beside`: right
-// behind a launch of the form for many.
-size_t tree_attention_ws_bytes(int head_dim);
-cudaError_t launch_tree_attention(const AttentionArgs& a, bool beside, cudaStream_t s);
-
 struct LinearArgs {
   const uint16_t* x;
   int64_t x_stride, y_stride;
