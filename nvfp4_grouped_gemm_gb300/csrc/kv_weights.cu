@@ -387,15 +387,6 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
           const int n = min(S::kChunk, cols - c0);
           auto add_all = [&](auto hides) {
             int c = 0;
-            if (S::kChunk >= 32) {
-#pragma unroll 1
-              for (; c + 32 <= n; c += 32) {
-                float v[32];
-                tmem_ld32(s_col + quarter + c, v);
-#pragma unroll
-                for (int x = 0; x < 32; x += 8) add8(v + x, c0 + c + x, hides);
-              }
-            }
 #pragma unroll 1
             for (; c < n; c += 16) {
               float v[16];
