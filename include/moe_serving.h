@@ -206,8 +206,8 @@ size_t moe_kv_keep_workspace_bytes(void);
  * rescaled by old / new and rounded again to nearest even, in all slots of such a page. A token
  * from or into a page out of range stays (MOE_DEVERR_PAGE). No two sequences may have a page in
  * common that holds new tokens. A sequence without a valid start keeps its length.
- *   keep i32 [B][width] (may be NULL if width is 0)  n_keep i32 [B]  new_lens i32 [B], not the
- *   batch's own seq_lens */
+ *   keep i32 [B][width] (may be NULL if width is 0)  n_keep i32 [B]  new_lens i32 [B], none of
+ *   the arrays that are read (the batch's seq_lens, n_keep) */
 moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch,
                             const int32_t* keep, const int32_t* n_keep, int32_t width,
                             int32_t* new_lens, void* ws, size_t ws_bytes, void* stream);
@@ -247,8 +247,8 @@ size_t moe_kv_evict_workspace_bytes(int32_t B, int32_t kv_heads);
  * token are left as they were. budgets i32 [B], or NULL for `width` everywhere; a sequence with a
  * negative budget is left alone (new_lens its length, kept -1). Old pages are only read, and may
  * be in use by other sequences; the pages of dst_table in use must be in nobody else's.
- *   w f32 [num_pages][kv_heads][page_size]   kept i32 [B][kv_heads][width]   new_lens i32 [B], not
- *   the batch's own   dst_table i32 [B][dst_stride] with at least ceil(width / page_size) columns
+ *   w f32 [num_pages][kv_heads][page_size]   kept i32 [B][kv_heads][width]   new_lens i32 [B], none
+ *   of the arrays that are read (the batch's seq_lens, budgets)   dst_table i32 [B][dst_stride] with at least ceil(width / page_size) columns
  * Tokens from or into pages out of range are not copied (MOE_DEVERR_PAGE). The batch's q_offsets are
  * not read. */
 moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch, float* w,
@@ -265,7 +265,8 @@ moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* bat
  * with rms(v) = sqrt(mean v^2 + eps) over the row and w = weight + weight_offset; with gate_sigmoid
  * g = 1 / (1 + exp(-gate)). All in f32; out and normed are rounded once each, n from the r that is
  * not rounded. y may be NULL (r = residual, then post_weight and gate are too); out or normed may be
- * NULL, not both. out may be residual or y itself, normed y or residual, with the same type and stride.
+ * NULL, not both. out may be residual or y itself, normed y or residual, with the same type and stride;
+ * neither may be the gate or a weight.
  *   y, residual, out, normed  rows of y_dtype, residual_dtype (out's too), normed_dtype (bf16, f16, f32)
  *   weights                   weight_dtype [H]
  *   gate                      gate_dtype, element (t, i) at t * gate_stride + i * gate_inner,

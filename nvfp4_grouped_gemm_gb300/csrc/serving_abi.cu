@@ -186,7 +186,9 @@ moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batc
   if ((st = check_batch(batch)) != MOE_OK) return st;
   if (width < 0 || (width > 0 && !keep) || !n_keep || !new_lens) return MOE_ERR_INVALID_ARG;
   if (!aligned(keep, 4) || !aligned(n_keep, 4) || !aligned(new_lens, 4)) return MOE_ERR_INVALID_ARG;
-  if (new_lens == batch->seq_lens) return MOE_ERR_INVALID_ARG;
+  // blocks of other heads read these while a block writes new_lens
+  if (new_lens == batch->seq_lens || new_lens == batch->q_offsets || new_lens == n_keep || new_lens == keep)
+    return MOE_ERR_INVALID_ARG;
   if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, moe_kv_keep_workspace_bytes())) != MOE_OK) return st;
   KeepArgs a = {};
@@ -257,7 +259,9 @@ moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* bat
   if (width <= 0 || first < 0 || recent < 0 || !w || !dst_table || !kept || !new_lens) return MOE_ERR_INVALID_ARG;
   if (!aligned(w, 4) || !aligned(dst_table, 4) || !aligned(budgets, 4) || !aligned(kept, 4) || !aligned(new_lens, 4))
     return MOE_ERR_INVALID_ARG;
-  if (new_lens == batch->seq_lens) return MOE_ERR_INVALID_ARG;
+  // blocks of other heads read these while a block writes new_lens; old pages are only read
+  if (new_lens == batch->seq_lens || new_lens == budgets || new_lens == kept || dst_table == batch->page_table)
+    return MOE_ERR_INVALID_ARG;
   if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30) || width > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   const int64_t pages = ((int64_t)width + cache->page_size - 1) / cache->page_size;
   if (dst_stride < pages) return MOE_ERR_INVALID_ARG;
@@ -313,6 +317,8 @@ moe_status moe_residual_norm(const void* y, int64_t y_stride, int32_t y_dtype, c
       !on(normed, normed_stride, normed_dtype, residual, residual_stride, residual_dtype) ||
       !on(normed, normed_stride, normed_dtype, y, y_stride, y_dtype) || (out && out == normed))
     return MOE_ERR_INVALID_ARG;
+  for (const void* in : {gate, post_weight, pre_weight})         // which other rows may share
+    if (in && (in == out || in == normed)) return MOE_ERR_INVALID_ARG;
   NormArgs a = {};
   a.y = y;
   a.residual = residual;

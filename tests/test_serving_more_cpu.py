@@ -122,7 +122,7 @@ def _weights(lib, cache=None, batch=None, **kw):
 
 
 def _evict(lib, cache=None, batch=None, **kw):
-    (a,) = _with(kw, dict(w=256, dst=256, ds=2, budgets=None, width=32, first=0, recent=0, kept=256, lens=512, ws=256,
+    (a,) = _with(kw, dict(w=256, dst=2048, ds=2, budgets=None, width=32, first=0, recent=0, kept=256, lens=512, ws=256,
                           nb=1 << 40, s=None))
     return lib.moe_kv_evict_e4m3(ctypes.byref(cache or _cache()), ctypes.byref(batch or _batch()), *a.values())
 
@@ -162,7 +162,7 @@ def test_tree_refusals(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(keep=None), 1), (dict(keep=258), 1), (dict(n=None), 1), (dict(n=255), 1), (dict(width=-1), 1),
-    (dict(lens=None), 1), (dict(lens=256), 1), (dict(ws=None), 3), (dict(nb=255), 3)])
+    (dict(lens=None), 1), (dict(lens=256), 1), (dict(n=512), 1), (dict(keep=512), 1), (dict(ws=None), 3), (dict(nb=255), 3)])
 def test_keep_refusals(lib, kw, status):
     assert _keep(lib, **kw) == status
 
@@ -179,13 +179,14 @@ def test_weights_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(w=None), 1), (dict(w=258), 1), (dict(dst=None), 1), (dict(ds=1), 1), (dict(width=0), 1), (dict(width=-3), 1),
     (dict(width=33), 1), (dict(first=-1), 1), (dict(recent=-1), 1), (dict(kept=None), 1), (dict(kept=257), 1),
-    (dict(budgets=258), 1), (dict(lens=None), 1), (dict(lens=256), 1), (dict(width=(1 << 30) + 1, ds=1 << 28), 2),
+    (dict(budgets=258), 1), (dict(lens=None), 1), (dict(lens=256), 1), (dict(budgets=512), 1), (dict(kept=512), 1), (dict(dst=1024), 1),
+    (dict(width=(1 << 30) + 1, ds=1 << 28), 2),
     (dict(width=1 << 30, ds=1 << 26, ), 0), (dict(ws=None), 3), (dict(nb=0), 3)])
 def test_evict_refusals(lib, kw, status):
     if status == 0:                  # more pages of copies than a grid has blocks
         assert _evict(lib, batch=_batch(B=60000), **kw) == 2
     else:
-        assert _evict(lib, **kw) == status
+        assert _evict(lib, batch=_batch(page_table=1024), **kw) == status
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -196,7 +197,8 @@ def test_evict_refusals(lib, kw, status):
     (dict(post=257), 1), (dict(pre=258, wd=2), 1), (dict(g=257), 1), (dict(gi=2), 1), (dict(gs=-1), 1),
     (dict(eps=-1.0), 1), (dict(eps=math.nan), 1), (dict(eps=math.inf), 1), (dict(scale=math.nan), 1), (dict(off=math.inf), 1),
     # outputs upon inputs of another stride or type, or upon one another
-    (dict(out=1024, os=72), 1), (dict(out=512), 1), (dict(n=512, nd=1), 1), (dict(n=1024, ns=128), 1), (dict(n=2048), 1)])
+    (dict(out=1024, os=72), 1), (dict(out=512), 1), (dict(n=512, nd=1), 1), (dict(n=1024, ns=128), 1), (dict(n=2048), 1),
+    (dict(g=2048), 1), (dict(g=4096), 1), (dict(pre=4096), 1), (dict(post=2048), 1)])
 def test_norm_refusals(lib, kw, status):
     a = dict(y=512, ys=64, yd=2, r=1024, rs=64, out=2048, os=64, rd=0, n=4096, ns=64, nd=0, T=2, H=64, post=256, pre=256,
              wd=0, g=256, gs=64, gi=1, gd=2, sig=0, scale=1.0, eps=1e-6, off=0.0, s=None)
