@@ -124,9 +124,9 @@ struct Shape {
   static constexpr int D = D_;
   static constexpr int kCtas = D == 256 ? 1 : 2;                       // per SM
   static constexpr int kGroups = MANY ? 2 : 3, kThreads = 32 * (4 * kGroups + 2);
-  static constexpr int kRows = MANY ? 128 : D == 256 ? 32 : 16;        // of a block
+  static constexpr int kRows = MANY ? (D == 64 ? 256 : 128) : D == 256 ? 32 : 16;        // of a block
   static constexpr int kChunk = kRows < 64 ? kRows : 64;               // of a product
-  static constexpr int kSlots = D == 64 ? 6 : D == 256 ? 3 : MANY ? 2 : 6, kHeads = 6;
+  static constexpr int kSlots = D == 64 ? (MANY ? 4 : 6) : D == 256 ? 3 : MANY ? 2 : 6, kHeads = 6;
   // every group has slots of its own, so that a wait never mistakes a phase
   static constexpr int kOwn = kSlots / kGroups, kOwnHeads = kHeads / kGroups;
   static_assert(kSlots % kGroups == 0 && kHeads % kGroups == 0, "");

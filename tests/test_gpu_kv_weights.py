@@ -63,7 +63,8 @@ def test_single_tokens_over_ragged_lengths(D, page, heads, group, dtype):
     (256, 32, 1, 2, "bf16", [(10, 40), (200, 9)]),
     (128, 16, 1, 1, "bf16", [(5, 130)]),
     (128, 64, 1, 7, "f16", [(0, 129), (300, 64), (3, 1)]),
-    (64, 64, 2, 3, "bf16", [(77, 100), (0, 45), (1, 0), (9, 2)])])
+    (64, 64, 2, 3, "bf16", [(77, 100), (0, 45), (1, 0), (9, 2)]),
+    (64, 16, 1, 9, "f16", [(60, 61), (300, 29), (1300, 143), (5, 28)])])
 def test_several_new_tokens_are_causal(D, page, heads, group, dtype, pairs):
     check(np.random.default_rng(group + D), pairs, page, heads, group, D, dtype)
 
