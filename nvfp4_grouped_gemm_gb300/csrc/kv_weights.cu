@@ -119,14 +119,14 @@ __global__ void __launch_bounds__(32 * kPrepWarps) prepare_kernel(const __grid_c
   }
 }
 
-template <int D_, bool MANY>
+template <int D_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr int kCtas = D == 256 ? 1 : 2;                       // per SM
-  static constexpr int kGroups = MANY ? 2 : 3, kThreads = 32 * (4 * kGroups + 2);
-  static constexpr int kRows = MANY ? (D == 64 ? 256 : 128) : D == 256 ? 32 : 16;        // of a block
+  static constexpr int kGroups = D == 256 ? 3 : 2, kThreads = 32 * (4 * kGroups + 2);
+  static constexpr int kRows = D == 64 ? 256 : D == 128 ? 128 : 32;        // of a block
   static constexpr int kChunk = kRows < 64 ? kRows : 64;               // of a product
-  static constexpr int kSlots = D == 64 ? (MANY ? 4 : 6) : D == 256 ? 3 : MANY ? 2 : 6, kHeads = 6;
+  static constexpr int kSlots = D == 64 ? 4 : D == 128 ? 2 : 3, kHeads = 6;
   // every group has slots of its own, so that a wait never mistakes a phase
   static constexpr int kOwn = kSlots / kGroups, kOwnHeads = kHeads / kGroups;
   static_assert(kSlots % kGroups == 0 && kHeads % kGroups == 0, "");
@@ -187,10 +187,10 @@ __device__ __forceinline__ float load_plain(const float* at) {
   return v;
 }
 
-template <int D, bool MANY>
-__global__ void __launch_bounds__(Shape<D, MANY>::kThreads, Shape<D, MANY>::kCtas)
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kCtas)
 weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CUtensorMap kmap) {
-  using S = Shape<D, MANY>;
+  using S = Shape<D>;
   constexpr int kThreads = S::kThreads, G = S::kGroups;
   extern __shared__ char smem_raw[];
   __shared__ uint64_t s_kfull[S::kSlots], s_kempty[S::kSlots], s_afull[G], s_sfull[G], s_sempty[G];
@@ -550,16 +550,16 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kCols));
 }
 
-template <int D, bool MANY>
+template <int D>
 cudaError_t launch_main(const WeightsArgs& a, cudaStream_t s) {
-  using S = Shape<D, MANY>;
+  using S = Shape<D>;
   CUtensorMap map;
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.c.kv_heads * a.c.page_size, (uint64_t)a.c.num_pages};
   const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.c.page_stride};
   const uint32_t box[3] = {(uint32_t)S::kRowB, (uint32_t)a.c.page_size, 1};
   if (!make_map3(&map, a.c.k_codes, dims, strides, box, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto kern = weights_kernel<D, MANY>;
+  auto kern = weights_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(S::kCtas * num_sms()), dim3(S::kThreads), S::kSmem, s, a, map);
@@ -574,11 +574,7 @@ cudaError_t launch_dim(const WeightsArgs& a, cudaStream_t s) {
   prepare_kernel<D><<<dim3((unsigned)a.b.B, (unsigned)(y < most ? y : most)), 32 * kPrepWarps, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // Few rows per sequence, as far as the sizes tell: a deeper ring instead of room for rows.
-  if constexpr (D <= 128) {
-    if ((long long)a.T * group > 16LL * a.b.B) return launch_main<D, true>(a, s);
-  }
-  return launch_main<D, false>(a, s);
+  return launch_main<D>(a, s);
 }
 
 }  // namespace
