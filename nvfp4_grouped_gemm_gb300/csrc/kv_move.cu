@@ -185,7 +185,7 @@ __device__ __forceinline__ int4 four_of_rank(const int* p, int rank) {
 
 // A cluster of `size` CTAs per (sequence, key head), each with a run of the candidates.
 __global__ void __launch_bounds__(kSelThreads, 4) select_kernel(const __grid_constant__ EvictArgs a, int size) {
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ __align__(16) int s_hist[2][kBins];             // in turn, so that others may still read the one before
   __shared__ int s_warp[kSelWarps], s_warp2[kSelWarps], s_all[2];
   __shared__ uint32_t s_prefix;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) select_kernel(const __grid_con
     for (int x = 0; x < kBatch; ++x) {
       const int j = lo + i + x * kSelThreads;
       bad |= !known(page[x]);
-      k[x] = load_ahead(a.w + ((int64_t)page[x] * heads + h) * P + (j & (P - 1)),
+      k[x] = load_ahead(a.w + (int64_t)page[x] * (heads * P) + (h * P + (j & (P - 1))),
                         i + x * kSelThreads < N && known(page[x]), 0x7fc00000u);
     }
 #pragma unroll
@@ -245,7 +245,14 @@ __global__ void __launch_bounds__(kSelThreads, 4) select_kernel(const __grid_con
   for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0;
   __syncthreads();
   auto each_key = [&](auto&& take) {           // take(key, there) by whole warps
-    for (int i0 = 0; i0 < held; i0 += kSelThreads) take(i0 + tid < held ? s_keys[i0 + tid] : 0u, i0 + tid < held);
+    for (int i0 = 0; i0 < held; i0 += 4 * kSelThreads) {
+      const int i = i0 + 4 * tid;
+      const uint4 k = i < held ? *reinterpret_cast<const uint4*>(s_keys + i) : make_uint4(0, 0, 0, 0);
+      take(k.x, i < held);
+      take(k.y, i + 1 < held);
+      take(k.z, i + 2 < held);
+      take(k.w, i + 3 < held);
+    }
     for (int i0 = held / (kSelThreads * kBatch) * (kSelThreads * kBatch); held < N && i0 < N; i0 += kSelThreads * kBatch) {
       uint32_t k[kBatch];
       load_keys(i0 + tid, k);
@@ -267,16 +274,14 @@ __global__ void __launch_bounds__(kSelThreads, 4) select_kernel(const __grid_con
     shift -= bits;
     each_key([&](uint32_t k, bool there) {
       const bool mine = there && (pass == 0 || (k >> (shift + bits)) == prefix);
-      const uint32_t any = __ballot_sync(0xffffffffu, mine);
-      if (any == 0) return;
-      const uint32_t bin = mine ? (k >> shift) & ((1u << bits) - 1) : 0xffffffffu;
-      // the lanes that share the first one's bin add together: weights that are all alike (0) would
-      // otherwise meet at one address
-      const int lead = __ffs(any) - 1;
-      const uint32_t led = __shfl_sync(0xffffffffu, bin, lead);
-      const uint32_t same = __ballot_sync(0xffffffffu, mine && bin == led);
-      if (lane == lead) atomicAdd(&hist[bin], __popc(same));
-      else if (mine && !(same >> lane & 1)) atomicAdd(&hist[bin], 1);
+      const uint32_t bin = (k >> shift) & ((1u << bits) - 1);
+      // weights that are all alike (0) would otherwise meet at one address
+      const uint32_t led = __shfl_sync(0xffffffffu, bin, 0);
+      if (__all_sync(0xffffffffu, mine && bin == led)) {
+        if (lane == 0) atomicAdd(&hist[bin], 32);
+      } else if (mine) {
+        atomicAdd(&hist[bin], 1);
+      }
     });
     if (size > 1) cluster_sync();
     else __syncthreads();
@@ -323,12 +328,12 @@ __global__ void __launch_bounds__(kSelThreads, 4) select_kernel(const __grid_con
     return known(page) ? weight_key(a.w[((int64_t)page * heads + h) * P + (j & (P - 1))]) : 0u;
   };
   int above = 0, equal = 0;
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const bool in = i0 + lane < r1;
-    const uint32_t k = in ? key(i0 + lane) : 0;
-    above += __popc(__ballot_sync(0xffffffffu, in && k > prefix));
-    equal += __popc(__ballot_sync(0xffffffffu, in && k == prefix));
+  for (int i = r0 + lane; i < r1; i += 32) {
+    const uint32_t k = key(i);
+    above += k > prefix, equal += k == prefix;
   }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) s_warp[warp] = above, s_warp2[warp] = equal;
   __syncthreads();
   int at = 0, eq = 0;                          // kept, equal before this warp's run
