@@ -206,7 +206,7 @@ size_t moe_kv_keep_workspace_bytes(void);
  * rescaled by old / new and rounded again to nearest even, in all slots of such a page. A token
  * from or into a page out of range stays (MOE_DEVERR_PAGE). No two sequences may have a page in
  * common that holds new tokens. A sequence without a valid start keeps its length.
- *   keep i32 [B][width] (may be NULL if width is 0)  n_keep i32 [B]  new_lens i32 [B], none of
+ *   keep i32 [B][width] (may be NULL if width is 0; width at most 2^30)  n_keep i32 [B]  new_lens i32 [B], none of
  *   the arrays that are read (the batch's seq_lens, n_keep) */
 moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch,
                             const int32_t* keep, const int32_t* n_keep, int32_t width,
@@ -271,7 +271,7 @@ moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* bat
  *   weights                   weight_dtype [H]
  *   gate                      gate_dtype, element (t, i) at t * gate_stride + i * gate_inner,
  *                             gate_inner 0 or 1, gate_stride 0 for one row that all share
- * H at most 32768; any alignment of the types (16-byte aligned rows and H a multiple of 8 are the
+ * H at most 32768, T at most 2^30; any alignment of the types (16-byte aligned rows and H a multiple of 8 are the
  * fast form). Takes no workspace. */
 moe_status moe_residual_norm(const void* y, int64_t y_stride, int32_t y_dtype, const void* residual,
                              int64_t residual_stride, void* out, int64_t out_stride,

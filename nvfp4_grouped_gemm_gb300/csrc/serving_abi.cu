@@ -189,7 +189,7 @@ moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batc
   // blocks of other heads read these while a block writes new_lens
   if (new_lens == batch->seq_lens || new_lens == batch->q_offsets || new_lens == n_keep || new_lens == keep)
     return MOE_ERR_INVALID_ARG;
-  if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30) || width > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, moe_kv_keep_workspace_bytes())) != MOE_OK) return st;
   KeepArgs a = {};
   a.c = *cache;
@@ -300,7 +300,7 @@ moe_status moe_residual_norm(const void* y, int64_t y_stride, int32_t y_dtype, c
   if (pre_weight && !normed) return MOE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f && eps < INFINITY) || !isfinite(scale) || !isfinite(weight_offset)) return MOE_ERR_INVALID_ARG;
   if (gate && (gate_inner < 0 || gate_inner > 1 || gate_stride < 0)) return MOE_ERR_INVALID_ARG;
-  if (H > 32768) return MOE_ERR_UNSUPPORTED;
+  if (H > 32768 || T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (!aligned(residual, size(residual_dtype)) || !aligned(out, size(residual_dtype)) ||
       (y && !aligned(y, size(y_dtype))) || (normed && !aligned(normed, size(normed_dtype))) ||
       !aligned(post_weight, size(weight_dtype)) || !aligned(pre_weight, size(weight_dtype)) ||

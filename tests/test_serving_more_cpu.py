@@ -161,7 +161,7 @@ def test_tree_refusals(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(keep=None), 1), (dict(keep=258), 1), (dict(n=None), 1), (dict(n=255), 1), (dict(width=-1), 1),
+    (dict(keep=None), 1), (dict(keep=258), 1), (dict(n=None), 1), (dict(n=255), 1), (dict(width=-1), 1), (dict(width=(1 << 30) + 1), 2),
     (dict(lens=None), 1), (dict(lens=256), 1), (dict(n=512), 1), (dict(keep=512), 1), (dict(ws=None), 3), (dict(nb=255), 3)])
 def test_keep_refusals(lib, kw, status):
     assert _keep(lib, **kw) == status
@@ -190,7 +190,7 @@ def test_evict_refusals(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(T=0), 1), (dict(H=0), 1), (dict(H=32769, ys=1 << 20, rs=1 << 20, os=1 << 20, ns=1 << 20), 2), (dict(r=None), 1),
+    (dict(T=0), 1), (dict(T=(1 << 30) + 1), 2), (dict(H=0), 1), (dict(H=32769, ys=1 << 20, rs=1 << 20, os=1 << 20, ns=1 << 20), 2), (dict(r=None), 1),
     (dict(r=257), 1), (dict(y=257), 1), (dict(y=258, yd=2), 1), (dict(out=None, n=None), 1), (dict(out=None, n=None, pre=None), 1),
     (dict(yd=3), 1), (dict(rd=-1), 1), (dict(nd=5), 1), (dict(wd=7), 1), (dict(gd=4), 1), (dict(ys=63), 1), (dict(rs=63), 1),
     (dict(os=63), 1), (dict(ns=0), 1), (dict(y=None), 1), (dict(y=None, post=None), 1), (dict(n=None), 1),
