@@ -446,15 +446,35 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
   // This CTA's piece of the line.
-  auto line_of = [&](const Seq& q) { return (long long)(q.steps + kSegmentCost) * q.blocks * heads; };
+  // Trees, few segments: each is made up to whole pieces of the least length, so that no CTA has two.
+  // (5 trees of 2 nodes, 2 key heads: FIGURES)
+  constexpr int kLeast = kWarps + kSegmentCost;
+  bool whole = false;
+  auto length_of = [&](const Seq& q) {
+    const int length = q.steps + kSegmentCost;
+    return TREE && whole ? (length + kLeast - 1) / kLeast * kLeast : length;
+  };
+  auto line_of = [&](const Seq& q) { return (long long)length_of(q) * q.blocks * heads; };
   long long total = 0, mine = 0, at = 0;
   for (int b0 = 0; b0 < a.b.B; b0 += kThreads) {
     mine = 0;
     if (b0 + tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, b0 + tid, group, blockIdx.x == 0 ? err : nullptr));
     total += block_scan<kWarps>(mine, s_sum, &at);
   }
+  if (TREE && a.b.B <= kThreads && total <= (long long)gridDim.x * kLeast) {
+    whole = true;
+    mine = 0;
+    if (tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, tid, group, nullptr));
+    total = block_scan<kWarps>(mine, s_sum, &at);
+    if (total > (long long)gridDim.x * kLeast) {
+      whole = false;
+      mine = 0;
+      if (tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, tid, group, nullptr));
+      total = block_scan<kWarps>(mine, s_sum, &at);
+    }
+  }
   long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kWarps + kSegmentCost) per = kWarps + kSegmentCost;
+  if (per < kLeast) per = kLeast;
   const long long begin = per * blockIdx.x, end = min(begin + per, total);
   if (begin >= end) {
     pdl_wait();
@@ -500,13 +520,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       first += line_of(q);
       q = read_seq<S, TREE>(a, ++b, group, nullptr);
     }
-    const int length = q.steps + kSegmentCost;
+    const int length = length_of(q);
     const long long in_seq = pos - first;
     const int seg = (int)(in_seq / length);
     const long long seg_at = first + (long long)seg * length;
     const int st0 = max(0, (int)(pos - seg_at) - kSegmentCost);
-    const int st1 = (int)min((long long)length, end - seg_at) - kSegmentCost;
-    pos = seg_at + st1 + kSegmentCost;
+    const int upto = (int)min((long long)length, end - seg_at);
+    const int st1 = min(upto - kSegmentCost, q.steps);
+    pos = seg_at + upto;
     if (st1 <= st0) continue;                  // only the segment's fixed cost fell to this CTA
     const int head = seg / q.blocks, block = seg % q.blocks;
     const int R = min(S::kRows, q.n * group - block * S::kRows);
@@ -828,7 +849,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     }
     if (!(opens && closes)) {
       // the last piece of the segment to arrive joins all of them
-      const int c0 = (int)((seg_at + kSegmentCost) / per), c1 = (int)((seg_at + length - 1) / per);
+      const int c0 = (int)((seg_at + kSegmentCost) / per), c1 = (int)((seg_at + q.steps + kSegmentCost - 1) / per);
       const int np = c1 - c0 + 1;
       __syncthreads();                         // the whole CTA's rows, then one thread's release
       if (tid == 0) {
@@ -966,7 +987,12 @@ size_t attention_ws_bytes(int q_heads, int kv_heads, int head_dim) {
 cudaError_t launch_attention(const AttentionArgs& args, cudaStream_t s) {
   AttentionArgs a = args;
   a.max_rows = kAllRows;
-  if (a.c.head_dim <= 128 && a.T > a.b.B && (long long)a.T * (a.q_heads / a.c.kv_heads) >= kPromptRows) {
+  const long long rows = (long long)a.T * (a.q_heads / a.c.kv_heads);
+  // Trees whose every segment, in tiles of 8 rows over the whole table, would find a CTA with its least
+  // piece have nothing to win in the other form, whose launch alone takes 5 us.
+  const bool small = a.tree && (rows / 8 + a.b.B) * a.c.kv_heads * ((long long)a.b.max_pages * a.c.page_size / 32 + kSegmentCost) <=
+                                   32LL * num_sms();
+  if (a.c.head_dim <= 128 && a.T > a.b.B && rows >= kPromptRows && !small) {
     // some sequence may have that many rows; which ones have is settled on the GPU
     const bool all = a.b.B == 1;
     const cudaError_t e = launch_prompt_attention(a, all ? 1 : kPromptRows, few_rows_ws_bytes(a.c.head_dim), s);
