@@ -30,7 +30,7 @@
 // For trees of drafted tokens (moe_attention_tree_e4m3) the same kernel asks a row's bits instead of
 // its place in the steps that hold new tokens or a window's edge; the bits, cut to what the window
 // leaves, lie in shared memory. One tree of 8 nodes after 1000 tokens, 16 query and 4 key
-// heads of 128: 16.5 us; 32 of 6 to 48 nodes after 500 to 12000, 32 and 8 heads: 165 us, 115 of them here
+// heads of 128: 15.9 us; 32 of 6 to 48 nodes after 500 to 12000, 32 and 8 heads: 165 us, 115 of them here
 // (the sequences below 73 rows) and the rest in the other form.
 //
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
@@ -446,8 +446,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
   // This CTA's piece of the line.
-  // Trees, few segments: each is made up to whole pieces of the least length, so that no CTA has two.
-  // (5 trees of 2 nodes, 2 key heads: FIGURES)
+  // Trees, few segments: each is made up to whole pieces of the least length, so that no CTA has two
+  // one after the other. 5 trees of 2 nodes, 14 query and 2 key heads of 64: 9.5 us against 15.6; one of
+  // 16 after 3000 tokens, 16 and 4 heads of 128: 21.6 against 26.0.
   constexpr int kLeast = kWarps + kSegmentCost;
   bool whole = false;
   auto length_of = [&](const Seq& q) {
@@ -461,7 +462,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     if (b0 + tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, b0 + tid, group, blockIdx.x == 0 ? err : nullptr));
     total += block_scan<kWarps>(mine, s_sum, &at);
   }
-  if (TREE && a.b.B <= kThreads && total <= (long long)gridDim.x * kLeast) {
+  if (TREE && a.b.B <= kThreads && total > 0 && total <= (long long)gridDim.x * kLeast) {
     whole = true;
     mine = 0;
     if (tid < a.b.B) mine = line_of(read_seq<S, TREE>(a, tid, group, nullptr));
@@ -988,10 +989,13 @@ cudaError_t launch_attention(const AttentionArgs& args, cudaStream_t s) {
   AttentionArgs a = args;
   a.max_rows = kAllRows;
   const long long rows = (long long)a.T * (a.q_heads / a.c.kv_heads);
-  // Trees whose every segment, in tiles of 8 rows over the whole table, would find a CTA with its least
-  // piece have nothing to win in the other form, whose launch alone takes 5 us.
-  const bool small = a.tree && (rows / 8 + a.b.B) * a.c.kv_heads * ((long long)a.b.max_pages * a.c.page_size / 32 + kSegmentCost) <=
-                                   32LL * num_sms();
+  // The other form's launch takes 5 us even where it finds no rows, and its start more than a short
+  // segment is worth. For trees, steps of all tiles of 8 rows over the whole table say when that counts;
+  // with and without this rule: 3 trees of 32 nodes after 300 tokens, 16 query and 4 key heads of 128, 22.0
+  // and 28.2 us, one of 64 after 8000 40.2 and 49.9; with twice the limit 8 of 64 after 1000, just beyond
+  // it, take 53.5 instead of 40.9.
+  const long long steps = (rows / 8 + a.b.B) * a.c.kv_heads * ((long long)a.b.max_pages * a.c.page_size / 32 + kSegmentCost);
+  const bool small = a.tree && steps <= 256LL * num_sms();
   if (a.c.head_dim <= 128 && a.T > a.b.B && rows >= kPromptRows && !small) {
     // some sequence may have that many rows; which ones have is settled on the GPU
     const bool all = a.b.B == 1;

@@ -53,22 +53,25 @@ def check(rng, pairs, page, heads, group, D, dtype, window=0, make=tree_bits, wo
     q = activations(rng, (batch.T, heads * group, D), dtype)
     want, wl, eo, el = oracle.attention(q.double().numpy(), *planes, batch.offsets, batch.lens, batch.table,
                                         D ** -0.5, window, seen_bits)
-    out = torch.full((batch.T, heads * group, D), float("nan"), dtype=q.dtype, device="cuda")
-    lse = torch.full((batch.T, heads * group), float("nan"), device="cuda")
-    ws = zeros_ws(moe.attention_workspace_bytes(heads * group, heads, D))
-    moe.moe_attention_tree_e4m3(q.cuda(), device_cache(planes), batch.device(), mask, out, ws, window=window, lse=lse)
-    assert moe.get_device_error(ws) == err
-    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
-    rel, floor = ROUND[dtype]
-    tol = eo + rel * (np.abs(want) + eo) + floor
-    off = np.abs(got - want)
-    ok = (off <= tol) | (np.isnan(got) & np.isnan(want))
-    assert ok.all(), float(np.nanmax(off / tol))
-    seen = wl > -np.inf
-    fine = np.isfinite(wl)
-    assert np.array_equal(np.isfinite(gl), fine) and np.all(gl[wl == -np.inf] == -np.inf)
-    assert np.all(np.abs(gl[fine] - wl[fine]) <= el[fine] + 1e-6)
-    assert np.all(got[~seen & ~np.isnan(wl)] == 0)
+    # a table of its own width, and one so wide that many rows take the form for many rows
+    for cols in (0, (1 << 20) // page):
+        batch.table = np.pad(batch.table, ((0, 0), (0, cols)), constant_values=-7)
+        out = torch.full((batch.T, heads * group, D), float("nan"), dtype=q.dtype, device="cuda")
+        lse = torch.full((batch.T, heads * group), float("nan"), device="cuda")
+        ws = zeros_ws(moe.attention_workspace_bytes(heads * group, heads, D))
+        moe.moe_attention_tree_e4m3(q.cuda(), device_cache(planes), batch.device(), mask, out, ws, window=window, lse=lse)
+        assert moe.get_device_error(ws) == err
+        got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        rel, floor = ROUND[dtype]
+        tol = eo + rel * (np.abs(want) + eo) + floor
+        off = np.abs(got - want)
+        ok = (off <= tol) | (np.isnan(got) & np.isnan(want))
+        assert ok.all(), float(np.nanmax(off / tol))
+        seen = wl > -np.inf
+        fine = np.isfinite(wl)
+        assert np.array_equal(np.isfinite(gl), fine) and np.all(gl[wl == -np.inf] == -np.inf)
+        assert np.all(np.abs(gl[fine] - wl[fine]) <= el[fine] + 1e-6)
+        assert np.all(got[~seen & ~np.isnan(wl)] == 0)
     return out, lse
 
 
@@ -82,7 +85,10 @@ SHAPES = [(128, 64, 2, 4, "bf16", [(100, 8), (0, 3), (511, 5), (64, 16)]),
           (128, 128, 1, 7, "f16", [(1000, 37), (0, 150)]),
           (256, 16, 2, 7, "f16", [(1, 100), (129, 33)]),
           (64, 32, 1, 1, "bf16", [(1025, 256)]),
-          (128, 32, 3, 2, "f16", [(95, 1), (0, 1), (31, 2), (63, 32), (62, 33)])]
+          (128, 32, 3, 2, "f16", [(95, 1), (0, 1), (31, 2), (63, 32), (62, 33)]),
+          # more sequences than a block has threads, and segments that reach over several pieces
+          (64, 16, 1, 2, "bf16", [(i % 40, 1 + i % 3) for i in range(140)]),
+          (128, 64, 1, 2, "bf16", [(2500, 9), (0, 2), (1500, 4)])]
 
 
 @pytest.mark.parametrize("D,page,heads,group,dtype,pairs", SHAPES)
