@@ -12,7 +12,7 @@
 // of 4096 16.5; with the threads of a block, not of a warp, on neighbouring values 32.2).
 //
 // Bound by bytes for many rows. 4096 x 4096, y f32, residual and outputs bf16, a gate per row:
-// 31.7 us, 5.3 TB/s (0.78 of the copy rate); one row of 2560: 3.6 us in a graph, which is the launch
+// 32.1 us, 5.2 TB/s (0.77 of the copy rate); one row of 2560: 2.8 us in a graph, which is the launch
 // and one chain of loads and two sums. Measured against this at 4096 x 4096: rows ahead in shared
 // memory (cp.async) instead of in registers 36.6 us (one) and 36.7 us (two); rows and their gates read
 // only when they are taken 38.9; 40 registers per thread and half again as many threads 44.6.

@@ -11,6 +11,7 @@ import torch
 import nvfp4_grouped_gemm_gb300 as moe
 from oracle import serving as oracle
 from oracle.nvfp4 import dequant
+from serving_util import Batch, activations, cache_planes, device_cache, zeros_ws
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -107,3 +108,45 @@ def test_the_cache_holds_what_the_text_says(example, page, budget):
             total = w[table[b, j // page], :, j % page].sum(0)
             rows = server.lens[b]
             assert np.all(np.abs(total - rows * group) <= rows * group * 2.0 ** -14)
+
+
+def test_a_step_on_another_stream():
+    """The operators in turn on a stream of their own give what they give on the current one, also behind
+    work that is still queued there when they are called."""
+    rng = np.random.default_rng(41)
+    batch, heads, page, D = Batch(rng, [(200, 12), (37, 5), (0, 9)], 16), 2, 16, 64
+    planes = cache_planes(rng, batch.num_pages + 30, heads, page, D)
+    q = activations(rng, (batch.T, heads * 2, D), "bf16").cuda()
+    bits = [[(2 << i) - 1 for i in range(n)] for _, n in batch.pairs]
+    mask = torch.tensor([[v] for t in bits for v in t], dtype=torch.int32).cuda()
+    keep = torch.tensor([[0, 2, 5], [1, 2, 4], [0, 3, 8]], dtype=torch.int32).cuda()
+    new_table = torch.arange(batch.num_pages, batch.num_pages + 30, dtype=torch.int32).view(3, 10).cuda()
+
+    def step(stream):
+        cache, dev = device_cache(planes), batch.device()
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        weights = torch.rand(batch.num_pages + 30, heads, page, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+        normed = torch.empty_like(q.flatten(1))
+        lens, cut = torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+        kept, three = torch.empty(3, heads, 40, dtype=torch.int32, device="cuda"), torch.full_like(lens, 3)
+        size = max(moe.attention_workspace_bytes(heads * 2, heads, D), moe.kv_keep_workspace_bytes(),
+                   moe.kv_weights_workspace_bytes(batch.T, heads * 2, heads, D), moe.kv_evict_workspace_bytes(3, heads))
+        spaces = [zeros_ws(size) for _ in range(4)]
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                busy = torch.ones(4096, 4096, device="cuda")
+                for _ in range(8):
+                    busy = busy @ busy * 2.0 ** -12
+        moe.moe_attention_tree_e4m3(q, cache, dev, mask, out, spaces[0], lse=lse, stream=stream)
+        moe.moe_kv_weights_e4m3(q, lse, cache, dev, weights, spaces[1], decay=0.5, stream=stream)
+        moe.moe_residual_norm(out.flatten(1), q.flatten(1), normed=normed, stream=stream)
+        moe.moe_kv_keep_e4m3(cache, dev, keep, three, lens, spaces[2], stream=stream)
+        after = moe.SeqBatch(dev.q_offsets, lens, dev.page_table)
+        moe.moe_kv_evict_e4m3(cache, after, weights, new_table, kept, cut, spaces[3], first=2, recent=7, stream=stream)
+        torch.cuda.synchronize()
+        assert all(moe.get_device_error(ws) == 0 for ws in spaces)
+        return [out, lse, normed, weights, lens, kept, cut, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales]
+
+    for a, b in zip(step(None), step(torch.cuda.Stream())):
+        assert torch.equal(a, b)
