@@ -365,6 +365,9 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
         const bool mine = j < run.len && at_ >= 0;
         const uint64_t ff = pair(f, f);
         uint64_t acc[2] = {0, 0};
+        // Token i sees key j if i - since, as a number without sign, is below `span`: no token before
+        // the key is, and no sum is made that a large window could take past 32 bits.
+        const uint32_t since = (uint32_t)(j - run.start), span = a.window > 0 ? a.window : 0x7fffffffu;
         // the weights of eight rows
         auto add8 = [&](const float* v, int r, auto hides) {
 #pragma unroll
@@ -375,10 +378,8 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
             e0 = exp2_approx(e0), e1 = exp2_approx(e1);
             if (decltype(hides)::value) {
               const int2 i = *reinterpret_cast<const int2*>(tokens + r + x);
-              // the tokens that see key j
-              const int from = max(j - run.start, 0), upto = a.window > 0 ? j - run.start + a.window : 0x7fffffff;
-              e0 = i.x >= from && i.x < upto ? e0 : 0.0f;
-              e1 = i.y >= from && i.y < upto ? e1 : 0.0f;
+              e0 = i.x - since < span ? e0 : 0.0f;
+              e1 = i.y - since < span ? e1 : 0.0f;
             }
             acc[x >> 1 & 1] = add2(acc[x >> 1 & 1], pair(e0, e1));
           }

@@ -171,3 +171,15 @@ def test_a_graph_with_other_lengths():
     want, bound = oracle.kv_weights(q.double().numpy(), lse2.astype(np.float32).astype(np.float64), w, planes[0],
                                     planes[1], batch.offsets, lens, batch.table, 128 ** -0.5)
     assert np.all(np.abs(wd.cpu().numpy() - want) <= bound)
+
+
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 2, (1 << 31) - 1])
+@pytest.mark.parametrize("D,group,pairs", [(128, 4, [(100, 40), (0, 5), (700, 1)]), (64, 3, [(0, 300), (130, 2)]),
+                                           (256, 2, [(9, 70)])])
+def test_a_window_past_every_place_hides_nothing(window, D, group, pairs):
+    """The largest windows, which end past the largest place, give what no window gives."""
+    rng = np.random.default_rng(19)
+    batch, planes, q, lse, w = setup(rng, pairs, 16, 2, group, D, "bf16")
+    none = call(batch, planes, q, lse, w, 0, 0.5)[0]
+    assert torch.equal(call(batch, planes, q, lse, w, window, 0.5)[0], none)
+    check(np.random.default_rng(20), pairs, 16, 2, group, D, "bf16", window=window, decay=0.5)
