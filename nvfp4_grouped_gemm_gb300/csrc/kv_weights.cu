@@ -435,14 +435,14 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
     int lt = 0;                                // next tile of lr
     auto ask_pages = [&] {
       while (lt >= lr.t1) {
-        if (!next_run(look, lr, a, group, S::kRows, G)) return -2;
+        if (!next_run(look, lr, a, group, S::kRows, G)) return -1;
         lt = max(lr.t0, lr.first);
       }
       const int t = lt + which, j = t * kTile + slot_page * P;
       const bool in = which < batch && t < lr.t1 && j < lr.len;
       const int page = (int)load_ahead(a.b.page_table + (int64_t)lr.b * a.b.table_stride + (j >> log_p), in, 0xffffffffu);
       lt += batch;
-      return in ? page : -2;                   // (-2: no such page is asked for)
+      return page;                             // (-1 where no page is asked for)
     };
     auto known = [&](int page) { return page >= 0 && page < a.c.num_pages; };
     uint32_t count[G] = {};                    // tiles of each group
@@ -524,7 +524,7 @@ weights_kernel(const __grid_constant__ WeightsArgs a, const __grid_constant__ CU
           begun = true;
           if (in_batch == min(1, min(batch, run.t1 - (t - in_batch)) - 1)) scale_next = ask_scale(page_next, h_next);
           const bool mine = which == in_batch, good = mine && known(page);
-          if (mine && !good && page != -2) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+          if (mine && !good && t * kTile + slot_page * P < run.len) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
           const bool had = good && run.block == 0 && a.decay != 0.0f && t * kTile + slot_page * P < run.start;
           const uint32_t olds = __popc(__ballot_sync(0xffffffffu, had));
           if (!(ok = wait_warp(&s_hempty[hb], (k / S::kOwnHeads & 1) ^ 1, abort_flag, err))) break;

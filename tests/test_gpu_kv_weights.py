@@ -183,3 +183,14 @@ def test_a_window_past_every_place_hides_nothing(window, D, group, pairs):
     none = call(batch, planes, q, lse, w, 0, 0.5)[0]
     assert torch.equal(call(batch, planes, q, lse, w, window, 0.5)[0], none)
     check(np.random.default_rng(20), pairs, 16, 2, group, D, "bf16", window=window, decay=0.5)
+
+
+@pytest.mark.parametrize("page", [-1, -2, -3, -(1 << 31), (1 << 31) - 1])
+@pytest.mark.parametrize("pairs", [[(100, 1), (40, 1)], [(300, 20), (40, 3)], [(2, 300), (40, 1)]])
+def test_every_page_out_of_range_is_reported(page, pairs):
+    rng = np.random.default_rng(21)
+
+    def edit(b):
+        b.table[0, 2] = page
+    check(rng, pairs, 16, 2, 2, 128, "bf16", edit=edit, err=moe.DEVERR_PAGE)
+    check(rng, pairs, 64, 1, 3, 64, "f16", edit=lambda b: b.table.__setitem__((0, 0), page), err=moe.DEVERR_PAGE)
