@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
   constexpr int kMostPages = kMoveThreads / 16, kInFlight = 8;
   __shared__ int64_t s_from[kMoveThreads], s_to[kMoveThreads];   // bytes into a plane (-1: nowhere)
   __shared__ float s_ratio[2][kMoveThreads];
-  __shared__ uint32_t s_top[2][kMostPages];
+  __shared__ uint32_t s_top[2][kMostPages], s_any[kMostPages];    // a page's largest scales; whether a token comes to it
   const int tid = threadIdx.x;
   const int P = a.c.page_size, log_p = 31 - __clz(P), D = a.c.head_dim, heads = a.c.kv_heads;
   const int blocks = (a.width + kMoveThreads - 1) / kMoveThreads;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
   const Share sh = share_of(a, b);
   const int i0 = blockIdx.x % blocks * kMoveThreads, i = i0 + tid;
   const int page = i < sh.keep ? a.dst_table[(int64_t)b * a.dst_stride + (i >> log_p)] : -1;
-  if (tid < kMostPages) s_top[0][tid] = s_top[1][tid] = 0;
+  if (tid < kMostPages) s_top[0][tid] = s_top[1][tid] = s_any[tid] = 0;
   pdl_wait();
   if (sh.alone || i0 >= sh.keep) return;
   const int count = min(kMoveThreads, sh.keep - i0);
@@ -425,15 +425,16 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
   if (good) {
     atomicMax(&s_top[0][tid >> log_p], __float_as_uint(sk));
     atomicMax(&s_top[1][tid >> log_p], __float_as_uint(sv));
+    s_any[tid >> log_p] = 1;
     a.w[((int64_t)page * heads + h) * P + (i & (P - 1))] = w;
   }
   __syncthreads();
   const float tk = __uint_as_float(s_top[0][tid >> log_p]), tv = __uint_as_float(s_top[1][tid >> log_p]);
   s_ratio[0][tid] = sk == tk ? 1.0f : sk / tk;
   s_ratio[1][tid] = sv == tv ? 1.0f : sv / tv;
-  if (tid < count && (tid & (P - 1)) == 0 && page >= 0 && page < a.c.num_pages) {
-    if (tk > 0.0f) a.c.k_scales[(int64_t)page * heads + h] = tk;
-    if (tv > 0.0f) a.c.v_scales[(int64_t)page * heads + h] = tv;
+  if (tid < count && (tid & (P - 1)) == 0 && s_any[tid >> log_p]) {      // (then the page is one of the cache's)
+    a.c.k_scales[(int64_t)page * heads + h] = tk;
+    a.c.v_scales[(int64_t)page * heads + h] = tv;
   }
   __syncthreads();
 #pragma unroll 1

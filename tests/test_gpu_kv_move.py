@@ -286,3 +286,34 @@ def test_repeated_calls_and_a_graph():
     torch.cuda.synchronize()
     for t, was in zip((cache.k_codes, cache.v_codes, cache.k_scales, weights, kept, new_lens), first):
         assert torch.equal(t, was)
+
+
+@pytest.mark.parametrize("page,D,heads", [(16, 64, 2), (64, 128, 1), (128, 256, 1)])
+def test_pages_copied_from_scales_of_zero(page, D, heads):
+    """A page of the copy has the largest of its tokens' scales, also where that is 0: what was 0 stays 0 on
+    pages whose scales were others before."""
+    rng = np.random.default_rng(29)
+    lens, budgets = [3 * page, 2 * page + 5, 2 * page], [2 * page + 3, 2 * page, page + 1]
+    batch = Batch(rng, [(n, 0) for n in lens], page, spare=12)
+    used = {int(v) for b, n in enumerate(lens) for v in batch.table[b, :-(-n // page)]}
+    dst = np.array([p for p in range(batch.num_pages) if p not in used][:9], np.int32).reshape(3, 3)
+    planes = loud(rng, cache_planes(rng, batch.num_pages, heads, page, D))
+    for c in (planes[0], planes[2]):                             # no sign to lose, no NaN
+        c &= 0x77
+    mine = batch.table[0, :3]
+    planes[1][mine] = planes[3][mine] = 0                        # all of the first sequence
+    planes[1][batch.table[1, 0]] = 0                             # a page of the second, of its keys only
+    w = weights_of(rng, (batch.num_pages, heads, page))
+    cache, weights = device_cache(planes), torch.from_numpy(w).cuda()
+    kept = torch.empty(3, heads, 2 * page + 3, dtype=torch.int32, device="cuda")
+    new_lens = torch.empty(3, dtype=torch.int32, device="cuda")
+    ws = zeros_ws(moe.kv_evict_workspace_bytes(3, heads))
+    moe.moe_kv_evict_e4m3(cache, batch.device(), weights, torch.from_numpy(dst).cuda(), kept, new_lens, ws,
+                          budgets=torch.tensor(budgets, dtype=torch.int32, device="cuda"), first=1, recent=3)
+    for b, n in enumerate(lens):
+        chosen = oracle.evict_choice(w, n, budgets[b], batch.table[b], 1, 3)
+        oracle.kv_evict_copy(planes[0], planes[1], None, chosen, batch.table[b], dst[b])
+        oracle.kv_evict_copy(planes[2], planes[3], None, chosen, batch.table[b], dst[b])
+    assert moe.get_device_error(ws) == 0
+    assert np.all(planes[1][dst[0]] == 0) and np.all(planes[3][dst[0]] == 0)
+    same_planes(cache, planes)
