@@ -11,11 +11,22 @@
 // and rows that are no whole 16-byte vectors are read value by value (2000 rows of 4095 in bf16 27.0 us,
 // of 4096 16.5; with the threads of a block, not of a warp, on neighbouring values 32.2).
 //
+// The row's factor meets y before the weight and the gate do, as the definition has it: y * weight * gate,
+// which could be made before the sum is known, may leave the range of f32 where the result is far from it
+// (an f32 gate of 1e30 beside y of 1e12). That costs a multiplication behind the sum, and a gate for
+// every value is held over it: instances with such gates keep the second norm's weights in shared memory,
+// so that no register spills (a spilled one waits for its load, and the row ahead with it: 36.0 us instead
+// of 31.6 at 4096 x 4096). 4096 x 4096 with a full gate 47.3 us where the product before the sum took
+// 45.0, a gate per channel 38.3 and 34.4, 1000 x 16384 without 49.4 and 46.9; a check per row whether the
+// product stays in range, with the definition's order behind it as a call, 43.9 where this takes 31.6.
+//
 // Bound by bytes for many rows. 4096 x 4096, y f32, residual and outputs bf16, a gate per row:
-// 32.1 us, 5.2 TB/s (0.77 of the copy rate); one row of 2560: 2.8 us in a graph, which is the launch
+// 31.6 us, 5.3 TB/s (0.78 of the copy rate); one row of 2560: 2.8 us in a graph, which is the launch
 // and one chain of loads and two sums. Measured against this at 4096 x 4096: rows ahead in shared
 // memory (cp.async) instead of in registers 36.6 us (one) and 36.7 us (two); rows and their gates read
 // only when they are taken 38.9; 40 registers per thread and half again as many threads 44.6.
+#include <type_traits>
+
 #include "serving.cuh"
 
 namespace moe {
@@ -181,11 +192,14 @@ __device__ __forceinline__ float block_sum(uint64_t pairs, float* s) {
 
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-template <int MOST, int V, bool VEC, bool Y32, bool R32>
+// GATES: there may be a gate for every value; then a row's gates are held over its sum, and the second
+// norm's weights in shared memory (a thread's own) instead of registers.
+template <int MOST, int V, bool VEC, bool Y32, bool R32, bool GATES>
 __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ __align__(16) float s_sum[2][32];
   constexpr int kY = Y32 ? 4 : 2, kR = R32 ? 4 : 2;
-  constexpr bool kHold = V == 1;
+  constexpr bool kHold = V == 1, kAside = kHold && GATES;
+  __shared__ ulonglong2 s_pre[2][kAside ? MOST : 1];
   const float each = 1.0f / (float)a.H;
   const char* y = static_cast<const char*>(a.y) + (int64_t)blockIdx.x * a.y_stride * kY;
   const char* res = static_cast<const char*>(a.residual) + (int64_t)blockIdx.x * a.residual_stride * kR;
@@ -218,7 +232,15 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_co
     return pack(f);
   };
   if (kHold && a.post) held[0] = weights(a.post, 0);
-  if (kHold && a.pre) held[1] = weights(a.pre, 0);
+  if (kHold && a.pre) {
+    const Eight w = weights(a.pre, 0);
+    if constexpr (kAside) {
+      s_pre[0][threadIdx.x] = make_ulonglong2(w.p[0], w.p[1]);
+      s_pre[1][threadIdx.x] = make_ulonglong2(w.p[2], w.p[3]);
+    } else {
+      held[1] = w;
+    }
+  }
   if (blockDim.x > 32) __syncthreads();
 
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -229,7 +251,15 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_co
       const float g = gate_size == 4 ? __uint_as_float(gate_bits) : scalar_of(gate_bits, a.gate_dtype);
       k *= a.sigmoid ? sigmoid(g) : g;
     }
-    Eight z[V];
+    const bool gates = GATES && a.gate && a.gate_inner;
+    auto gate_of = [&](int v) {                // scale times the gate's values
+      float f[8];
+      operand<VEC>(gate, a.gate_dtype, v, a.H, f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) f[x] = a.scale * (a.sigmoid ? sigmoid(f[x]) : f[x]);
+      return pack(f);
+    };
+    Eight z[V], g_held = {};
     uint64_t sum = 0;
     if (a.y) {
 #pragma unroll
@@ -239,22 +269,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_co
         z[v] = pack(f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum = fma2(z[v].p[i], z[v].p[i], sum);
-        if (a.post) {                          // what does not need the sum, before it
-          const Eight w = kHold ? held[0] : weights(a.post, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[v].p[i] = mul2(z[v].p[i], w.p[i]);
-        }
-        if (a.gate && a.gate_inner) {
-          operand<VEC>(gate, a.gate_dtype, v, a.H, f);
-          if (a.sigmoid) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) f[x] = sigmoid(f[x]);
-          }
-          const Eight g = pack(f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[v].p[i] = mul2(z[v].p[i], g.p[i]);
-        }
       }
+      if (kHold && gates) g_held = gate_of(0);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -262,16 +278,32 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_co
       values_of<R32>(rw[v], a.residual_dtype, f);
       r[v] = pack(f);
     }
-    gate += gate_step;
+    const char* gate_next = gate + gate_step;
+    if (kHold) gate = gate_next;
     if (kHold && a.T - t > (int)gridDim.x) ask_rows();  // the next row, into registers that this one is done with
     if (a.y) {
-      if (a.post) k *= rsqrtf(fmaf(block_sum(sum, s_sum[0]), each, a.eps));
+      if (a.post) {
+        // y is normed before its weight and then the gate meet it: y * weight * gate, whose product needs
+        // no sum, may leave the range of f32 where none of these does
+        const float n = rsqrtf(fmaf(block_sum(sum, s_sum[0]), each, a.eps));
+        const uint64_t nn = pair(n, n);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const Eight w = kHold ? held[0] : weights(a.post, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[v].p[i] = mul2(mul2(z[v].p[i], nn), w.p[i]);
+        }
+      }
       const uint64_t kk = pair(k, k);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        Eight g;
+        if (gates) g = kHold ? g_held : gate_of(v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[v].p[i] = fma2(z[v].p[i], kk, r[v].p[i]);
+        for (int i = 0; i < 4; ++i) r[v].p[i] = fma2(z[v].p[i], gates ? g.p[i] : kk, r[v].p[i]);
+      }
     }
+    if (!kHold) gate = gate_next;
     if (a.normed) {
       sum = 0;
 #pragma unroll
@@ -298,7 +330,13 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < 4; ++i) e.p[i] = mul2(r[v].p[i], nn);
         if (a.pre) {
-          const Eight w = kHold ? held[1] : weights(a.pre, v);
+          Eight w;
+          if constexpr (kAside) {
+            const ulonglong2 x = s_pre[0][threadIdx.x], y = s_pre[1][threadIdx.x];
+            w = {{x.x, x.y, y.x, y.y}};
+          } else {
+            w = kHold ? held[1] : weights(a.pre, v);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) e.p[i] = mul2(e.p[i], w.p[i]);
         }
@@ -328,10 +366,15 @@ cudaError_t launch_size(const NormArgs& a, cudaStream_t s) {
   const int threads = V > 1 ? MOST : (a.H + 255) / 256 * 32;
   const long long most = (long long)num_sms() * (1024 / threads);
   const unsigned grid = (unsigned)(a.T < most ? a.T : most);
-  if (y32 && r32) norm_kernel<MOST, V, VEC, true, true><<<grid, threads, 0, s>>>(a);
-  else if (y32) norm_kernel<MOST, V, VEC, true, false><<<grid, threads, 0, s>>>(a);
-  else if (r32) norm_kernel<MOST, V, VEC, false, true><<<grid, threads, 0, s>>>(a);
-  else norm_kernel<MOST, V, VEC, false, false><<<grid, threads, 0, s>>>(a);
+  auto launch = [&](auto gates) {
+    constexpr bool G = decltype(gates)::value;
+    if (y32 && r32) norm_kernel<MOST, V, VEC, true, true, G><<<grid, threads, 0, s>>>(a);
+    else if (y32) norm_kernel<MOST, V, VEC, true, false, G><<<grid, threads, 0, s>>>(a);
+    else if (r32) norm_kernel<MOST, V, VEC, false, true, G><<<grid, threads, 0, s>>>(a);
+    else norm_kernel<MOST, V, VEC, false, false, G><<<grid, threads, 0, s>>>(a);
+  };
+  if (V > 1 || a.gate_inner) launch(std::true_type{});
+  else launch(std::integral_constant<bool, (V > 1)>{});
   return cudaGetLastError();
 }
 

@@ -160,3 +160,25 @@ def test_another_stream_and_a_graph():
     r, n, er, en = want(s)
     close(s["out"], r, er, "bf16")
     close(s["normed"], n, en, "bf16")
+
+
+@pytest.mark.parametrize("H", [512, 513, 9000, 20000])
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+def test_gates_and_weights_far_from_one(H, gate):
+    """y is normed before its weight, the gate and the scale meet it: none of the products on the way leaves
+    the range of f32 where the result does not."""
+    rng = np.random.default_rng(H)
+    for y_amp, w_amp, g_amp, scale in ((1e12, 1.0, 1e30, 1.0), (1e12, 1e30, 1e-25, 1.0), (1e-12, 1.0, 1e-30, 1e30),
+                                       (1e15, 1.0, 1e30, 1e-20), (1e12, 1e20, 1.0, 1e10)):
+        s = make(rng, 5, H, y="f32", residual="f32", normed="f32", gate=gate, wt="f32")
+        s["y"] *= y_amp / 2
+        s["post_weight"] *= w_amp
+        s["gate"] *= g_amp
+        s["residual"] *= w_amp * g_amp * scale
+        if w_amp * g_amp * scale > 1e15:                         # squares of the sum leave f32 by definition
+            s["normed"] = s["pre_weight"] = None
+        check(s, scale=scale, eps=1e-30)
+    s = make(rng, 5, H, y="f32", residual="f32", normed="f32", gate=gate, post=False)
+    s["y"] *= 1e12
+    s["gate"] *= 1e30                                            # without a norm scale * gate comes first
+    check(s, scale=1e-30)
