@@ -205,12 +205,15 @@ struct StepKeys {
 
 // What the rows of a block of trees see: of the tokens before the new ones those from lo[row] on, of the
 // new ones those of bits[row][..].
+template <bool TREE>
 struct TreeRows {
   const uint32_t* bits;
   const int* lo;
   int start;                                   // place of the first new token
 };
-__device__ __forceinline__ bool tree_sees(const TreeRows& t, int row, int j) {
+template <>
+struct TreeRows<false> {};
+__device__ __forceinline__ bool tree_sees(const TreeRows<true>& t, int row, int j) {
   const int c = j - t.start;
   if (c < 0) return j >= t.lo[row];
   return c < 32 * kMaxTreeWords && (t.bits[row * kMaxTreeWords + (c >> 5)] >> (c & 31) & 1) != 0;
@@ -221,7 +224,7 @@ __device__ __forceinline__ bool tree_sees(const TreeRows& t, int row, int j) {
 template <class S, bool masked, bool TREE>
 __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepKeys<S::kHalves>& k,
                                           const char* st, const char* s_q, int lane, int j0, int len,
-                                          int window, const TreeRows& tree) {
+                                          int window, const TreeRows<TREE>& tree) {
   constexpr int D = S::D, NT = S::NT, H = S::kHalves;
   float sc[NT][H][4];
 #pragma unroll
@@ -275,9 +278,9 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
         sc[nt][h][x] = fmaf(sc[nt][h][x], k.f[h] * t.rowf[nt][y], k.v[h] - base[y]);
         if (masked) {
           const int j = j0 + h * 16 + (x >> 1) * 8 + f.tau, pl = t.place[nt][y];
-          const bool see = k.good[h] && j < len &&
-                           (TREE ? tree_sees(tree, 8 * nt + 2 * (lane & 3) + y, j)
-                                 : j <= pl && (window == 0 || j > pl - window));
+          bool see;
+          if constexpr (TREE) see = k.good[h] && j < len && tree_sees(tree, 8 * nt + 2 * (lane & 3) + y, j);
+          else see = k.good[h] && j <= pl && j < len && (window == 0 || j > pl - window);
           if (!see) sc[nt][h][x] = -INFINITY;
         }
         top[nt][y] = fmaxf(top[nt][y], sc[nt][h][x]);
@@ -373,7 +376,7 @@ __device__ __forceinline__ void take_step(Rows<S>& t, const Frag& f, const StepK
 // instead of bits 75.0).
 template <class S, bool TREE>
 __device__ __noinline__ void keep_nan_out(char* st, int lane, bool there, int j0, int window, const int* places,
-                                          uint32_t* bits, volatile int* any, TreeRows tree) {
+                                          uint32_t* bits, volatile int* any, TreeRows<TREE> tree) {
   constexpr int D = S::D, kWords = D / 32, kChunks = S::kPlaneB / 16 / 32;
   const int sub = D == 256 ? lane >> 4 : 0, tok = D == 256 ? lane & 15 : lane;
   char* row = st + S::kPlaneB + sub * (S::kStep * 128) + tok * S::kRowB;
@@ -400,10 +403,12 @@ __device__ __noinline__ void keep_nan_out(char* st, int lane, bool there, int j0
     const uint32_t four = (m >> 7 & 1) | (m >> 14 & 2) | (m >> 21 & 4) | (m >> 28 & 8);
     const int d = sub * 128 + ((i / 4) ^ swz) * 16 + (i % 4) * 4;
 #pragma unroll 1
-    for (int r = 0; there && r < S::kRows; ++r)
-      if (TREE ? tree_sees(tree, r, j0 + tok)
-               : j0 + tok <= places[r] && (window == 0 || j0 + tok > places[r] - window))
-        atomicOr(bits + r * kWords + d / 32, four << (d % 32));
+    for (int r = 0; there && r < S::kRows; ++r) {
+      bool see;
+      if constexpr (TREE) see = tree_sees(tree, r, j0 + tok);
+      else see = j0 + tok <= places[r] && (window == 0 || j0 + tok > places[r] - window);
+      if (see) atomicOr(bits + r * kWords + d / 32, four << (d % 32));
+    }
   }
   // plain writes to the ring's memory come before the next copies into it
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -527,7 +532,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     const long long seg_at = first + (long long)seg * length;
     const int st0 = max(0, (int)(pos - seg_at) - kSegmentCost);
     const int upto = (int)min((long long)length, end - seg_at);
-    const int st1 = min(upto - kSegmentCost, q.steps);
+    int st1 = upto - kSegmentCost;
+    if constexpr (TREE) st1 = min(st1, q.steps);               // (not the steps that make a segment up to whole pieces)
     pos = seg_at + upto;
     if (st1 <= st0) continue;                  // only the segment's fixed cost fell to this CTA
     const int head = seg / q.blocks, block = seg % q.blocks;
@@ -714,7 +720,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
       }
     }
 
-    const TreeRows tree = {s_bits, s_lo, q.start};
+    TreeRows<TREE> tree;
+    if constexpr (TREE) tree = {s_bits, s_lo, q.start};
     bool ok = true;
     for (int i = 0; i < count; ++i) {
       // every lane looks at the barrier itself; the bounded wait is for copies not there yet
@@ -850,7 +857,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant_
     }
     if (!(opens && closes)) {
       // the last piece of the segment to arrive joins all of them
-      const int c0 = (int)((seg_at + kSegmentCost) / per), c1 = (int)((seg_at + q.steps + kSegmentCost - 1) / per);
+      const int c0 = (int)((seg_at + kSegmentCost) / per);
+      const int c1 = (int)((seg_at + (TREE ? q.steps + kSegmentCost : length) - 1) / per);
       const int np = c1 - c0 + 1;
       __syncthreads();                         // the whole CTA's rows, then one thread's release
       if (tid == 0) {
