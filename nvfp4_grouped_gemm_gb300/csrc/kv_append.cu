@@ -123,7 +123,7 @@ __device__ Item find_item(const KvAppendArgs& a, int it) {
       rows = new_rows(a.b, b, a.T);
       const int n = rows.y - rows.x, len = a.b.seq_lens[b];
       start = len - n;
-      if (start < 0) {
+      if (len < n) {                           // (not by start, which may wrap)
         // more new tokens than the sequence is long: the first ones have no place
         if (n > 0) atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
         start = 0;

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constan
   const int P = a.c.page_size, log_p = 31 - __clz(P), D = a.c.head_dim, heads = a.c.kv_heads;
   const int n = max(a.b.q_offsets[b + 1] - a.b.q_offsets[b], 0), len = a.b.seq_lens[b];
   const int start = len - n, asked = min(max(a.n_keep[b], 0), a.width);
-  if (start < 0 || len > (int64_t)a.b.max_pages * P) {
+  if (len < n || len > (int64_t)a.b.max_pages * P) {         // (not by start, which may wrap)
     if (h == 0 && tid == 0) {
       atomicOr(a.err, (uint32_t)MOE_DEVERR_PAGE);
       a.new_lens[b] = len;

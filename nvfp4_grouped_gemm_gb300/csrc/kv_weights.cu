@@ -59,7 +59,7 @@ __device__ __forceinline__ Seq read_seq(const WeightsArgs& a, int b, uint32_t* e
   q.len = a.b.seq_lens[b];
   q.start = q.len - q.n;
   const int cap = a.b.max_pages * a.c.page_size;
-  if (q.n > 0 && (q.start < 0 || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+  if (q.n > 0 && (q.len < q.n || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
   q.tiles = q.n > 0 ? (q.len + kTile - 1) / kTile : 0;
   return q;

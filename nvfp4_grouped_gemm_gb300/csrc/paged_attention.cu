@@ -142,7 +142,7 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
   q.len = a.b.seq_lens[b];
   q.start = q.len - q.n;
   const int cap = a.b.max_pages * a.c.page_size;
-  if (q.n > 0 && (q.start < 0 || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+  if (q.n > 0 && (q.len < q.n || q.len > cap) && err) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
   const int lo = a.window > 0 ? max(0, min(q.start - a.window + (TREE ? 0 : 1), q.len)) : 0;
   q.step0 = lo / S::kStep;

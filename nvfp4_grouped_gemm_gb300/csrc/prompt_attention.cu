@@ -127,7 +127,7 @@ __device__ __forceinline__ Seq read_seq(const AttentionArgs& a, int b, int group
   q.per_head = 0;
   if (q.n * group < min_rows || q.n == 0) return q;        // the other form's, or nothing to do
   const int cap = a.b.max_pages * a.c.page_size, lane = threadIdx.x & 31;
-  if ((q.start < 0 || q.len > cap) && err && lane == 0) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
+  if ((q.len < q.n || q.len > cap) && err && lane == 0) atomicOr(err, (uint32_t)MOE_DEVERR_PAGE);
   q.len = min(max(q.len, 0), cap);
   q.blocks = (q.n * group + kBlock - 1) / kBlock;
   for (int i = lane; i < q.blocks; i += 32) q.per_head += block_line<TREE>(q, i, group, a.window);

@@ -192,3 +192,17 @@ def test_nan_stays_in_its_own_code():
     (256, 11, False, "bf16", [(0, 7101)])])
 def test_many_tokens_with_odd_numbers_of_query_heads(D, qh, inter, dtype, pairs):
     assert check(np.random.default_rng(12), pairs, 128, 1, qh, D, D, inter, dtype) == 0
+
+
+@pytest.mark.parametrize("length", [0, -1, -(1 << 31), 3 - (1 << 31)])
+def test_lengths_below_the_new_tokens_leave_pages_alone(length):
+    rng = np.random.default_rng(23)
+    cache = moe.PagedKvCache.allocate(4, 1, 16, 64)
+    k = activations(rng, (6, 1, 64), "bf16").cuda()
+    b = moe.SeqBatch(torch.tensor([0, 6], dtype=torch.int32).cuda(), torch.tensor([length], dtype=torch.int32).cuda(),
+                     torch.tensor([[1, 2]], dtype=torch.int32).cuda())
+    ws = zeros_ws(moe.kv_append_workspace_bytes())
+    moe.moe_kv_append_rope_e4m3(cache, b, k, k, None, None, ws)
+    assert moe.get_device_error(ws) == moe.DEVERR_PAGE
+    assert not cache.k_codes.any() and not cache.v_codes.any()
+    assert torch.all(cache.k_scales == 1) and torch.all(cache.v_scales == 1)

@@ -317,3 +317,14 @@ def test_pages_copied_from_scales_of_zero(page, D, heads):
     assert moe.get_device_error(ws) == 0
     assert np.all(planes[1][dst[0]] == 0) and np.all(planes[3][dst[0]] == 0)
     same_planes(cache, planes)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), 8 - (1 << 31), (1 << 31) - 1])
+def test_keep_with_lengths_of_any_value(length):
+    """Lengths below the number of new tokens, also where their difference leaves 32 bits, and above the table."""
+    rng = np.random.default_rng(30)
+
+    def edit(b):
+        b.lens[1] = length
+    lens = keep(rng, [(30, 9), (30, 9), (5, 40)], [[1, 4, 8], [0, 4, 8], [3, 39]], 16, 2, 64, edit=edit, err=moe.DEVERR_PAGE)
+    assert lens.tolist() == [33, length, 7]

@@ -194,3 +194,13 @@ def test_every_page_out_of_range_is_reported(page, pairs):
         b.table[0, 2] = page
     check(rng, pairs, 16, 2, 2, 128, "bf16", edit=edit, err=moe.DEVERR_PAGE)
     check(rng, pairs, 64, 1, 3, 64, "f16", edit=lambda b: b.table.__setitem__((0, 0), page), err=moe.DEVERR_PAGE)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), 3 - (1 << 31)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_lengths_below_the_new_tokens(length, window):
+    rng = np.random.default_rng(22)
+
+    def edit(b):
+        b.lens[1] = length
+    check(rng, [(100, 6), (30, 6), (7, 2)], 16, 2, 3, 64, "bf16", window=window, edit=edit, err=moe.DEVERR_PAGE)

@@ -468,3 +468,14 @@ def test_nan_keys_reach_only_the_rows_that_see_them(D, page, heads, group, dtype
     tol = eo + rel * (np.abs(want) + eo) + floor
     assert np.all(np.abs(got - want)[~nan] <= tol[~nan])
     assert np.all(np.abs(gl - wl)[~nan] <= el[~nan] + 1e-6)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), 3 - (1 << 31)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_lengths_below_the_new_tokens(length, window):
+    rng = np.random.default_rng(77)
+
+    def edit(b):
+        b.lens[1] = length
+    for group in (2, 20):
+        check(rng, [(100, 6), (30, 6), (7, 2)], 16, 2, group, 64, "bf16", window=window, edit=edit, err=moe.DEVERR_PAGE)

@@ -189,3 +189,14 @@ def test_a_graph_with_another_tree():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), 3 - (1 << 31)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_lengths_below_the_new_tokens(length, window):
+    rng = np.random.default_rng(37)
+
+    def edit(b):
+        b.lens[1] = length
+    for group in (2, 20):
+        check(rng, [(100, 6), (30, 6), (7, 2)], 16, 2, group, 64, "bf16", window=window, edit=edit, err=moe.DEVERR_PAGE)
