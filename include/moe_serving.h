@@ -206,8 +206,8 @@ size_t moe_kv_keep_workspace_bytes(void);
  * rescaled by old / new and rounded again to nearest even, in all slots of such a page. A token
  * from or into a page out of range stays (MOE_DEVERR_PAGE). No two sequences may have a page in
  * common that holds new tokens. A sequence without a valid start keeps its length.
- *   keep i32 [B][width] (may be NULL if width is 0; width at most 2^30)  n_keep i32 [B]  new_lens i32 [B], none of
- *   the arrays that are read (the batch's seq_lens, n_keep) */
+ *   keep i32 [B][width] (may be NULL if width is 0; width at most 2^30)  n_keep i32 [B]  new_lens i32 [B], on no
+ *   part of an array that is read (the batch's, keep, n_keep; refused) */
 moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch,
                             const int32_t* keep, const int32_t* n_keep, int32_t width,
                             int32_t* new_lens, void* ws, size_t ws_bytes, void* stream);
@@ -222,7 +222,8 @@ size_t moe_kv_weights_workspace_bytes(int32_t T, int32_t q_heads, int32_t kv_hea
  * moe_attention_paged_e4m3 (causal, window), whose lse is given here; a row with lse -inf adds
  * nothing. decay 0 does not read w. Sequences without new tokens, and slots past a sequence's
  * end, are left alone; two sequences with new tokens must not have a page in common. A NaN key code makes the weights of its token NaN if a row sees it.
- *   w, w_out  f32 [num_pages][kv_heads][page_size], the slots of the cache, 16-byte aligned; may be the same
+ *   w, w_out  f32 [num_pages][kv_heads][page_size], the slots of the cache, 16-byte aligned; may be the
+ *             same, but w_out on no other part of w, nor on q or lse (refused)
  *   lse       f32 [T][q_heads]                       decay within [0, 1]
  * Products are as in the attention (f16 operands, f32 sums); each token's sum is made in one order,
  * so two calls give the same bits. Tokens in pages out of range are left out (MOE_DEVERR_PAGE). */
@@ -247,8 +248,10 @@ size_t moe_kv_evict_workspace_bytes(int32_t B, int32_t kv_heads);
  * token are left as they were. budgets i32 [B], or NULL for `width` everywhere; a sequence with a
  * negative budget is left alone (new_lens its length, kept -1). Old pages are only read, and may
  * be in use by other sequences; the pages of dst_table in use must be in nobody else's.
- *   w f32 [num_pages][kv_heads][page_size]   kept i32 [B][kv_heads][width]   new_lens i32 [B], none
- *   of the arrays that are read (the batch's seq_lens, budgets)   dst_table i32 [B][dst_stride] with at least ceil(width / page_size) columns
+ *   w f32 [num_pages][kv_heads][page_size]   kept i32 [B][kv_heads][width]   new_lens i32 [B]
+ *   dst_table i32 [B][dst_stride] with at least ceil(width / page_size) columns
+ * w, kept and new_lens lie on no part of one another, of the batch's seq_lens and page_table, of
+ * budgets or of dst_table (refused).
  * Tokens from or into pages out of range are not copied (MOE_DEVERR_PAGE). The batch's q_offsets are
  * not read. */
 moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch, float* w,

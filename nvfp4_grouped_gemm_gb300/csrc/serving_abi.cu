@@ -45,6 +45,23 @@ moe_status check_batch(const moe_seq_batch* b) {
   return MOE_OK;
 }
 
+// A call's arrays as addresses: whether one that is written lies upon another that is read or written.
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
+}
+Span table_span(const int32_t* table, int64_t rows, int64_t stride, int64_t cols) {
+  return {table, ((rows - 1) * stride + cols) * 4};
+}
+// Rows `stride` elements apart.
+Span rows_span(const void* p, int64_t rows, int64_t stride, int64_t row, int64_t size) {
+  return {p, ((rows - 1) * stride + row) * size};
+}
+
 bool act_dtype(int dt) { return dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_F16; }
 
 // What both forms of the attention call take.
@@ -191,6 +208,11 @@ moe_status moe_kv_keep_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batc
     return MOE_ERR_INVALID_ARG;
   if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30) || width > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, moe_kv_keep_workspace_bytes())) != MOE_OK) return st;
+  const Span lens = {new_lens, (int64_t)batch->B * 4};
+  for (const Span& in : {Span{batch->seq_lens, (int64_t)batch->B * 4}, Span{batch->q_offsets, ((int64_t)batch->B + 1) * 4},
+                         table_span(batch->page_table, batch->B, batch->table_stride, batch->max_pages),
+                         Span{n_keep, (int64_t)batch->B * 4}, Span{keep, (int64_t)batch->B * width * 4}})
+    if (overlap(lens, in)) return MOE_ERR_INVALID_ARG;
   KeepArgs a = {};
   a.c = *cache;
   a.b = *batch;
@@ -226,6 +248,11 @@ moe_status moe_kv_weights_e4m3(const void* q, int64_t q_stride, int32_t T, int32
   if ((int64_t)batch->max_pages * cache->page_size > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, kv_weights_ws_bytes(T, q_heads, cache->kv_heads, cache->head_dim))) != MOE_OK)
     return st;
+  // the new weights on the old ones slot by slot or not at all, and on nothing that is read beside
+  const int64_t plane = (int64_t)cache->num_pages * cache->kv_heads * cache->page_size * 4;
+  if ((w != w_out && overlap({w, plane}, {w_out, plane})) || overlap({w_out, plane}, {lse, (int64_t)T * q_heads * 4}) ||
+      overlap({w_out, plane}, rows_span(q, T, q_stride, (int64_t)q_heads * cache->head_dim, 2)))
+    return MOE_ERR_INVALID_ARG;
   WeightsArgs a = {};
   a.c = *cache;
   a.b = *batch;
@@ -267,6 +294,15 @@ moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* bat
   if (dst_stride < pages) return MOE_ERR_INVALID_ARG;
   if (pages * batch->B * cache->kv_heads >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(ws, ws_bytes, moe_kv_evict_workspace_bytes(batch->B, cache->kv_heads))) != MOE_OK) return st;
+  // blocks read the batch, the budgets and the tables (and the second kernel the lists) while others write
+  const Span lens = {new_lens, (int64_t)batch->B * 4}, lists = {kept, (int64_t)batch->B * cache->kv_heads * width * 4};
+  const Span plane = {w, (int64_t)cache->num_pages * cache->kv_heads * cache->page_size * 4};
+  for (const Span& out : {lens, lists, plane})
+    for (const Span& in : {Span{batch->seq_lens, (int64_t)batch->B * 4}, Span{budgets, (int64_t)batch->B * 4},
+                           table_span(batch->page_table, batch->B, batch->table_stride, batch->max_pages),
+                           table_span(dst_table, batch->B, dst_stride, pages)})
+      if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
+  if (overlap(lens, lists) || overlap(lens, plane) || overlap(lists, plane)) return MOE_ERR_INVALID_ARG;
   EvictArgs a = {};
   a.c = *cache;
   a.b = *batch;

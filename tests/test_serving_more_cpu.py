@@ -225,3 +225,56 @@ def test_the_binding_refuses_host_tensors(lib, monkeypatch):
         moe.moe_residual_norm(x, x, x)
     with pytest.raises(ValueError):
         moe.moe_residual_norm(None, torch.zeros(64), torch.zeros(64))
+
+
+# Addresses that lie apart by far (nothing is launched: there is no device, or the call is refused).
+_FAR = [0x10000000 * i for i in range(1, 12)]
+
+
+def _far_batch(**kw):
+    b = dict(q_offsets=_FAR[0], seq_lens=_FAR[1], page_table=_FAR[2])
+    b.update(kw)
+    return _batch(**b)
+
+
+@pytest.mark.parametrize("shift", [0, 4])
+@pytest.mark.parametrize("on", ["seq_lens", "q_offsets", "page_table", "n", "keep"])
+def test_keep_refuses_new_lengths_upon_what_it_reads(lib, on, shift):
+    """Also where only a part of them lies there."""
+    at = {"seq_lens": _FAR[1], "q_offsets": _FAR[0], "page_table": _FAR[2], "n": _FAR[3], "keep": _FAR[4]}
+    kw = dict(n=_FAR[3], keep=_FAR[4], ws=_FAR[5])
+    for lens in (at[on] + shift, at[on] - 4):
+        assert _keep(lib, batch=_far_batch(), lens=lens, **kw) == 1
+
+
+@pytest.mark.parametrize("on", ["seq_lens", "budgets", "page_table", "dst", "other", "w"])
+@pytest.mark.parametrize("out", ["kept", "lens", "w"])
+def test_evict_refuses_outputs_upon_what_it_reads_or_writes(lib, out, on):
+    a = dict(w=_FAR[3], dst=_FAR[4], budgets=_FAR[5], kept=_FAR[6], lens=_FAR[7], ws=_FAR[8])
+    at = dict(seq_lens=_FAR[1], page_table=_FAR[2], budgets=a["budgets"], dst=a["dst"], w=a["w"],
+              other=a["lens" if out == "kept" else "kept"])[on]
+    if out == on:
+        return
+    for shift in (0, 4, -4):
+        assert _evict(lib, batch=_far_batch(), **{**a, out: at + shift}) == 1
+    assert _evict(lib, batch=_far_batch(), **{**a, "nb": 0}) == 3          # (the others are no reason to refuse)
+
+
+@pytest.mark.parametrize("kw", [dict(out=_FAR[3] + 64), dict(out=_FAR[3] - 16), dict(out=_FAR[4]), dict(out=_FAR[5]),
+                                dict(out=_FAR[5] + 4 * 1024 * 2 - 16)])
+def test_weights_refuses_new_weights_upon_a_part_of_what_it_reads(lib, kw):
+    a = dict(w=_FAR[3], out=_FAR[6], lse=_FAR[4], q=_FAR[5], ws=_FAR[8])
+    assert _weights(lib, batch=_far_batch(), **{**a, **kw}) == 1
+    assert _weights(lib, batch=_far_batch(), **{**a, **kw, "nb": 0}) == 3
+
+
+def test_the_first_and_last_bytes_of_neighbours_may_touch(lib):
+    """Arrays one behind the other are not refused: without a device such a call gets as far as the launch."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch")
+    one = dict(n=_FAR[3], keep=_FAR[4], ws=_FAR[5], lens=_FAR[1] + 8)      # B = 2: right behind seq_lens
+    assert _keep(lib, batch=_far_batch(), **one) == 4
+    a = dict(w=_FAR[3], out=_FAR[3] + 4 * 4 * 2 * 16, lse=_FAR[4], q=_FAR[5], ws=_FAR[8])
+    assert _weights(lib, batch=_far_batch(), **a) == 4
+    b = dict(w=_FAR[3], dst=_FAR[4], budgets=_FAR[1] + 8, kept=_FAR[6], lens=_FAR[1] + 16, ws=_FAR[8])
+    assert _evict(lib, batch=_far_batch(), **b) == 4
