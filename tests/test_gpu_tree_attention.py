@@ -200,3 +200,43 @@ def test_lengths_below_the_new_tokens(length, window):
         b.lens[1] = length
     for group in (2, 20):
         check(rng, [(100, 6), (30, 6), (7, 2)], 16, 2, group, 64, "bf16", window=window, edit=edit, err=moe.DEVERR_PAGE)
+
+
+def used_slots(batch):
+    used = np.zeros((batch.num_pages, batch.page), bool)
+    for b, n in enumerate(batch.lens):
+        for i in range(int(n)):
+            used[batch.table[b, i // batch.page], i % batch.page] = True
+    return used
+
+
+@pytest.mark.parametrize("D,group,pairs", [(128, 4, [(700, 40), (90, 3)]), (64, 8, [(2500, 17), (10, 60)]), (256, 2, [(400, 30)])])
+def test_repeated_calls_repeat_bit_for_bit(D, group, pairs):
+    """The same bits from every call: with a used and with a new workspace, in a graph, over other stale slots."""
+    rng = np.random.default_rng(38)
+    batch = Batch(rng, pairs, 16)
+    planes = cache_planes(rng, batch.num_pages, 2, 16, D)
+    mask = mask_of([tree_bits(rng, n) for _, n in pairs], 2)
+    q = activations(rng, (batch.T, 2 * group, D), "f16").cuda()
+    for cols in (0, 1 << 16):                                    # few rows alone, and both forms
+        batch.table = np.pad(batch.table, ((0, 0), (0, cols)), constant_values=-7)
+        dev, ws = batch.device(), zeros_ws(moe.attention_workspace_bytes(2 * group, 2, D))
+        want = None
+        for i in range(6):
+            other = [p.copy() for p in planes]
+            for c in (other[0], other[2]):
+                c.transpose(0, 2, 1, 3)[~used_slots(batch)] = rng.integers(0, 256)
+            cache, out = device_cache(other), torch.empty_like(q)
+            lse = torch.empty(q.shape[:2], device="cuda")
+            space = ws if i % 2 else torch.zeros_like(ws)
+            call = lambda: moe.moe_attention_tree_e4m3(q, cache, dev, mask, out, space, lse=lse)   # noqa: B023, E731
+            if i < 4:
+                call()
+            else:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    call()
+                graph.replay()
+            torch.cuda.synchronize()
+            want = (out, lse) if want is None else want
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

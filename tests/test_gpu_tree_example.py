@@ -150,3 +150,55 @@ def test_a_step_on_another_stream():
 
     for a, b in zip(step(None), step(torch.cuda.Stream())):
         assert torch.equal(a, b)
+
+
+def test_operators_wait_for_their_stream():
+    """Work queued on a stream puts the inputs into place, behind long work: operators that are called on that
+    stream, while another is the current one, see them, and would see the inputs' old values anywhere else."""
+    rng = np.random.default_rng(43)
+    batch, heads, page, D = Batch(rng, [(200, 12), (37, 5), (0, 9)], 16), 2, 16, 64
+    planes = cache_planes(rng, batch.num_pages + 30, heads, page, D)
+    wrong = cache_planes(rng, batch.num_pages + 30, heads, page, D)
+    q = activations(rng, (batch.T, heads * 2, D), "bf16").cuda()
+    other_q = activations(rng, (batch.T, heads * 2, D), "bf16").cuda()
+    mask = torch.tensor([[(2 << i) - 1] for _, n in batch.pairs for i in range(n)], dtype=torch.int32).cuda()
+    keep = torch.tensor([[0, 2, 5], [1, 2, 4], [0, 3, 8]], dtype=torch.int32).cuda()
+    new_table = torch.arange(batch.num_pages, batch.num_pages + 30, dtype=torch.int32).view(3, 10).cuda()
+    w = torch.from_numpy(rng.random((batch.num_pages + 30, heads, page), np.float32)).cuda()
+    size = max(moe.attention_workspace_bytes(heads * 2, heads, D), moe.kv_keep_workspace_bytes(),
+               moe.kv_weights_workspace_bytes(batch.T, heads * 2, heads, D), moe.kv_evict_workspace_bytes(3, heads))
+
+    def step(stream):
+        right, cache, dev = device_cache(planes), device_cache(wrong), batch.device()
+        x, weights, list_ = other_q.clone(), torch.zeros_like(w), torch.zeros_like(keep)
+        pairs = [(x, q), (weights, w), (list_, keep), (cache.k_codes, right.k_codes), (cache.v_codes, right.v_codes),
+                 (cache.k_scales, right.k_scales), (cache.v_scales, right.v_scales)]
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        normed, bits = torch.empty_like(q.flatten(1)), torch.ones_like(mask)
+        lens, cut, three = (torch.full((3,), 3, dtype=torch.int32, device="cuda") for _ in range(3))
+        kept = torch.empty(3, heads, 40, dtype=torch.int32, device="cuda")
+        spaces = [zeros_ws(size) for _ in range(4)]
+        busy = torch.ones(8192, 8192, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for _ in range(4 if stream is not None else 0):
+                busy = busy @ busy * 2.0 ** -13
+            for to, src in pairs + [(bits, mask)]:
+                to.copy_(src)
+        moe.moe_attention_tree_e4m3(x, cache, dev, bits, out, spaces[0], lse=lse, stream=stream)
+        moe.moe_kv_weights_e4m3(x, lse, cache, dev, weights, spaces[1], decay=0.5, stream=stream)
+        moe.moe_residual_norm(out.flatten(1), x.flatten(1), normed=normed, stream=stream)
+        moe.moe_kv_keep_e4m3(cache, dev, list_, three, lens, spaces[2], stream=stream)
+        after = moe.SeqBatch(dev.q_offsets, lens, dev.page_table)
+        moe.moe_kv_evict_e4m3(cache, after, weights, new_table, kept, cut, spaces[3], first=2, recent=7, stream=stream)
+        queued = stream is None or not stream.query()            # all of it was called while the stream was busy
+        torch.cuda.synchronize()
+        assert all(moe.get_device_error(ws) == 0 for ws in spaces)
+        return queued, [out, lse, normed, weights, lens, kept, cut, cache.k_codes, cache.v_codes, cache.k_scales,
+                        cache.v_scales]
+
+    _, want = step(None)
+    queued, got = step(torch.cuda.Stream())
+    assert queued
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
