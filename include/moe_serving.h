@@ -185,7 +185,9 @@ moe_status moe_verify_draft(const int32_t* draft_ids, const int32_t* n_draft, in
  *   tree_mask  u32 [T][tree_words], rows tree_stride words apart; 1 <= tree_words <= 8
  * The rest is as above, and so is the workspace (moe_attention_workspace_bytes). Positions for the
  * rotation are the caller's: moe_kv_append_rope_e4m3 takes them (a node's is the number of tokens
- * before the new ones plus its depth). */
+ * before the new ones plus its depth). Which kernels run is settled by the sizes that the host has,
+ * max_pages among them: a table much wider than the longest sequence (or than the window) can cost a
+ * small batch of trees several microseconds. */
 moe_status moe_attention_tree_e4m3(const void* q, int64_t q_stride, int32_t T, int32_t q_heads,
                                    int32_t dtype, const moe_kv_cache* cache,
                                    const moe_seq_batch* batch, const uint32_t* tree_mask,
@@ -221,7 +223,9 @@ size_t moe_kv_weights_workspace_bytes(int32_t T, int32_t q_heads, int32_t kv_hea
  * over the rows r (new tokens, times the query heads of h) that see j as in
  * moe_attention_paged_e4m3 (causal, window), whose lse is given here; a row with lse -inf adds
  * nothing. decay 0 does not read w. Sequences without new tokens, and slots past a sequence's
- * end, are left alone; two sequences with new tokens must not have a page in common. A NaN key code makes the weights of its token NaN if a row sees it.
+ * end, are left alone; two sequences with new tokens must not have a page in common, not even one
+ * that holds a common beginning (both would write its weights; nothing can refuse it). A NaN key code
+ * makes the weights of its token NaN if a row sees it.
  *   w, w_out  f32 [num_pages][kv_heads][page_size], the slots of the cache, 16-byte aligned; may be the
  *             same, but w_out on no other part of w, nor on q or lse (refused)
  *   lse       f32 [T][q_heads]                       decay within [0, 1]
@@ -253,7 +257,8 @@ size_t moe_kv_evict_workspace_bytes(int32_t B, int32_t kv_heads);
  * w, kept and new_lens lie on no part of one another, of the batch's seq_lens and page_table, of
  * budgets or of dst_table (refused).
  * Tokens from or into pages out of range are not copied (MOE_DEVERR_PAGE). The batch's q_offsets are
- * not read. */
+ * not read. How many blocks choose a sequence's tokens is settled by max_pages and B: a table much
+ * wider than the longest sequence takes more blocks than it needs. */
 moe_status moe_kv_evict_e4m3(const moe_kv_cache* cache, const moe_seq_batch* batch, float* w,
                              const int32_t* dst_table, int32_t dst_stride, const int32_t* budgets,
                              int32_t width, int32_t first, int32_t recent, int32_t* kept,

@@ -15,9 +15,9 @@
 // adds up over distributed shared memory), then lists the kept places by ballots in order: ties at the
 // threshold go to the lower places. copy_kernel has a CTA per 256 places of the copy; all reads are from
 // pages that nobody writes, so pages are independent of one another. 32 sequences of 2500 to 16000 cut to
-// 4096, 8 key heads of 128: 92.8 us, of which select takes about 29 (instructions) and the copy
+// 4096, 8 key heads of 128: 93.0 us, of which select takes about 29 (instructions) and the copy
 // 64 (6.3 TB/s, 0.92 of the copy rate); with one CTA per threshold and one per page of the copy 157.6. One
-// sequence of 1090 cut to 1024: 12.8 us, two kernels of dependent steps. The copy starts its loads when select has
+// sequence of 1090 cut to 1024: 12.9 us, two kernels of dependent steps. The copy starts its loads when select has
 // ended: let go at select's start, its CTAs take the places of select's (117 where both took 95.5).
 #include "serving.cuh"
 

@@ -18,10 +18,12 @@
 // block take the piece's tiles again and add to what the block before left.
 //
 // With one new token per sequence the bytes bound it: 64 sequences of 100 to 16000 tokens, 32 query and
-// 8 key heads of 128: 48.6 us, 4.6 TB/s (0.68 of the copy rate); one sequence of 32767, 64 query heads:
+// 8 key heads of 128: 48.4 us, 4.6 TB/s (0.68 of the copy rate); one sequence of 32767, 64 query heads:
 // 13.6 us, of which 7.5 are fixed (a sequence of 1000 takes them). With many rows it is the groups' chain:
-// 6 prompts of 1000 to 16001 tokens judged by 32 tokens, 40 query and 8 key heads of 64 (160 rows): 27.2
-// us, 26.5 with the exponentials taken out. Measured against this, in its state of then: mma.sync with keys
+// 6 prompts of 1000 to 16001 tokens judged by 32 tokens, 40 query and 8 key heads of 64 (160 rows): 27.0
+// us, 26.5 with the exponentials taken out (when it took 27.4). Heads of 256 have blocks of 32 rows and
+// spill 56 / 72 bytes: 32 sequences of 100 to 8000, 16 query and 4 key heads, 19.5 us (floor 9.4), the
+// prompts with such heads (128 rows) 36.6 (5.8). Measured against this, in its state of then: mma.sync with keys
 // and rows in registers 69 us where the 64 sequences took 59; products, widening and sums as roles of
 // their own 55 where they took 49; rows in blocks of 128 at heads of 64 30.3 (a tile is widened twice),
 // the next columns of S asked for before these are used 33.8, two products of 32 columns in flight 30.1

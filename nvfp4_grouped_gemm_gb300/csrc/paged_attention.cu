@@ -30,8 +30,12 @@
 // For trees of drafted tokens (moe_attention_tree_e4m3) the same kernel asks a row's bits instead of
 // its place in the steps that hold new tokens or a window's edge; the bits, cut to what the window
 // leaves, lie in shared memory. One tree of 8 nodes after 1000 tokens, 16 query and 4 key
-// heads of 128: 15.9 us; 32 of 6 to 48 nodes after 500 to 12000, 32 and 8 heads: 165 us, 115 of them here
-// (the sequences below 73 rows) and the rest in the other form.
+// heads of 128: 16.1 us; 32 of 6 to 48 nodes after 500 to 12000, 32 and 8 heads: 165 us, 115 of them here
+// (the sequences below 73 rows) and the rest in the other form. Heads of 256 have no other form: 16 trees of
+// 48 nodes after 4000, 16 and 4 heads, 274 us in passes of 16 rows, 32 of 4 nodes 65.5. Of the instances for
+// trees the one of three row tiles at heads of 64 spills most (120 / 224 bytes; causal 44 / 60).
+// The causal instances compute and pass nothing of this: with a tree's rows as an argument that they do not
+// use the one-token forms spilled, and 64 sequences took 76.5 us where they take 75.7.
 //
 // Keys past a row's place, outside the window, in unused slots or in pages out of range get
 // weight 0. V's bytes that are nobody's are replaced by 0 (they may be NaN codes). NaN codes of

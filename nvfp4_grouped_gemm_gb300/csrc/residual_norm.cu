@@ -3,8 +3,8 @@
 // Row statistics are sums of squares in f32: a CTA takes a row, each thread holds eight neighbouring
 // values of y and of the residual in registers, and the two sums meet through shuffles and shared
 // memory. y, the residual and the gate are read once and the outputs written once; the weights stay
-// in registers over all rows of a CTA. A CTA takes every grid-th row, and the next row's values are
-// asked for as soon as a row's are used up, before its sums meet and its stores.
+// in registers (or shared memory, below) over all rows of a CTA. A CTA takes every grid-th row, and the
+// next row's values are asked for as soon as a row's are used up, before its sums meet and its stores.
 //
 // A CTA has as many threads as the row has vectors of eight (H = 2560: 320), up to 1024; rows beyond
 // 8192 values take two or four vectors per thread (without registers for weights and the next row),
@@ -21,10 +21,12 @@
 // product stays in range, with the definition's order behind it as a call, 43.9 where this takes 31.6.
 //
 // Bound by bytes for many rows. 4096 x 4096, y f32, residual and outputs bf16, a gate per row:
-// 31.6 us, 5.3 TB/s (0.78 of the copy rate); one row of 2560: 2.8 us in a graph, which is the launch
-// and one chain of loads and two sums. Measured against this at 4096 x 4096: rows ahead in shared
-// memory (cp.async) instead of in registers 36.6 us (one) and 36.7 us (two); rows and their gates read
-// only when they are taken 38.9; 40 registers per thread and half again as many threads 44.6.
+// 31.6 us, 5.3 TB/s (0.78 of the copy rate); one row of 2560 without a post weight: 2.9 us in a graph,
+// which is the launch and one chain of loads and a sum. Rows beyond 8192 values spill (y, the residual
+// and the sums of two or four vectors): 1000 x 16384 49.4 us, 500 x 32768 71, floor 24.2 each. Measured
+// against this at 4096 x 4096: rows ahead in shared memory (cp.async) instead of in registers 36.6 us
+// (one) and 36.7 us (two); rows and their gates read only when they are taken 38.9; 40 registers per
+// thread and half again as many threads 44.6.
 #include <type_traits>
 
 #include "serving.cuh"

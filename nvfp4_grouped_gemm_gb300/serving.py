@@ -296,7 +296,8 @@ def moe_kv_weights_e4m3(q: torch.Tensor, lse: torch.Tensor, cache: PagedKvCache,
                         stream=None) -> None:
     """weights float32 [num_pages, kv_heads, page_size] of the batch's tokens times decay (0 for new
     tokens) plus what the rows q [T, q_heads, head_dim], whose lse [T, q_heads] the attention left,
-    give each of them; into out (weights itself when None). scale, window as in the attention."""
+    give each of them; into out (weights itself when None). scale, window as in the attention. No two
+    sequences with new tokens may share a page, a common beginning's included."""
     dev = _device()
     if cache.dev != dev or batch.dev != dev:
         raise _elsewhere("cache and batch")
